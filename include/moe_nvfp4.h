@@ -141,7 +141,9 @@ typedef struct {
                           MOE_FLAG_STATIC_ACT_SCALES) */
 } moe_config;
 
-typedef enum { MOE_DTYPE_BF16 = 1 } moe_dtype;
+/* Expert weights are bf16; the operators around the layer (moe_route_select,
+ * moe_block_norm) take any of the three. */
+typedef enum { MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_F32 = 3 } moe_dtype;
 
 /* Shape of an expert weight tensor as the caller holds it: a contiguous,
  * row-major [dims[0], dims[1], dims[2]] array of dtype on device `device`. */
@@ -387,6 +389,148 @@ MOE_API moe_status moe_debug_convert(const float* in, uint8_t* e2m1, uint8_t* e4
 MOE_API moe_status moe_debug_block_scaled_gemm(const uint8_t* a_codes, const uint8_t* a_sf,
                                        const uint8_t* b_codes, const uint8_t* b_sf,
                                        float* d, int M, int N, int K, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the layer.  They need no handle, allocate nothing, keep
+ * nothing between calls and launch on `stream` of the current device, which
+ * must be an sm_103a device (else MOE_ERR_UNSUPPORTED).  Row strides are in
+ * elements and at least the row's length; rows need no alignment beyond
+ * their element's (aligned rows whose length is a multiple of 8, for the
+ * routing of 4, take wider loads).  Zero tokens are a no-op.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+/* The choice of top_k of num_experts experts from logits l:
+ *   s_e = softmax over all experts of l, or sigmoid(l_e);
+ *   v_e = s_e + bias_e with a balance bias or with MOE_GROUP_TOP2 groups,
+ *         else l_e (which orders as s_e does);
+ *   groups: the experts form num_groups runs of equal length, and only those
+ *         of the top_groups best groups may be chosen.  A group scores its
+ *         largest v, or the sum of its two largest;
+ *   ids:  the top_k largest v, ties to the lower expert id (between groups
+ *         to the lower group);
+ *   w_k = scale * s / (sum of the chosen s + 1e-20) with renormalize, else
+ *         scale * s.  The bias moves the choice only, never a weight.
+ * An expert is closed to a token if its logit is -inf (or its v is -inf or
+ * NaN).  Closed experts, and those outside the chosen groups, rank below all
+ * others, in id order; where a token has fewer than top_k open experts they
+ * fill its last slots, with weight 0, so ids are always distinct and valid.
+ * A token with a NaN logit (with softmax also one with a +inf logit) has no
+ * defined weights: its ids are 0 .. top_k-1 and its weights NaN.
+ * Scores and sums are FP32; two v closer than about 4e-7 may order either way
+ * unless they come from equal logits and equal biases.
+ * Limits: num_experts <= 512, top_k <= 32, num_groups <= 32 and a divisor of
+ * num_experts, top_k <= the experts of top_groups groups. */
+typedef struct {
+  int num_experts;
+  int top_k;
+  int score;        /* moe_score */
+  int num_groups;   /* 1: no groups */
+  int top_groups;   /* groups a token may choose from */
+  int group_score;  /* moe_group_score */
+  int renormalize;
+  float scale;      /* factor on the weights; finite and not 0 */
+} moe_route_config;
+
+/* logits: [num_tokens, num_experts] of moe_dtype `dtype`, rows logits_stride
+ * elements apart; bias: FP32 [num_experts] or NULL; topk_ids: int32
+ * [num_tokens, top_k] and topk_w: FP32 [num_tokens, top_k], contiguous,
+ * slots in descending order of v. */
+MOE_API moe_status moe_route_select(const moe_route_config* cfg, const void* logits, int dtype, int64_t logits_stride,
+                                    const float* bias, int64_t num_tokens, int32_t* topk_ids, float* topk_w,
+                                    void* stream);
+
+/* Gradient of the weights with respect to the logits, the choice held fixed
+ * (the bias gets none).  logits, topk_ids and topk_w are moe_route_select's
+ * input and outputs, dweights FP32 [num_tokens, top_k]; dlogits gets every
+ * element of [num_tokens, num_experts] in the logits' type.  A slot of weight
+ * 0, or whose id is outside [0, num_experts), passes no gradient; a token's
+ * ids must be distinct.  dlogits may be logits itself (same stride). */
+MOE_API moe_status moe_route_select_backward(const moe_route_config* cfg, const void* logits, int dtype,
+                                             int64_t logits_stride, const int32_t* topk_ids, const float* topk_w,
+                                             const float* dweights, int64_t num_tokens, void* dlogits,
+                                             int64_t dlogits_stride, void* stream);
+
+/* Makes the forwards of a handle choose experts by cfg and bias (FP32 [E] on
+ * the handle's device, or NULL) instead of the default rule (softmax over the
+ * logits, renormalised); cfg = NULL returns to the default.  num_experts and
+ * top_k must be the handle's.  The bias is copied on `stream` into a buffer
+ * of the handle, the same every time: a captured forward replays with a bias
+ * set later, but keeps the rule (and whether there is a bias) it was captured
+ * with.  moe_forward_ex's gate_bias is still added to the logits first. */
+MOE_API moe_status moe_set_routing(moe_handle* h, const moe_route_config* cfg, const float* bias, void* stream);
+
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
+
+/* The norms before and after a block, with its gate and residual:
+ *   n(x; w) = x / sqrt(mean(x^2) + eps) * (weight_offset + w)     (RMS), or
+ *             the same of x - mean(x)                             (LAYER);
+ *   u  = n(y; post_weight) with `post`, else y        (the block's output)
+ *   r' = r + branch_scale * g * u                     (the residual stream)
+ *   h  = n(r'; pre_weight) with `pre`                 (the next block's input)
+ * h is formed from r' before r' is rounded to its type.  g is 1, or `gate`:
+ * one value a channel [H], a token [rows], or an element [rows, H], passed
+ * through a sigmoid first with gate_sigmoid.  A NULL weight counts as
+ * w = 1 - weight_offset (no weight).  Without y (`branch` 0) r' = r, nothing
+ * is written for it and h is a plain pre-norm; then post and gate are off.
+ * y, gate and h are of `dtype`, the residual of that type or FP32, the
+ * weights of that type or FP32.  Statistics, sums and the weights' gradients
+ * are FP32.  hidden <= 16384. */
+typedef struct {
+  int hidden;
+  int kind;            /* moe_norm_kind */
+  int branch, post, pre;
+  int gate;            /* moe_gate_kind */
+  int gate_sigmoid;
+  int dtype, residual_dtype, weight_dtype; /* moe_dtype */
+  float eps;           /* > 0 */
+  float weight_offset;
+  float branch_scale;
+} moe_norm_config;
+
+/* Operands of one call; strides are row strides in elements (gate_stride:
+ * the row stride of a full gate, ignored otherwise). */
+typedef struct {
+  const void *y, *residual, *gate, *post_weight, *pre_weight;
+  void *residual_out, *h;
+  int64_t y_stride, residual_stride, gate_stride, residual_out_stride, h_stride;
+} moe_norm_io;
+
+/* rows tokens.  residual_out may be residual itself, and h may be y itself
+ * (same stride and type); any other overlap of an output with another operand
+ * is MOE_ERR_ALIAS. */
+MOE_API moe_status moe_block_norm(const moe_norm_config* cfg, const moe_norm_io* io, int64_t rows, void* stream);
+
+/* Operands of the gradient.  Read: residual_out (r' as stored), y, gate and
+ * weights as in the forward call, dresidual_out (gradient of r' from beyond;
+ * NULL = zero) and dh (with `pre`).  Written: dresidual, dy, dgate (shaped as
+ * the gate, a full gate's rows dgate_stride apart; of `dtype`, but FP32 for
+ * a channel gate) and FP32 dpost_weight, dpre_weight [H].
+ * dpost_weight, dpre_weight and dgate may be NULL.  Without `branch`,
+ * residual_out is r, dy is not written, and dresidual = dresidual_out + the
+ * pre-norm's part. */
+typedef struct {
+  const void *dresidual_out, *dh, *residual_out, *y, *gate, *post_weight, *pre_weight;
+  void *dresidual, *dy, *dgate;
+  float *dpost_weight, *dpre_weight;
+  void* workspace;     /* moe_block_norm_workspace_bytes(cfg, rows), 16-byte aligned */
+  int64_t dresidual_out_stride, dh_stride, residual_out_stride, y_stride, gate_stride;
+  int64_t dresidual_stride, dy_stride, dgate_stride;
+} moe_norm_grad_io;
+
+/* Device bytes moe_block_norm_backward needs for its column sums; 0 for a
+ * refused cfg.  Never more than 152 * 2 rows of 3 * hidden floats. */
+MOE_API size_t moe_block_norm_workspace_bytes(const moe_norm_config* cfg, int64_t rows);
+
+/* The statistics are those of the stored residual_out.  dresidual may be
+ * dresidual_out and dy may be dh or y (same stride and type); other overlaps
+ * are MOE_ERR_ALIAS.  Column sums run in an order fixed by rows and hidden:
+ * results repeat bit for bit. */
+MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const moe_norm_grad_io* io, int64_t rows,
+                                           void* stream);
 
 #ifdef __cplusplus
 }

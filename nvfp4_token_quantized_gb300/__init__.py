@@ -29,3 +29,4 @@ from .binding import (  # noqa: F401
     moe_route_noalloc,
     moe_set_static_scales,
 )
+from .operators import BlockNorm, ExpertRouter  # noqa: F401

@@ -30,6 +30,12 @@ MOE_FLAG_STATIC_ACT_SCALES = 2
 MOE_FLAG_SHARED_AVERAGE = 4
 MOE_FLAG_ACCURATE_SIGMOID = 8
 MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F16 = 2
+MOE_DTYPE_F32 = 3
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 
 EXPORTED = (
     "moe_create", "moe_destroy", "moe_load_weights", "moe_refresh_scales_inplace", "moe_forward",
@@ -38,7 +44,8 @@ EXPORTED = (
     "moe_debug_act_quant", "moe_debug_weight_quant", "moe_debug_intermediate", "moe_debug_buffer_ptrs",
     "moe_debug_convert", "moe_debug_block_scaled_gemm", "moe_set_stage_timing", "moe_get_stage_times",
     "moe_stage_name", "moe_route_noalloc", "moe_set_static_scales", "moe_load_shared_weights",
-    "moe_debug_shared", "moe_debug_shared_act_quant",
+    "moe_debug_shared", "moe_debug_shared_act_quant", "moe_route_select", "moe_route_select_backward",
+    "moe_set_routing", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
 )
 MOE_ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 MOE_NUM_STAGES = 7
@@ -52,6 +59,35 @@ class moe_config(ctypes.Structure):
 
 class moe_weight_desc(ctypes.Structure):
     _fields_ = [("dims", ctypes.c_int64 * 3), ("dtype", ctypes.c_int), ("device", ctypes.c_int)]
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int),
+                ("num_groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("group_score", ctypes.c_int),
+                ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("kind", ctypes.c_int), ("branch", ctypes.c_int), ("post", ctypes.c_int),
+                ("pre", ctypes.c_int), ("gate", ctypes.c_int), ("gate_sigmoid", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("branch_scale", ctypes.c_float)]
+
+
+class moe_norm_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("y", "residual", "gate", "post_weight", "pre_weight", "residual_out",
+                                                "h")]
+                + [(n, ctypes.c_int64) for n in ("y_stride", "residual_stride", "gate_stride", "residual_out_stride",
+                                                 "h_stride")])
+
+
+class moe_norm_grad_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dresidual_out", "dh", "residual_out", "y", "gate", "post_weight",
+                                                "pre_weight", "dresidual", "dy", "dgate", "dpost_weight",
+                                                "dpre_weight", "workspace")]
+                + [(n, ctypes.c_int64) for n in ("dresidual_out_stride", "dh_stride", "residual_out_stride",
+                                                 "y_stride", "gate_stride", "dresidual_stride", "dy_stride",
+                                                 "dgate_stride")])
 
 
 class MoEError(RuntimeError):
@@ -107,6 +143,12 @@ def load_library() -> ctypes.CDLL:
         "moe_set_static_scales": (I, [P, P, P, P]),
         "moe_debug_shared": (I, [P, P, P, P, P, P]),
         "moe_debug_shared_act_quant": (I, [P, P, P, P, P]),
+        "moe_route_select": (I, [ctypes.POINTER(moe_route_config), P, I, L, P, L, P, P, P]),
+        "moe_route_select_backward": (I, [ctypes.POINTER(moe_route_config), P, I, L, P, P, P, L, P, L, P]),
+        "moe_set_routing": (I, [P, ctypes.POINTER(moe_route_config), P, P]),
+        "moe_block_norm": (I, [ctypes.POINTER(moe_norm_config), ctypes.POINTER(moe_norm_io), L, P]),
+        "moe_block_norm_workspace_bytes": (S, [ctypes.POINTER(moe_norm_config), L]),
+        "moe_block_norm_backward": (I, [ctypes.POINTER(moe_norm_config), ctypes.POINTER(moe_norm_grad_io), L, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -317,6 +359,16 @@ class MoE:
         return cls(shape.H, shape.I, shape.E, shape.K, max_num_tokens or shape.max_num_tokens, device,
                    shape.deterministic if deterministic is None else deterministic, static_scales,
                    accurate_sigmoid=accurate_sigmoid)
+
+    def set_routing(self, router=None, bias: Optional[torch.Tensor] = None, stream=None):
+        """Choose experts by an ``ExpertRouter`` and its balance bias (float32
+        [E]) from the next forward on; None: by the default rule."""
+        if bias is not None:
+            _check_dev(bias, torch.float32, "bias", self.device)
+            if tuple(bias.shape) != (self.E,):
+                raise ValueError(f"bias must be [{self.E}], got {tuple(bias.shape)}")
+        cfg = None if router is None else ctypes.byref(router.config)
+        _raise(self._h, load_library().moe_set_routing(self._h, cfg, _ptr(bias), _stream(stream)))
 
     def set_static_scales(self, x_gs: torch.Tensor, h_gs: torch.Tensor, stream=None):
         moe_set_static_scales(self._h, x_gs, h_gs, stream)

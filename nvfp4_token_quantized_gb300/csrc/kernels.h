@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kernels_ops.h"
+
 namespace moe {
 
 // ---- routing (kernels_route.cu) ----
@@ -106,6 +108,11 @@ struct FrontArgs {
   // the last front CTA to publish its routing derives off their path.
   int all_experts;
   int* status;                // device status word (a bounded wait that ran out)
+  // experts chosen by `rule` with route_bias [E] or nullptr (moe_set_routing)
+  // instead of the softmax top-k
+  int ruled;
+  RouteRule rule;
+  const float* route_bias;
 };
 constexpr int FRONT_SYNC_WORDS = 64;
 // Words of the front kernel's sync block used by the all-experts small-batch

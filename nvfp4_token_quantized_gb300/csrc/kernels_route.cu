@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "grouping.cuh"
 #include "kernels.h"
+#include "route_select.cuh"
 
 namespace moe {
 
@@ -576,6 +577,27 @@ __device__ __forceinline__ void quantize_token_row(const uint4* xr, int t, int H
   if (lane == 0) gs_rows[t] = gs;
 }
 
+// The choice of a handle's routing rule from a token's logits in shared
+// memory (E <= 256; 16 experts a lane cover every group count).
+template <int NE>
+__device__ __forceinline__ void front_select_n(const RouteRule& r, const float* lrow, const float* __restrict__ bias,
+                                               int lane, int& e_lane, float& w_lane) {
+  float raw[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = select_expert(r, lane, i);
+    raw[i] = e < 0 ? -INFINITY : lrow[e];
+  }
+  select_warp<NE>(
+      r, lane, raw, [&](int e) { return lrow[e]; }, [&](int e) { return bias ? __ldg(bias + e) : 0.0f; }, e_lane,
+      w_lane);
+}
+__device__ __forceinline__ void front_select(const RouteRule& r, const float* lrow, const float* __restrict__ bias,
+                                             int lane, int& e_lane, float& w_lane) {
+  if (select_per_lane(r) <= 8) front_select_n<8>(r, lrow, bias, lane, e_lane, w_lane);
+  else front_select_n<16>(r, lrow, bias, lane, e_lane, w_lane);
+}
+
 // Stages of the front kernel's router-weight ring: one round of the
 // canonical order (256 rows of H, every expert) per stage, double-buffered
 // while two stages fit; each row padded by 16 bytes.
@@ -605,7 +627,8 @@ __host__ __device__ constexpr int front_stage_bytes(int E) { return 32 * 9 * fro
 // .. + 7, all E experts) at p * 9 (2E + 16) bytes, row k of the chunk at
 // k (2E + 16) bytes within it (the padding is never read).  Lane p reads
 // chunk p, so the 8 lanes of one shared-memory wavefront hit distinct banks.
-template <int TPC, int UPW>
+// RULED: step 3 chooses by p.rule (moe_set_routing) instead.
+template <int TPC, int UPW, bool RULED>
 __global__ void __launch_bounds__(256, 1) front_small_kernel(const __grid_constant__ FrontArgs p) {
   extern __shared__ __align__(128) uint8_t front_smem[];
   __shared__ int red[ROUTER_WARPS];
@@ -794,7 +817,8 @@ __global__ void __launch_bounds__(256, 1) front_small_kernel(const __grid_consta
     if (t < T) {
       int e_lane;
       float w;
-      topk_warp<true>(slog + warp * E, E, K, lane, e_lane, w);
+      if constexpr (RULED) front_select(p.rule, slog + warp * E, p.route_bias, lane, e_lane, w);
+      else topk_warp<true>(slog + warp * E, E, K, lane, e_lane, w);
       if (lane < K) {
         p.topk_ids[(size_t)t * K + lane] = e_lane;
         p.topk_w[(size_t)t * K + lane] = w;
@@ -918,10 +942,14 @@ template <int TPC, int UPW>
 cudaError_t raise_front_attr(int H, int E) {
   const int bytes = front_smem_bytes(H, E, TPC);
   if (bytes > 227 * 1024) return cudaErrorInvalidValue;  // hidden sizes beyond 16384 at 128 experts
-  cudaFuncAttributes a{};
-  cudaError_t e = cudaFuncGetAttributes(&a, front_small_kernel<TPC, UPW>);
-  if (e != cudaSuccess || a.maxDynamicSharedSizeBytes >= bytes) return e;
-  return cudaFuncSetAttribute(front_small_kernel<TPC, UPW>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (auto kernel : {front_small_kernel<TPC, UPW, false>, front_small_kernel<TPC, UPW, true>}) {
+    cudaFuncAttributes a{};
+    cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess && a.maxDynamicSharedSizeBytes < bytes)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // Tokens per CTA: one up to 32 tokens, two above (at most 32 CTAs at 64
@@ -948,7 +976,7 @@ cudaError_t with_front(int T, int E, F&& f) {
 template <int TPC, int UPW>
 cudaError_t launch_front_t(const FrontArgs& a, cudaStream_t s) {
   // first kernel of a forward: ordinary stream order
-  return launch_k(front_small_kernel<TPC, UPW>, dim3((a.T + TPC - 1) / TPC), dim3(256),
+  return launch_k(a.ruled ? front_small_kernel<TPC, UPW, true> : front_small_kernel<TPC, UPW, false>, dim3((a.T + TPC - 1) / TPC), dim3(256),
                   (size_t)front_smem_bytes(a.H, a.E, TPC), s, false, a);
 }
 

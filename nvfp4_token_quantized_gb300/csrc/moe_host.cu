@@ -70,6 +70,10 @@ struct moe_handle {
   int s_clusters[2] = {0, 0};
   cudaStream_t side = nullptr;
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
+  // moe_set_routing: the rule of the choice of experts and its balance bias [E]
+  bool ruled = false, rule_bias = false;
+  RouteRule rule{};
+  float* route_bias = nullptr;
   float* static_x_gs = nullptr;    // static contract: the w13 input's calibrated scale [1]
   float* static_h_gs = nullptr;    // static contract: the w2 input's calibrated scale per expert [E]
   float* hbuf = nullptr;           // small batches: FP32 SwiGLU rows [E*128][Ipad]
@@ -380,12 +384,19 @@ moe_status forward_impl(moe_handle* h, const void* x, const void* gate_w, const 
       fa.static_gs = h->static_scales ? h->static_x_gs : nullptr;
       fa.all_experts = all_experts;
       fa.status = h->status_dev;
+      fa.ruled = h->ruled;
+      fa.rule = h->rule;
+      fa.route_bias = h->rule_bias ? h->route_bias : nullptr;
       CK(h, launch_front_small(fa, s));
       for (int i = 1; i <= 4; ++i) CK(h, mark(h, i, s));
     } else {
       CK(h, launch_router_logits(x, gate_w, bias, h->logits, T, H, E, s));
       CK(h, mark(h, 1, s));
-      CK(h, launch_topk(h->logits, T, E, K, h->topk_ids, h->topk_w, s));
+      if (h->ruled)
+        CK(h, launch_select(h->rule, h->logits, MOE_DTYPE_F32, E, h->rule_bias ? h->route_bias : nullptr, T,
+                            h->topk_ids, h->topk_w, true, s));
+      else
+        CK(h, launch_topk(h->logits, T, E, K, h->topk_ids, h->topk_w, s));
       CK(h, mark(h, 2, s));
       PermuteOut po{h->expert_offsets, h->src_of_row, h->row_of_src, h->pad_row_of_src,
                     h->src_of_padrow,  h->tiles,      h->num_tiles};
@@ -583,6 +594,7 @@ moe_status moe_create(const moe_config* cfg, moe_handle** out) {
   A(h->num_tiles, sizeof(int32_t) * 4);
   A(h->front_sync, sizeof(uint32_t) * FRONT_SYNC_WORDS);
   A(h->expert_done, sizeof(uint32_t) * 256);
+  A(h->route_bias, sizeof(float) * E);
   if (Is > 0) {
     h->Is = Is;
     h->Ipad_s = (Is + 255) / 256 * 256;
@@ -677,6 +689,38 @@ moe_status moe_set_static_scales(moe_handle* h, const float* x_gs, const float* 
   CK(h, cudaMemcpyAsync(h->static_x_gs, x_gs, sizeof(float), cudaMemcpyDeviceToDevice, s));
   CK(h, cudaMemcpyAsync(h->static_h_gs, h_gs, sizeof(float) * h->E, cudaMemcpyDeviceToDevice, s));
   h->static_set = true;
+  return MOE_OK;
+}
+
+moe_status moe_set_routing(moe_handle* h, const moe_route_config* cfg, const float* bias, void* stream) {
+  if (!h) return MOE_ERR_INVALID_ARG;
+  if (!cfg) {
+    h->ruled = h->rule_bias = false;
+    return MOE_OK;
+  }
+  if (cfg->num_experts != h->E || cfg->top_k != h->K) {
+    set_err(h, "moe_set_routing: top-%d of %d experts on a handle of top-%d of %d", cfg->top_k, cfg->num_experts,
+            h->K, h->E);
+    return MOE_ERR_INVALID_ARG;
+  }
+  RouteRule rule;
+  const moe_status st = make_route_rule(cfg, bias != nullptr, &rule);
+  if (st != MOE_OK) {
+    set_err(h, "moe_set_routing: groups, scores or scale outside the supported set");
+    return st;
+  }
+  DeviceGuard dg(h->cfg.device);
+  if (bias) {
+    if (device_of(bias) != h->cfg.device) {
+      set_err(h, "moe_set_routing: the bias is not on device %d", h->cfg.device);
+      return MOE_ERR_INVALID_ARG;
+    }
+    CK(h, cudaMemcpyAsync(h->route_bias, bias, sizeof(float) * h->E, cudaMemcpyDeviceToDevice,
+                          reinterpret_cast<cudaStream_t>(stream)));
+  }
+  h->rule = rule;
+  h->rule_bias = bias != nullptr;
+  h->ruled = true;
   return MOE_OK;
 }
 
