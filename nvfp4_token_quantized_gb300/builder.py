@@ -82,7 +82,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, "-shared", f"-gencode={GENCODE}", "-cudart", "static", "-o", tmp, *objs]

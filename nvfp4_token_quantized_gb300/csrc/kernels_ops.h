@@ -44,9 +44,8 @@ cudaError_t launch_select_backward(const RouteRule& r, const void* logits, int d
 // Column sums of the norms' gradient: of each weight and a channel gate.
 constexpr int NORM_SUMS = 3;
 
-// CTAs of the gradient's row loop, and how many column sums each keeps.
-int norm_backward_ctas(const moe_norm_config& c, int64_t rows);
-int norm_backward_sums(const moe_norm_config& c);
+// Bytes of the CTAs' partial column sums.
+size_t norm_backward_workspace(const moe_norm_config& c, int64_t rows);
 // vec: every row starts on 16 bytes and hidden is a multiple of 8.
 cudaError_t launch_block_norm(const moe_norm_config& c, const moe_norm_io& io, int64_t rows, bool vec,
                               cudaStream_t s);

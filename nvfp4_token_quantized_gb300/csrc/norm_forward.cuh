@@ -1,0 +1,233 @@
+// norm_forward.cuh - the norms before and after a block with its gate and
+// residual.
+//
+//   u = n(y; wp), r' = r + a g u, h = n(r'; wn),
+//   n(x; w) = (x - mean) rstd (offset + w), rstd = 1 / sqrt(mean((x - mean)^2) + eps),
+// the mean taken as 0 for the RMS kind.  Statistics come from the row's own
+// values after the mean has been taken off (never as a difference of sums),
+// in FP32.
+//
+// Bytes bound it: y, r, r' and h move once, a row stays on the SM between its
+// two sums.
+#pragma once
+
+#include "norm_common.cuh"
+
+namespace moe {
+
+namespace {
+
+// Takes the mean of a row off (LAYER) and returns 1 / sqrt(mean square + eps).
+template <int V, bool LAYER, bool VEC, int LANES, typename Sums>
+__device__ __forceinline__ float centre_and_scale(const NormShape& s, const Place<VEC, LANES>& p, Sums& sums,
+                                                  Pairs (&x)[V]) {
+  float a[1];
+  if (LAYER && s.layer) {
+    float2 t = both(0.0f);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = add2(t, x[v].p[j]);
+    a[0] = sum_pairs(t);
+    sums(a);
+    const float mean = -a[0] * s.inv_h;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[v].p[j] = add2(x[v].p[j], make_float2(p.in_row(v, 2 * j) ? mean : 0.0f,
+                                                p.in_row(v, 2 * j + 1) ? mean : 0.0f));
+  }
+  float2 q = both(0.0f);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q = fma2(x[v].p[j], x[v].p[j], q);
+  a[0] = sum_pairs(q);
+  sums(a);
+  return inv_sqrt(a[0] * s.inv_h + s.eps);
+}
+
+template <typename T, typename R, int V, bool WITH_GATE>
+struct ForwardRun {
+  using X = RingPieces<R, V, 0>;
+  using Y = RingPieces<T, V, X::END>;
+  using G = RingPieces<T, V, Y::END>;
+  static constexpr int UNITS = WITH_GATE ? G::END : Y::END;
+};
+
+// A group of s.lanes threads walks rows; each CTA holds blockDim.x / s.lanes
+// groups.  LAYER, GATE and PARTS leave the code of the centred kind, of gates
+// and of absent parts out.
+template <typename T, typename R, int V, bool VEC, int LANES, bool WIDE, bool LAYER, int GATE, int PARTS>
+__global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const NormShape s, const moe_norm_io io,
+                                                                         int64_t rows) {
+  using Run = ForwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>;
+  constexpr int STAGES = ring_stages(Run::UNITS);
+  using Sums = RowSums<WIDE>;
+  __shared__ __align__(16) float red[Sums::WORDS];
+  extern __shared__ uint4 ring[];
+  const int lanes = VEC ? s.lanes : LANES;
+  Sums sums{red, lanes};
+  sums.clear();
+  const int groups = WIDE ? 1 : blockDim.x / lanes, group = WIDE ? 0 : threadIdx.x / lanes;
+  const Place<VEC, LANES> p((int)threadIdx.x - group * lanes, lanes, s.H);
+  const bool branch = PARTS == PARTS_ALL || s.branch, post = PARTS == PARTS_ALL || s.post;
+  const bool pre = PARTS == PARTS_ALL || s.pre;
+  const bool full = (GATE & GATE_BY_ELEMENT) && (GATE != GATE_ANY || s.gate == MOE_GATE_FULL);
+  const bool channel = (GATE & GATE_BY_CHANNEL) && (GATE != GATE_ANY || s.gate == MOE_GATE_CHANNEL);
+  const bool by_element = full || channel, token = s.gate == MOE_GATE_TOKEN;
+  const T* gate = static_cast<const T*>(io.gate);
+  // The weights stay in registers while two chunks' worth fit there; wider
+  // rows read them again for each row (L1 and L2 hold them).
+  constexpr bool KEEP = V <= 2;
+  Pairs wp[KEEP ? V : 1], wn[KEEP ? V : 1];
+  const int64_t step = (int64_t)gridDim.x * groups;
+  // (the rows of a warp end together: a group past the last row idles)
+  const int64_t first = (int64_t)blockIdx.x * groups;
+  const int warp_group = WIDE ? 0 : (threadIdx.x & ~31) / lanes;
+
+  Pairs ahead_r[VEC ? 1 : V], ahead_y[VEC ? 1 : V];
+  auto run_of = [&](int stage) { return ring + stage * Run::UNITS * blockDim.x + threadIdx.x; };
+  auto fetch = [&](int64_t t, int stage) {
+    const R* r_row = static_cast<const R*>(io.residual) + t * io.residual_stride;
+    const T* y_row = static_cast<const T*>(io.y) + t * io.y_stride;
+    if constexpr (VEC) {
+      if (t < rows) {
+        uint4* run = run_of(stage);
+        Run::X::fetch(run, r_row, p);
+        if (branch) Run::Y::fetch(run, y_row, p);
+        if (full) Run::G::fetch(run, gate + t * io.gate_stride, p);
+      }
+      copies_commit();
+    } else if (t < rows) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ahead_r[v] = load_pairs<R>(r_row, v, p);
+        if (branch) ahead_y[v] = load_pairs<T>(y_row, v, p);
+      }
+    }
+  };
+  int64_t t = first + group;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * step, i);
+  } else {
+    fetch(t, 0);
+  }
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (post) wp[v] = weight_pairs<T>(s, io.post_weight, v, p);
+      if (pre) wn[v] = weight_pairs<T>(s, io.pre_weight, v, p);
+    }
+  }
+  int stage = 0;
+#pragma unroll 1
+  for (int64_t w = first + warp_group; w < rows; w += step, t += step) {
+    const bool live = WIDE || t < rows;
+    const uint4* run = run_of(stage);
+    Pairs r[V], y[V];
+    if constexpr (VEC) {
+      // into the stage of the row before this one (or, with one stage, this
+      // row's), whose values this thread has used
+      fetch(t + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copies_wait<STAGES - 1>();
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[v] = Run::X::read(run, v, p);
+      if (branch) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = Run::Y::read(run, v, p);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        r[v] = ahead_r[v];
+        y[v] = ahead_y[v];
+      }
+      fetch(t + step, 0);
+    }
+    if (branch) {
+      float scale = s.scale;
+      if (token && live) scale *= gate_value(s, to_f32(gate[t]));
+      if (post) scale *= centre_and_scale<V, LAYER>(s, p, sums, y);
+      const float2 k = both(scale);
+      R* out = static_cast<R*>(io.residual_out) + t * io.residual_out_stride;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (post) {
+          const Pairs f = KEEP ? wp[KEEP ? v : 0] : weight_pairs<T>(s, io.post_weight, v, p);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[v].p[j] = mul2(y[v].p[j], f.p[j]);
+        }
+        if (by_element && live) {
+          Pairs g;
+          if (!full) g = load_pairs<T>(gate, v, p);
+          else if constexpr (VEC) g = Run::G::read(run, v, p);
+          else g = load_pairs<T>(gate + t * io.gate_stride, v, p);
+          gate_pairs(s, g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[v].p[j] = mul2(y[v].p[j], g.p[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[v].p[j] = fma2(y[v].p[j], k, r[v].p[j]);
+        if (live) put_pairs<R>(out, v, p, r[v]);
+      }
+    }
+    if (pre) {
+      const float2 k = both(centre_and_scale<V, LAYER>(s, p, sums, r));
+      T* h = static_cast<T*>(io.h) + t * io.h_stride;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Pairs f = KEEP ? wn[KEEP ? v : 0] : weight_pairs<T>(s, io.pre_weight, v, p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(mul2(r[v].p[j], k), f.p[j]);
+        if (live) put_pairs<T>(h, v, p, r[v]);
+      }
+    }
+  }
+  if constexpr (VEC) copies_wait<0>();
+}
+
+template <typename T, typename R, int V, bool VEC, int LANES, bool WIDE, bool LAYER, int GATE, int PARTS>
+cudaError_t launch_rows(NormShape s, const moe_norm_io& io, int64_t rows, cudaStream_t stream) {
+  s.lanes = row_lanes(s.H, V, LANES);
+  const int threads = row_cta_threads(s.lanes), groups = rows_per_cta(s.lanes);
+  constexpr int UNITS = ForwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>::UNITS;
+  const int smem = VEC ? ring_stages(UNITS) * UNITS * threads * 16 : 0;
+  auto kernel = block_norm_kernel<T, R, V, VEC, LANES, WIDE, LAYER, GATE, PARTS>;
+  static std::atomic<uint64_t> raised{0};
+  static std::atomic<int> resident[17];  // CTAs an SM holds, by warps; 0: not asked yet
+  cudaError_t e = raise_shared(kernel, VEC ? RING_ROOM : 0, raised);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>& slot = resident[threads / 32];
+  int ctas = slot.load(std::memory_order_relaxed);
+  if (ctas == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    ctas = std::max(ctas, 1);
+    slot.store(ctas, std::memory_order_relaxed);
+  }
+  const int64_t need = (rows + groups - 1) / groups;
+  return launch_k(kernel, dim3((unsigned)std::min<int64_t>(need, 152 * ctas)), dim3(threads), smem, stream, false, s,
+                  io, rows);
+}
+
+}  // namespace
+
+template <typename T, typename R>
+cudaError_t launch_block_norm_t(const moe_norm_config& c, const moe_norm_io& io, int64_t rows, bool vec,
+                                cudaStream_t stream) {
+  const NormShape s = norm_shape(c);
+  return with_width(s.H, 4096, vec, [&](auto chunks, auto v, auto fixed, auto wide) {
+    constexpr int V = decltype(chunks)::value;
+    constexpr bool VEC = decltype(v)::value;
+    return with_kind<VEC, V>(s, s.post && s.pre, [&](auto layer, auto gate, auto parts) {
+      return launch_rows<T, R, V, VEC, decltype(fixed)::value, decltype(wide)::value, decltype(layer)::value,
+                         decltype(gate)::value, decltype(parts)::value>(s, io, rows, stream);
+    });
+  });
+}
+
+}  // namespace moe

@@ -260,8 +260,7 @@ moe_status moe_block_norm(const moe_norm_config* cfg, const moe_norm_io* io, int
 
 size_t moe_block_norm_workspace_bytes(const moe_norm_config* cfg, int64_t rows) {
   if (check_norm_config(cfg) != MOE_OK || rows <= 0 || rows > MAX_ROWS) return 0;
-  const int sums = norm_backward_sums(*cfg);
-  return sizeof(float) * (size_t)norm_backward_ctas(*cfg, rows) * sums * ((cfg->hidden + 7) & ~7);
+  return norm_backward_workspace(*cfg, rows);
 }
 
 moe_status moe_block_norm_backward(const moe_norm_config* cfg, const moe_norm_grad_io* io, int64_t rows,
