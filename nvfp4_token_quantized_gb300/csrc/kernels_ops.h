@@ -14,7 +14,7 @@ constexpr int SELECT_MAX_TOPK = 32;    // a slot per lane
 constexpr int SELECT_MAX_GROUPS = 32;  // at least a lane per group
 constexpr float SELECT_SUM_EPS = 1e-20f;
 
-// A validated moe_route_config.  Group g's size experts belong to the
+// A validated moe_route_config (vec is set by the launch).  Group g's size experts belong to the
 // 1 << lane_shift lanes from g << lane_shift on; with nothing to limit the
 // whole warp holds one group.
 struct RouteRule {
@@ -22,13 +22,27 @@ struct RouteRule {
   int groups, size, top_groups, lane_shift;
   int sigmoid, top2, renormalize;
   int by_score;  // the choice compares scores (plus bias), not logits
+  // 2^block_shift lanes of a chosen group form a block; the chosen groups have
+  // at least K/2 blocks, so K experts rank no lower than the lowest second
+  // best of a block.  -1: the bound is found by rounds instead.
+  int block_shift;
   float scale;
+  // A lane's experts of its group: chunks of four neighbours (rows that take
+  // loads of four logits), else every 2^lane_shift-th one.
+  int vec;
 };
+
+// Sets r.vec for rows whose groups of four logits may (or may not) be loaded
+// at once.  Chunks of four need at least one for every lane: the blocks that
+// bound the choice would be empty otherwise.
+__host__ __device__ inline void set_select_loads(RouteRule& r, bool aligned) {
+  r.vec = aligned && r.size % 4 == 0 && r.size >= 4 << r.lane_shift;
+}
 
 // Experts a lane holds, in multiples of four.
 __host__ __device__ inline int select_per_lane(const RouteRule& r) {
   const int lanes = 1 << r.lane_shift;
-  return (r.size + 4 * lanes - 1) / (4 * lanes) * 4;
+  return r.vec ? (r.size + 4 * lanes - 1) / (4 * lanes) * 4 : ((r.size + lanes - 1) / lanes + 3) / 4 * 4;
 }
 
 // MOE_OK and the rule, or why the configuration is refused (ops_host.cu).

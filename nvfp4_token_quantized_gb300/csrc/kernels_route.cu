@@ -581,21 +581,16 @@ __device__ __forceinline__ void quantize_token_row(const uint4* xr, int t, int H
 // memory (E <= 256; 16 experts a lane cover every group count).
 template <int NE>
 __device__ __forceinline__ void front_select_n(const RouteRule& r, const float* lrow, const float* __restrict__ bias,
-                                               int lane, int& e_lane, float& w_lane) {
-  float raw[NE];
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = select_expert(r, lane, i);
-    raw[i] = e < 0 ? -INFINITY : lrow[e];
-  }
-  select_warp<NE>(
-      r, lane, raw, [&](int e) { return lrow[e]; }, [&](int e) { return bias ? __ldg(bias + e) : 0.0f; }, e_lane,
-      w_lane);
+                                               int lane, SelectScratch<1>& sm, int32_t* ids, float* w) {
+  float b[NE];
+  const bool finite = load_bias<NE>(r, bias, lane, b);
+  select_rows<NE, 1, SELECT_ANY>(r, lrow, MOE_DTYPE_F32, 0, 1, bias, b, finite, lane, sm, ids, w);
 }
-__device__ __forceinline__ void front_select(const RouteRule& r, const float* lrow, const float* __restrict__ bias,
-                                             int lane, int& e_lane, float& w_lane) {
-  if (select_per_lane(r) <= 8) front_select_n<8>(r, lrow, bias, lane, e_lane, w_lane);
-  else front_select_n<16>(r, lrow, bias, lane, e_lane, w_lane);
+__device__ __forceinline__ void front_select(RouteRule r, const float* lrow, const float* __restrict__ bias,
+                                             int lane, SelectScratch<1>& sm, int32_t* ids, float* w) {
+  set_select_loads(r, true);  // (rows of 8n floats, 16-byte aligned)
+  if (select_per_lane(r) <= 8) front_select_n<8>(r, lrow, bias, lane, sm, ids, w);
+  else front_select_n<16>(r, lrow, bias, lane, sm, ids, w);
 }
 
 // Stages of the front kernel's router-weight ring: one round of the
@@ -815,14 +810,20 @@ __global__ void __launch_bounds__(256, 1) front_small_kernel(const __grid_consta
   if (warp < TPC) {
     const int t = t0 + warp;
     if (t < T) {
-      int e_lane;
-      float w;
-      if constexpr (RULED) front_select(p.rule, slog + warp * E, p.route_bias, lane, e_lane, w);
-      else topk_warp<true>(slog + warp * E, E, K, lane, e_lane, w);
-      if (lane < K) {
-        p.topk_ids[(size_t)t * K + lane] = e_lane;
-        p.topk_w[(size_t)t * K + lane] = w;
-        chosen[warp][lane] = e_lane;
+      if constexpr (RULED) {
+        __shared__ __align__(16) SelectScratch<1> scratch[TPC];
+        int32_t* ids = p.topk_ids + (size_t)t * K;
+        front_select(p.rule, slog + warp * E, p.route_bias, lane, scratch[warp], ids, p.topk_w + (size_t)t * K);
+        if (lane < K) chosen[warp][lane] = ids[lane];
+      } else {
+        int e_lane;
+        float w;
+        topk_warp<true>(slog + warp * E, E, K, lane, e_lane, w);
+        if (lane < K) {
+          p.topk_ids[(size_t)t * K + lane] = e_lane;
+          p.topk_w[(size_t)t * K + lane] = w;
+          chosen[warp][lane] = e_lane;
+        }
       }
     }
   } else if (warp >= 6 && p.out_acc) {

@@ -10,33 +10,21 @@ namespace {
 
 constexpr int SELECT_WARPS = 8;
 
-// One warp per token.
-template <typename T, int NE>
-__global__ void __launch_bounds__(32 * SELECT_WARPS) select_kernel(const RouteRule r, const T* __restrict__ logits,
-                                                                   int64_t stride, const float* __restrict__ bias,
-                                                                   int64_t rows, int32_t* __restrict__ ids,
-                                                                   float* __restrict__ w) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * SELECT_WARPS + (threadIdx.x >> 5);
+// RB rows a warp.
+template <int NE, int RB, int MODE>
+__global__ void __launch_bounds__(32 * SELECT_WARPS, NE <= 8 ? 3 : 1)
+    select_kernel(const RouteRule r, const void* __restrict__ logits, int dtype, int64_t stride,
+                  const float* __restrict__ bias, int64_t rows, int32_t* __restrict__ ids, float* __restrict__ w) {
+  __shared__ __align__(16) SelectScratch<RB> scratch[SELECT_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = ((int64_t)blockIdx.x * SELECT_WARPS + warp) * RB;
   pdl_trigger();
   pdl_wait();
   if (t >= rows) return;
-  const T* row = logits + t * stride;
-  float raw[NE];
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = select_expert(r, lane, i);
-    raw[i] = e < 0 ? -INFINITY : to_f32(row[e]);
-  }
-  int e;
-  float wj;
-  select_warp<NE>(
-      r, lane, raw, [&](int i) { return to_f32(row[i]); }, [&](int i) { return bias ? __ldg(bias + i) : 0.0f; }, e,
-      wj);
-  if (lane < r.K) {
-    ids[t * r.K + lane] = e;
-    w[t * r.K + lane] = wj;
-  }
+  float b[NE];
+  const bool finite = load_bias<NE>(r, bias, lane, b);
+  select_rows<NE, RB, MODE>(r, row_at(logits, dtype, t * stride), dtype, stride, (int)(rows - t < RB ? rows - t : RB),
+                            bias, b, finite, lane, scratch[warp], ids + t * r.K, w + t * r.K);
 }
 
 // One warp per token; lane j < K holds slot j.  Every element gets its part
@@ -95,16 +83,40 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
   if (live) drow[id] = from_f32<T>(score * (ds - mean));
 }
 
-template <typename T>
-cudaError_t select_t(const RouteRule& r, const void* logits, int64_t stride, const float* bias, int64_t rows,
-                     int32_t* ids, float* w, bool pdl, cudaStream_t s) {
-  const dim3 grid((unsigned)((rows + SELECT_WARPS - 1) / SELECT_WARPS)), block(32 * SELECT_WARPS);
-  const int n = select_per_lane(r);
-  const T* p = static_cast<const T*>(logits);
-  if (n <= 4) return launch_k(select_kernel<T, 4>, grid, block, 0, s, pdl, r, p, stride, bias, rows, ids, w);
-  if (n <= 8) return launch_k(select_kernel<T, 8>, grid, block, 0, s, pdl, r, p, stride, bias, rows, ids, w);
-  if (n <= 16) return launch_k(select_kernel<T, 16>, grid, block, 0, s, pdl, r, p, stride, bias, rows, ids, w);
-  return launch_k(select_kernel<T, 32>, grid, block, 0, s, pdl, r, p, stride, bias, rows, ids, w);
+template <int NE, int RB, int MODE>
+cudaError_t launch_select_rows(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
+                               int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
+  const int64_t per_cta = SELECT_WARPS * RB;
+  return launch_k(select_kernel<NE, RB, MODE>, dim3((unsigned)((rows + per_cta - 1) / per_cta)),
+                  dim3(32 * SELECT_WARPS), 0, s, pdl, r, logits, dtype, stride, bias, rows, ids, w);
+}
+
+// Rows a warp takes together: four (two of up to 16 experts a lane) once that
+// still leaves every scheduler a few warps, by kernels compiled for the kind of
+// rule; one below, where latency counts, by one kernel for all.
+template <int NE, int RB>
+cudaError_t select_n(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
+                     int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
+  if (RB == 1 || rows < 152 * 4 * 4 * RB)
+    return launch_select_rows<NE, 1, SELECT_ANY>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if constexpr (RB > 1) {
+    const int mode = (r.sigmoid ? SELECT_SIGMOID : 0) | (r.by_score ? SELECT_BY_SCORE : 0) |
+                     (r.top_groups < r.groups ? SELECT_LIMITED : 0);
+#define MOE_SELECT_MODE(M) \
+  case M: return launch_select_rows<NE, RB, M>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s)
+    switch (mode) {
+      MOE_SELECT_MODE(0);
+      MOE_SELECT_MODE(1);
+      MOE_SELECT_MODE(2);
+      MOE_SELECT_MODE(3);
+      MOE_SELECT_MODE(4);
+      MOE_SELECT_MODE(5);
+      MOE_SELECT_MODE(6);
+      MOE_SELECT_MODE(7);
+    }
+#undef MOE_SELECT_MODE
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>
@@ -118,11 +130,16 @@ cudaError_t select_backward_t(const RouteRule& r, const void* logits, int64_t st
 
 }  // namespace
 
-cudaError_t launch_select(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
+cudaError_t launch_select(const RouteRule& rule, const void* logits, int dtype, int64_t stride, const float* bias,
                           int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
-  if (dtype == MOE_DTYPE_F32) return select_t<float>(r, logits, stride, bias, rows, ids, w, pdl, s);
-  if (dtype == MOE_DTYPE_F16) return select_t<__half>(r, logits, stride, bias, rows, ids, w, pdl, s);
-  return select_t<__nv_bfloat16>(r, logits, stride, bias, rows, ids, w, pdl, s);
+  RouteRule r = rule;
+  const int bytes = dtype == MOE_DTYPE_F32 ? 4 : 2;
+  set_select_loads(r, stride % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (4 * bytes - 1)) == 0);
+  const int n = select_per_lane(r);
+  if (n <= 4) return select_n<4, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if (n <= 8) return select_n<8, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if (n <= 16) return select_n<16, 2>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  return select_n<32, 1>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
 }
 
 cudaError_t launch_select_backward(const RouteRule& r, const void* logits, int dtype, int64_t stride,
