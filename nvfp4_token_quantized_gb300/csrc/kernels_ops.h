@@ -22,10 +22,7 @@ struct RouteRule {
   int groups, size, top_groups, lane_shift;
   int sigmoid, top2, renormalize;
   int by_score;  // the choice compares scores (plus bias), not logits
-  // 2^block_shift lanes of a chosen group form a block; the chosen groups have
-  // at least K/2 blocks, so K experts rank no lower than the lowest second
-  // best of a block.  -1: the bound is found by rounds instead.
-  int block_shift;
+  int slot_shift;  // 2^slot_shift >= K: lanes of a row's slots
   float scale;
   // A lane's experts of its group: chunks of four neighbours (rows that take
   // loads of four logits), else every 2^lane_shift-th one.
@@ -33,8 +30,8 @@ struct RouteRule {
 };
 
 // Sets r.vec for rows whose groups of four logits may (or may not) be loaded
-// at once.  Chunks of four need at least one for every lane: the blocks that
-// bound the choice would be empty otherwise.
+// at once.  Chunks of four need at least one for every lane, or the experts
+// would crowd in a few.
 __host__ __device__ inline void set_select_loads(RouteRule& r, bool aligned) {
   r.vec = aligned && r.size % 4 == 0 && r.size >= 4 << r.lane_shift;
 }

@@ -35,10 +35,7 @@ moe_status make_route_rule(const moe_route_config* cfg, bool has_bias, RouteRule
   r.by_score = has_bias || (G > 1 && r.top2);
   r.lane_shift = 5;
   while ((r.groups << r.lane_shift) > 32) --r.lane_shift;
-  // blocks of a power of two lanes bound a choice of 2, 4 or 8 tightly; more
-  // slots take the bound by rounds
-  r.block_shift = K <= 8 ? r.lane_shift : -1;
-  while (r.block_shift >= 0 && 2 * (r.top_groups << (r.lane_shift - r.block_shift)) < K) --r.block_shift;
+  while ((1 << r.slot_shift) < K) ++r.slot_shift;
   *out = r;
   return MOE_OK;
 }

@@ -8,15 +8,17 @@
 // is instructions.  The usual row takes this path, several rows of a warp
 // together:
 //  - scores by the hardware's exponential and reciprocal;
-//  - the two best of each lane, block of lanes and group by min and max;
-//  - a bound that at least K experts reach and few more: up to 8 slots the
-//    lowest second best of the chosen groups' blocks, above the K-th of the
-//    lanes' two best, by K rounds of a maximum over the warp;
-//  - those candidates, one a lane, two rows side by side: their scores again
-//    at full accuracy (for the weights), and the rank of each among them.
-// Rows it does not cover (NaN, infinite scores or biases, fewer open experts
-// than slots, more than 32 candidates, as with many equal values) go through
-// select_by_rounds.
+//  - the two best of each lane and, with groups, of each group, by min and
+//    max;
+//  - K rounds of a maximum over the lanes' heads, each lane moving on to its
+//    second best.  If exactly K experts reach the last maximum, no two lanes
+//    tied and none held a third: the rounds are the slots;
+//  - the slots of all rows, one a lane: their scores at full accuracy, and the
+//    weights.
+// Otherwise the experts that reach the last maximum, if at most 32, are
+// ranked one a lane; and rows that this does not cover either (NaN, infinite
+// scores or biases, fewer open experts than slots, many equal values) go
+// through select_by_rounds.
 #pragma once
 
 #include "common.cuh"
@@ -169,11 +171,13 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
 
 // Scratch of one warp for RB rows.
 template <int RB>
-struct SelectScratch {
-  uint32_t key[RB][32];  // candidates: what they are compared by
-  int e[RB][32];         // and their experts
-  float out_s[RB][32];  // slots: scores
-  int out_e[RB][32];    // and experts
+struct alignas(16) SelectScratch {  // (read 16 bytes at a time)
+  int slot_e[RB][32];              // experts of the slots
+  float slot_s[32];                // a ranked row's scores
+  uint32_t key[32];                // a ranked row's candidates: what they are compared by
+  int e[32];                       // and their experts
+  uint32_t reach[RB][32];          // each lane's experts that reach a row's bound
+  float top[RB], total[RB];        // softmax: the largest logit, the sum
 };
 
 // exp(x) and 1 / (1 + exp(-x)) for the choice: relative errors of a few
@@ -271,8 +275,7 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       for (int i = 0; i < NE; ++i) v[q][i] = -INFINITY;
     }
   }
-  float top[RB], total[RB];  // softmax: the largest logit, the sum
-  float lane1[RB], block2[RB], group[RB];
+  float lane1[RB], lane2[RB], group[RB];
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
     // A finite sum means finite logits.  Otherwise some are closed (fine), or
@@ -287,25 +290,25 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       for (int i = 0; i < NE; ++i) bad |= !(v[q][i] < INFINITY);
       if (__any_sync(all, bad)) odd |= 1u << q;
     }
-    top[q] = 0.0f, total[q] = 1.0f;
+    float top = 0.0f, total = 1.0f;
     if (!sigmoid) {
       float m = v[q][0];
 #pragma unroll
       for (int i = 1; i < NE; ++i) m = fmaxf(m, v[q][i]);
       m = max_lanes(m);
-      top[q] = m == -INFINITY ? 0.0f : m;
+      top = m == -INFINITY ? 0.0f : m;
     }
     if (by_score || need_total) {
       float s[NE];
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        s[i] = sigmoid ? sigmoid_fast(v[q][i]) : exp_fast(v[q][i] - top[q]);
+        s[i] = sigmoid ? sigmoid_fast(v[q][i]) : exp_fast(v[q][i] - top);
         if (need_total) sum += s[i];
       }
       if (need_total) {
         sum = sum_lanes(sum);
-        total[q] = sum == 0.0f ? 1.0f : sum;
+        total = sum == 0.0f ? 1.0f : sum;
       }
       if (by_score) {
         if (closed) {
@@ -313,7 +316,7 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
           for (int i = 0; i < NE; ++i)
             if (v[q][i] == -INFINITY) s[i] = -INFINITY;
         }
-        const float k = sigmoid ? 1.0f : 1.0f / total[q];
+        const float k = sigmoid ? 1.0f : 1.0f / total;
 #pragma unroll
         for (int i = 0; i < NE; ++i) v[q][i] = sigmoid ? s[i] + b[i] : fmaf(s[i], k, b[i]);
       }
@@ -323,16 +326,16 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
     for (int i = 2; i < NE; i += 2)
       merge2(b1, b2, fmaxf(v[q][i], v[q][i + 1]), fminf(v[q][i], v[q][i + 1]));
     lane1[q] = b1;
-    auto merge_lanes = [&](int from, int to) {
-#pragma unroll 1
-      for (int s = from; s < to; ++s)
-        merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
-    };
-    merge_lanes(0, r.block_shift);
-    block2[q] = b2;
+    lane2[q] = b2;
     if (limited) {
-      merge_lanes(max(r.block_shift, 0), r.lane_shift);
+#pragma unroll 1
+      for (int s = 0; s < r.lane_shift; ++s)
+        merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
       group[q] = r.top2 && b2 > -INFINITY ? b1 + b2 : b1;
+    }
+    if (!sigmoid && lane == 0) {
+      sm.top[q] = top;
+      sm.total[q] = total;
     }
   }
   // Which groups each row keeps.  A group's score is in all its lanes: lane d
@@ -357,10 +360,11 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
     const int rank = rank_of(mine);
     kept = __ballot_sync(all, g < r.groups && rank < r.top_groups);
   }
-  // the candidates of each row: a bit for each of this lane's experts, and
-  // how many the lower lanes have (a byte for each row)
-  unsigned mask[RB];
-  unsigned counts = 0;
+  // K rounds for all rows at once.  pops: the rounds this lane's two best won,
+  // as k + 1 in base 64.
+  uint32_t head[RB], next[RB], low[RB];
+  unsigned pops[RB];
+  unsigned mine = 0;  // rows that keep this lane's group
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
     bool keep = g < r.groups;
@@ -372,125 +376,143 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
         keep = keep && rank < r.top_groups;
       }
     }
-    // the bound: the lowest second best of the kept blocks, or the K-th of the
-    // two best of every kept lane (-inf where there are too few)
-    uint32_t low;
-    if (r.block_shift >= 0) {
-      low = __reduce_min_sync(all, keep ? order_bits(block2[q]) : 0xffffffffu);
-    } else {
-      uint32_t head = keep ? order_bits(lane1[q]) : 0u, next = keep ? order_bits(block2[q]) : 0u;
-#pragma unroll 1
-      for (int k = 0; k < r.K; ++k) {
-        low = __reduce_max_sync(all, head);
-        if (head == low) {
-          head = next;
-          next = 0u;
-        }
-      }
-    }
-    float bound = low == 0u ? -INFINITY : __uint_as_float((low & 0x80000000u) ? (low & 0x7FFFFFFFu) : ~low);
-    bound = keep ? fmaxf(bound, -3.402823466e38f) : __int_as_float(0x7fffffff);  // (NaN: none)
-    mask[q] = 0;
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (v[q][i] >= bound) mask[q] |= 1u << i;
-    counts |= (unsigned)__popc(mask[q]) << (8 * q);
+    mine |= (unsigned)keep << q;
+    head[q] = keep ? order_bits(lane1[q]) : 0u;  // (0: below every value)
+    next[q] = keep ? order_bits(lane2[q]) : 0u;
+    pops[q] = 0;
+    low[q] = 0u;
   }
-  // (bytes hold the counts of up to 255 candidates a row)
-  unsigned upto = counts;
-  if constexpr (NE * 32 > 255) {
-    // more could carry into the next row's byte: saturate by giving rows with
-    // many up beforehand
+#pragma unroll 1
+  for (int k = 1; k <= r.K; ++k) {
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
-      const unsigned n = __reduce_add_sync(all, (unsigned)__popc(mask[q]));
-      if (n > 255) {
-        odd |= 1u << q;
-        counts &= ~(255u << (8 * q));
+      low[q] = __reduce_max_sync(all, head[q]);
+      if (head[q] == low[q]) {
+        pops[q] = pops[q] * 64 + k;
+        head[q] = next[q];
+        next[q] = 0u;
       }
     }
-    upto = counts;
   }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned t = __shfl_up_sync(all, upto, o);
-    if (lane >= o) upto += t;
-  }
-  const unsigned totals = __shfl_sync(all, upto, 31);
-  upto -= counts;
+  unsigned ranked = 0;  // rows whose candidates are to be ranked
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
-    const int n = totals >> (8 * q) & 255;
+    // (0: the heads ran out)
+    float bound = low[q] == 0u ? -INFINITY
+                               : __uint_as_float((low[q] & 0x80000000u) ? (low[q] & 0x7FFFFFFFu) : ~low[q]);
+    bound = (mine >> q & 1) ? fmaxf(bound, -3.402823466e38f) : __int_as_float(0x7fffffff);  // (NaN: none)
+    unsigned reach = 0, best = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      if (v[q][i] >= bound) reach |= 1u << i;
+      if (v[q][i] == lane1[q]) best |= 1u << i;
+    }
+    const int n = __reduce_add_sync(all, __popc(reach));
     if (n < r.K || n > 32) odd |= 1u << q;
-    if ((odd >> q & 1) || q >= valid) continue;
-    int at = upto >> (8 * q) & 255;
-    while (mask[q]) {
-      const int i = __ffs(mask[q]) - 1;
-      mask[q] &= mask[q] - 1;
-      sm.e[q][at++] = g * r.size + select_place(r, lane, i);
+    if (q >= valid || (odd >> q & 1)) continue;
+    // the last maximum an open expert's: each expert that reaches it is one of
+    // a lane's two best and won a round of its own
+    if (n == r.K && low[q] > order_bits(-INFINITY)) {
+      if (reach) {
+        // one expert, or the best first
+        const int i1 = __ffs(reach & best) - 1;
+        const unsigned rest = reach & ~(1u << i1);
+        const unsigned first = pops[q] >= 64 ? pops[q] >> 6 : pops[q];
+        sm.slot_e[q][first - 1] = g * r.size + select_place(r, lane, i1);
+        if (rest) sm.slot_e[q][(pops[q] & 63) - 1] = g * r.size + select_place(r, lane, __ffs(rest) - 1);
+      }
+    } else {
+      ranked |= 1u << q;
+      sm.reach[q][lane] = reach;
     }
   }
-  odd &= (1u << valid) - 1u;
+  const unsigned rows_here = (1u << valid) - 1u;
+  odd &= rows_here;
   __syncwarp();
-  // The candidates, one a lane: two rows side by side where both fit.
-#pragma unroll
-  for (int q0 = 0; q0 < RB; q0 += 2) {
-    constexpr int PAIR = RB > 1 ? 1 : 0;
-    if (q0 >= valid) break;
-    const int n0 = (odd >> q0 & 1) ? 0 : totals >> (8 * q0) & 255;
-    const int n1 =
-        PAIR == 0 || q0 + 1 >= valid || (odd >> (q0 + PAIR) & 1) ? 0 : totals >> (8 * (q0 + PAIR)) & 255;
-    const bool paired = PAIR == 1 && n0 <= 16 && n1 <= 16 && r.K <= 16;
-    for (int pass = 0; pass < (paired || PAIR == 0 ? 1 : 2); ++pass) {
-      const bool second = paired ? lane >= 16 : pass == 1;
-      const int q = q0 + (second ? PAIR : 0);
-      const int n = second ? n1 : n0;
-      const int c = paired ? lane & 15 : lane;
-      const int longest = paired ? max(n0, n1) : n;
-      float score = 0.0f;
-      // candidates compare as (value, lower id first)
-      uint32_t key = 0;
-      int e = 0;
-      if (c < n) {
-        e = sm.e[q][c];
-        const float l = logit_at(row_at(rows, dtype, q * stride), dtype, e);
-        float value = l;
-        if (sigmoid) score = sigmoid_ieee(l);
-        else score = expf(l - (second ? top[q0 + PAIR] : top[q0])) / (second ? total[q0 + PAIR] : total[q0]);
-        if (by_score) value = score + (bias ? __ldg(bias + e) : 0.0f);
-        key = order_bits(value);
-      }
-      sm.key[q][c] = key;
-      __syncwarp();
-      int rank = 0;
+  // the slots of the rows that the rounds settled
+  const unsigned settled = rows_here & ~odd & ~ranked;
+  const int slots = 1 << r.slot_shift, at_once = 32 >> r.slot_shift;
+  if (settled) {
 #pragma unroll 1
-      for (int j = 0; j < longest; j += 4) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&sm.key[q][j]);
-        const int4 oe = *reinterpret_cast<const int4*>(&sm.e[q][j]);
-        rank += o.x > key || (o.x == key && oe.x < e);
-        rank += o.y > key || (o.y == key && oe.y < e);
-        rank += o.z > key || (o.z == key && oe.z < e);
-        rank += o.w > key || (o.w == key && oe.w < e);
+    for (int q0 = 0; q0 < RB; q0 += at_once) {
+      const int q = q0 + (lane >> r.slot_shift), c = lane & (slots - 1);
+      const bool slot = q < RB && (settled >> q & 1) && c < r.K;
+      float s = 0.0f;
+      int e = 0;
+      if (slot) {
+        e = sm.slot_e[q][c];
+        const float l = logit_at(row_at(rows, dtype, q * stride), dtype, e);
+        s = sigmoid ? sigmoid_ieee(l) : expf(l - sm.top[q]) / sm.total[q];
       }
-      if (c < n && rank < r.K) {
-        sm.out_s[q][rank] = score;
-        sm.out_e[q][rank] = e;
-      }
-      __syncwarp();
-      const bool slot = n > 0 && c < r.K;
-      float s = slot ? sm.out_s[q][c] : 0.0f;
       if (r.renormalize) {
         float sum = s;
-        if (!paired) sum += __shfl_xor_sync(all, sum, 16);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
+#pragma unroll 1
+        for (int o = slots >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
         s = s / (sum + SELECT_SUM_EPS);
       }
       if (slot) {
-        ids[q * r.K + c] = sm.out_e[q][c];
+        ids[q * r.K + c] = e;
         w[q * r.K + c] = s * r.scale;
       }
     }
+  }
+  // rows with ties or a lane with three: the candidates, one a lane
+  while (ranked) {
+    const int q = __ffs(ranked) - 1;
+    ranked &= ranked - 1;
+    const void* row = row_at(rows, dtype, q * stride);
+    unsigned reach = sm.reach[q][lane];
+    int upto = __popc(reach);
+    int at = -upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(all, upto, o);
+      if (lane >= o) upto += t;
+    }
+    const int n = __shfl_sync(all, upto, 31);
+    at += upto;
+    while (reach) {
+      const int i = __ffs(reach) - 1;
+      reach &= reach - 1;
+      sm.e[at++] = g * r.size + select_place(r, lane, i);
+    }
+    __syncwarp();
+    // they compare as (value, lower id first)
+    float score = 0.0f;
+    uint32_t key = 0;
+    int e = 0;
+    if (lane < n) {
+      e = sm.e[lane];
+      const float l = logit_at(row, dtype, e);
+      float value = l;
+      score = sigmoid ? sigmoid_ieee(l) : expf(l - sm.top[q]) / sm.total[q];
+      if (by_score) value = score + (bias ? __ldg(bias + e) : 0.0f);
+      key = order_bits(value);
+    }
+    sm.key[lane] = key;
+    __syncwarp();
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&sm.key[j]);
+      const int4 oe = *reinterpret_cast<const int4*>(&sm.e[j]);
+      rank += o.x > key || (o.x == key && oe.x < e);
+      rank += o.y > key || (o.y == key && oe.y < e);
+      rank += o.z > key || (o.z == key && oe.z < e);
+      rank += o.w > key || (o.w == key && oe.w < e);
+    }
+    if (lane < n && rank < r.K) {
+      sm.slot_s[rank] = score;
+      sm.slot_e[q][rank] = e;
+    }
+    __syncwarp();
+    float s = lane < r.K ? sm.slot_s[lane] : 0.0f;
+    if (r.renormalize) s = s / (sum_lanes(s) + SELECT_SUM_EPS);
+    if (lane < r.K) {
+      ids[q * r.K + lane] = sm.slot_e[q][lane];
+      w[q * r.K + lane] = s * r.scale;
+    }
+    __syncwarp();
   }
   // the rows left over
   while (odd) {
