@@ -37,11 +37,11 @@ def _device(t, name: str) -> int:
     """The CUDA ordinal of t, which must be the current device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev} but the current device is cuda:{torch.cuda.current_device()}")
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev} but the current device is cuda:{_current_device()}")
     return dev
 
 
@@ -49,26 +49,25 @@ def _rows(t, dtype, rows: int, width: int, name: str, dev: int) -> int:
     """Checks a [rows, width] tensor; returns its row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.get_device() != dev:
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor on cuda:{dev}")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
-        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(shape)}")
     s0, s1 = t.stride()
     if s1 != 1 and width > 1:
         raise ValueError(f"{name}: the elements of a row must be next to each other")
-    if rows <= 1:
-        return width
-    if s0 < width:
+    if s0 >= width:
+        return s0
+    if rows > 1:
         raise ValueError(f"{name}: rows overlap (row stride {s0}, width {width})")
-    return s0
+    return width
 
 
 def _vector(t, dtype, n: int, name: str, dev: int) -> int:
-    """Checks a contiguous tensor of n elements of a vector's shape; returns its address."""
+    """Checks a contiguous tensor of n elements; returns its address."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{dev}")
     return t.data_ptr()
 
@@ -92,8 +91,11 @@ class _OnStream:
         return self._ctx.__exit__(*a)
 
 
-def _current(dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+# The current stream's handle and the current device, by torch's own cheap
+# getters where it has them (a Stream object costs more than a launch).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _ok(st: int, what: str) -> None:
@@ -117,20 +119,21 @@ class ExpertRouter:
                                        int(top_groups), _choice(_GROUP_SCORES, group_score, "group_score"),
                                        int(bool(renormalize)), float(scale))
         self._cfg = ctypes.byref(self.config)
+        self._lib = load_library()
         # (no tokens: only the configuration is looked at)
-        _ok(load_library().moe_route_select(self._cfg, None, MOE_DTYPE_F32, 0, None, 0, None, None, None),
+        _ok(self._lib.moe_route_select(self._cfg, None, MOE_DTYPE_F32, 0, None, 0, None, None, None),
             f"ExpertRouter(num_experts={num_experts}, top_k={top_k}, num_groups={num_groups}, "
             f"top_groups={top_groups}, scale={scale})")
 
-    def _logits(self, logits, name="logits"):
-        dev = _device(logits, name)
+    def _logits(self, logits):
+        dev = _device(logits, "logits")
         dt = _DTYPES.get(logits.dtype)
         if dt is None:
-            raise ValueError(f"{name} must be bfloat16, float16 or float32")
-        if logits.dim() != 2:
-            raise ValueError(f"{name} must be [num_tokens, {self.E}], got {tuple(logits.shape)}")
-        T = logits.shape[0]
-        return dev, dt, T, _rows(logits, logits.dtype, T, self.E, name, dev)
+            raise ValueError("logits must be bfloat16, float16 or float32")
+        shape = logits.shape
+        if len(shape) != 2:
+            raise ValueError(f"logits must be [num_tokens, {self.E}], got {tuple(shape)}")
+        return dev, dt, shape[0], _rows(logits, logits.dtype, shape[0], self.E, "logits", dev)
 
     def select(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
                weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -143,19 +146,24 @@ class ExpertRouter:
 
     def _select(self, logits, bias, ids, weights, stream):
         dev, dt, T, ld = self._logits(logits)
+        n = T * self.K
         b = None if bias is None else _vector(bias, torch.float32, self.E, "bias", dev)
         if ids is None:
-            ids = logits.new_empty((T, self.K), dtype=torch.int32)
-        elif tuple(ids.shape) != (T, self.K):
+            ids = torch.empty((T, self.K), dtype=torch.int32, device=logits.device)
+            pi = ids.data_ptr()
+        elif ids.shape != (T, self.K):
             raise ValueError(f"ids must be [{T}, {self.K}], got {tuple(ids.shape)}")
+        else:
+            pi = _vector(ids, torch.int32, n, "ids", dev)
         if weights is None:
-            weights = logits.new_empty((T, self.K), dtype=torch.float32)
-        elif tuple(weights.shape) != (T, self.K):
+            weights = torch.empty((T, self.K), dtype=torch.float32, device=logits.device)
+            pw = weights.data_ptr()
+        elif weights.shape != (T, self.K):
             raise ValueError(f"weights must be [{T}, {self.K}], got {tuple(weights.shape)}")
-        pi = _vector(ids, torch.int32, T * self.K, "ids", dev)
-        pw = _vector(weights, torch.float32, T * self.K, "weights", dev)
-        st = load_library().moe_route_select(self._cfg, logits.data_ptr(), dt, ld, b, T, pi, pw,
-                                             _current(dev) if stream is None else stream)
+        else:
+            pw = _vector(weights, torch.float32, n, "weights", dev)
+        st = self._lib.moe_route_select(self._cfg, logits.data_ptr(), dt, ld, b, T, pi, pw,
+                                        _current(dev) if stream is None else stream)
         if st != MOE_OK:
             raise MoEError(st, f"moe_route_select(T={T}, E={self.E}, K={self.K})")
         return ids, weights
@@ -173,9 +181,10 @@ class ExpertRouter:
         dev, dt, T, ld = self._logits(logits)
         n = T * self.K
         if dlogits is None:
-            dlogits = logits.new_empty((T, self.E))
-        ldd = _rows(dlogits, logits.dtype, T, self.E, "dlogits", dev)
-        st = load_library().moe_route_select_backward(
+            dlogits, ldd = torch.empty((T, self.E), dtype=logits.dtype, device=logits.device), self.E
+        else:
+            ldd = _rows(dlogits, logits.dtype, T, self.E, "dlogits", dev)
+        st = self._lib.moe_route_select_backward(
             self._cfg, logits.data_ptr(), dt, ld, _vector(ids, torch.int32, n, "ids", dev),
             _vector(weights, torch.float32, n, "weights", dev), _vector(dweights, torch.float32, n, "dweights", dev),
             T, dlogits.data_ptr(), ldd, _current(dev) if stream is None else stream)
@@ -202,8 +211,9 @@ class BlockNorm:
         self.post, self.pre, self.gate_sigmoid = bool(post), bool(pre), bool(gate_sigmoid)
         self.eps, self.weight_offset, self.branch_scale = float(eps), float(weight_offset), float(branch_scale)
         self._configs = {}
+        self._lib = load_library()
         # (no rows: only the configuration is looked at)
-        _ok(load_library().moe_block_norm(self._config(True, torch.float32, torch.float32, torch.float32),
+        _ok(self._lib.moe_block_norm(self._config(True, torch.float32, torch.float32, torch.float32),
                                           ctypes.byref(moe_norm_io()), 0, None),
             f"BlockNorm(hidden={hidden}, eps={eps}, weight_offset={weight_offset}, branch_scale={branch_scale})")
 
@@ -258,9 +268,10 @@ class BlockNorm:
 
     def _forward(self, residual, y, gate, post_weight, pre_weight, residual_out, h, stream):
         dev = _device(residual, "residual")
-        if residual.dim() != 2:
-            raise ValueError(f"residual must be [num_tokens, {self.H}], got {tuple(residual.shape)}")
-        T, rt = residual.shape[0], residual.dtype
+        shape = residual.shape
+        if len(shape) != 2:
+            raise ValueError(f"residual must be [num_tokens, {self.H}], got {tuple(shape)}")
+        T, rt, place = shape[0], residual.dtype, residual.device
         branch = y is not None
         dt = y.dtype if branch else rt if h is None else h.dtype
         r_ld = _rows(residual, rt, T, self.H, "residual", dev)
@@ -273,7 +284,7 @@ class BlockNorm:
             y_ld = _rows(y, dt, T, self.H, "y", dev)
             py = y.data_ptr()
             if residual_out is None:
-                residual_out = residual.new_empty((T, self.H))
+                residual_out = torch.empty((T, self.H), dtype=rt, device=place)
             else:
                 o_ld = _rows(residual_out, rt, T, self.H, "residual_out", dev)
             po = residual_out.data_ptr()
@@ -281,14 +292,14 @@ class BlockNorm:
             residual_out = None
         if self.pre:
             if h is None:
-                h = residual.new_empty((T, self.H), dtype=dt)
+                h = torch.empty((T, self.H), dtype=dt, device=place)
             else:
                 h_ld = _rows(h, dt, T, self.H, "h", dev)
             ph = h.data_ptr()
         else:
             h = None
         io = moe_norm_io(py, residual.data_ptr(), g, wp, wn, po, ph, y_ld, r_ld, g_ld, o_ld, h_ld)
-        st = load_library().moe_block_norm(cfg, ctypes.byref(io), T, _current(dev) if stream is None else stream)
+        st = self._lib.moe_block_norm(cfg, ctypes.byref(io), T, _current(dev) if stream is None else stream)
         if st != MOE_OK:
             raise MoEError(st, f"moe_block_norm(T={T}, H={self.H})")
         return residual_out, h
@@ -314,16 +325,16 @@ class BlockNorm:
     def workspace_bytes(self, rows: int, branch: bool = True) -> int:
         """Bytes of workspace the gradient of ``rows`` rows needs."""
         cfg = self._config(branch, torch.float32, torch.float32, torch.float32)
-        return int(load_library().moe_block_norm_workspace_bytes(cfg, rows))
+        return int(self._lib.moe_block_norm_workspace_bytes(cfg, rows))
 
     def _backward(self, dresidual_out, dh, residual_out, y, gate, post_weight, pre_weight, dresidual, dy, workspace,
                   stream):
-        H, lib = self.H, load_library()
+        H, lib = self.H, self._lib
         first = dh if dresidual_out is None else dresidual_out
         dev = _device(first, "the incoming gradient")
-        if first.dim() != 2:
+        if len(first.shape) != 2:
             raise ValueError(f"gradients must be [num_tokens, {H}], got {tuple(first.shape)}")
-        T, branch = first.shape[0], y is not None
+        T, branch, place = first.shape[0], y is not None, first.device
         rt = dresidual_out.dtype if residual_out is None else residual_out.dtype
         dt = y.dtype if branch else dh.dtype if dh is not None else rt
         wp, wn, wt = self._weights(branch, post_weight, pre_weight, dt, dev)
@@ -339,7 +350,7 @@ class BlockNorm:
             x_ld = _rows(residual_out, rt, T, H, "residual_out", dev)
             ph, px = dh.data_ptr(), residual_out.data_ptr()
         if dresidual is None:
-            dresidual = first.new_empty((T, H), dtype=rt)
+            dresidual = torch.empty((T, H), dtype=rt, device=place)
         else:
             dr_ld = _rows(dresidual, rt, T, H, "dresidual", dev)
         dgate = dpost = dpre = None
@@ -347,26 +358,26 @@ class BlockNorm:
             y_ld = _rows(y, dt, T, H, "y", dev)
             py = y.data_ptr()
             if dy is None:
-                dy = y.new_empty((T, H))
+                dy = torch.empty((T, H), dtype=dt, device=place)
             else:
                 dy_ld = _rows(dy, dt, T, H, "dy", dev)
             pdy = dy.data_ptr()
             if g is not None:
-                dgate = (gate.new_empty((T, H)) if self.gate == MOE_GATE_FULL else
+                dgate = (torch.empty((T, H), dtype=dt, device=place) if self.gate == MOE_GATE_FULL else
                          torch.empty_like(gate, dtype=torch.float32 if self.gate == MOE_GATE_CHANNEL else dt))
                 pdg = dgate.data_ptr()
             if wp is not None:
-                dpost = first.new_empty((H,), dtype=torch.float32)
+                dpost = torch.empty(H, dtype=torch.float32, device=place)
                 pdp = dpost.data_ptr()
         else:
             dy = None
         if wn is not None:
-            dpre = first.new_empty((H,), dtype=torch.float32)
+            dpre = torch.empty(H, dtype=torch.float32, device=place)
             pdn = dpre.data_ptr()
         need = int(lib.moe_block_norm_workspace_bytes(cfg, T))
         if need:
             if workspace is None:
-                workspace = first.new_empty((need,), dtype=torch.uint8)
+                workspace = torch.empty(need, dtype=torch.uint8, device=place)
             elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
                 raise ValueError(f"workspace must be a contiguous tensor of {need} bytes or more on cuda:{dev}")
             ws = workspace.data_ptr()
