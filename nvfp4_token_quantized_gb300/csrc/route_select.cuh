@@ -8,13 +8,16 @@
 // is instructions.  The usual row takes this path, several rows of a warp
 // together:
 //  - scores by the hardware's exponential and reciprocal;
-//  - the two best of each lane and, with groups, of each group, by min and
-//    max;
+//  - the two best of each lane (three where groups leave fewer lanes) and, with
+//    groups, the two best of each group, by min and max;
 //  - K rounds of a maximum over the lanes' heads, each lane moving on to its
-//    second best.  If exactly K experts reach the last maximum, no two lanes
-//    tied and none held a third: the rounds are the slots;
+//    next best.  If exactly K experts reach the last maximum, no two lanes
+//    tied and none held one more: the rounds are the slots;
 //  - the slots of all rows, one a lane: their scores at full accuracy, and the
 //    weights.
+// Comparisons, selections and logic take two issue slots a warp, additions and
+// fused multiply-adds one: counts, ranks and the places of a lane's best are
+// therefore sums of reaches(), not bit masks.
 // Otherwise the experts that reach the last maximum, if at most 32, are
 // ranked one a lane; and rows that this does not cover either (NaN, infinite
 // scores or biases, fewer open experts than slots, many equal values) go
@@ -193,6 +196,23 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return y;
 }
 
+// The largest over the warp.
+__device__ __forceinline__ float warp_top(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// 1 where v >= bound, else 0 (a = 1); 1 only where v > bound with a = 0; 0
+// where v - bound is NaN.  Exact unless the two differ by less than 2^-126,
+// which takes a bound below TINY: the caller sends such rows another way.
+constexpr float TINY = 7.888609e-31f;  // 2^-100
+__device__ __forceinline__ float reaches(float v, float bound, float a = 1.0f) {
+  return __saturatef(fmaf(v - bound, 8.507059173e37f, a));
+}
+// A small non-negative whole float as an integer.
+__device__ __forceinline__ int whole(float v) { return __float_as_int(v + 8388608.0f) & 0x7fffff; }
+
 // Merges the two best (b1 >= b2) of two sets.
 __device__ __forceinline__ void merge2(float& b1, float& b2, float c1, float c2) {
   b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
@@ -230,6 +250,28 @@ __device__ __forceinline__ void load_logits(const RouteRule& r, const void* row,
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       raw[i] = i * lanes + l < size ? logit_at(row, dtype, g * r.size + l + i * lanes) : -INFINITY;
+  }
+}
+
+// The two or three best (DEPTH) of NE values, each as often as it occurs, by
+// merging sorted runs: the k-th of two runs is the largest min(a_i, b_j) with
+// i + j = k, a_0 and b_0 taken as infinite.
+template <int NE, int DEPTH>
+__device__ __forceinline__ void lane_best(const float (&v)[NE], float (&b)[DEPTH]) {
+#pragma unroll
+  for (int i = 0; i < NE; i += 4) {
+    const float p1 = fmaxf(v[i], v[i + 1]), p2 = fminf(v[i], v[i + 1]);
+    const float q1 = fmaxf(v[i + 2], v[i + 3]), q2 = fminf(v[i + 2], v[i + 3]);
+    const float c1 = fmaxf(p1, q1), c2 = fmaxf(fmaxf(p2, q2), fminf(p1, q1));
+    const float c3 = DEPTH > 2 ? fmaxf(fminf(p1, q2), fminf(p2, q1)) : 0.0f;
+    if (i == 0) {
+      b[0] = c1, b[1] = c2;
+      if constexpr (DEPTH > 2) b[2] = c3;
+    } else {
+      if constexpr (DEPTH > 2) b[2] = fmaxf(fmaxf(fmaxf(b[2], c3), fminf(b[0], c2)), fminf(b[1], c1));
+      b[1] = fmaxf(fmaxf(b[1], c2), fminf(b[0], c1));
+      b[0] = fmaxf(b[0], c1);
+    }
   }
 }
 
@@ -275,7 +317,9 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       for (int i = 0; i < NE; ++i) v[q][i] = -INFINITY;
     }
   }
-  float lane1[RB], lane2[RB], group[RB];
+  // this lane's best, and its group's score
+  constexpr int DEPTH = MODE < 0 || (MODE & SELECT_LIMITED) ? 3 : 2;
+  float best[RB][DEPTH], group[RB];
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
     // A finite sum means finite logits.  Otherwise some are closed (fine), or
@@ -321,16 +365,12 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
         for (int i = 0; i < NE; ++i) v[q][i] = sigmoid ? s[i] + b[i] : fmaf(s[i], k, b[i]);
       }
     }
-    float b1 = fmaxf(v[q][0], v[q][1]), b2 = fminf(v[q][0], v[q][1]);
-#pragma unroll
-    for (int i = 2; i < NE; i += 2)
-      merge2(b1, b2, fmaxf(v[q][i], v[q][i + 1]), fminf(v[q][i], v[q][i + 1]));
-    lane1[q] = b1;
-    lane2[q] = b2;
+    lane_best<NE, DEPTH>(v[q], best[q]);
     if (limited) {
-#pragma unroll 1
-      for (int s = 0; s < r.lane_shift; ++s)
-        merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
+      float b1 = best[q][0], b2 = best[q][1];
+#pragma unroll
+      for (int s = 0; s < 5; ++s)
+        if (s < r.lane_shift) merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
       group[q] = r.top2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
     if (!sigmoid && lane == 0) {
@@ -345,24 +385,28 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
   unsigned kept = all;  // bit of lane (group's first + d): row d keeps the group
   const bool together = lanes >= RB;
   auto rank_of = [&](float mine) {
-    int rank = 0;
-#pragma unroll 1
-    for (int k = 1; k < (32 >> r.lane_shift); ++k) {
-      const float other = __shfl_xor_sync(all, mine, k << r.lane_shift);
-      rank += other > mine || (other == mine && (g ^ k) < g);
+    float rank = 0.0f;
+    const int others = 32 >> r.lane_shift;
+#pragma unroll
+    for (int k = 1; k < 32; ++k) {
+      if (k >= others) break;
+      // (an equal score at a lower index outranks; of groups without an open
+      // expert it does not matter which are kept)
+      rank += reaches(__shfl_xor_sync(all, mine, k << r.lane_shift), mine, (g ^ k) < g ? 1.0f : 0.0f);
     }
     return rank;
   };
+  const float top_groups = (float)r.top_groups;
   if (limited && together) {
     float mine = group[0];
 #pragma unroll
     for (int q = 1; q < RB; ++q) mine = (lane & (RB - 1)) == q ? group[q] : mine;
-    const int rank = rank_of(mine);
-    kept = __ballot_sync(all, g < r.groups && rank < r.top_groups);
+    const float rank = rank_of(mine);
+    kept = __ballot_sync(all, g < r.groups && rank < top_groups);
   }
-  // K rounds for all rows at once.  pops: the rounds this lane's two best won,
-  // as k + 1 in base 64.
-  uint32_t head[RB], next[RB], low[RB];
+  // K rounds for all rows at once.  pops: the rounds this lane's best won, k
+  // (from 1) as digits of base 64, the best's highest.
+  float head[RB][DEPTH], low[RB];
   unsigned pops[RB];
   unsigned mine = 0;  // rows that keep this lane's group
 #pragma unroll
@@ -372,57 +416,75 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       if (together) {
         keep = kept >> ((lane & ~(lanes - 1)) + q) & 1;
       } else {
-        const int rank = rank_of(group[q]);
-        keep = keep && rank < r.top_groups;
+        const float rank = rank_of(group[q]);
+        keep = keep && rank < top_groups;
       }
     }
     mine |= (unsigned)keep << q;
-    head[q] = keep ? order_bits(lane1[q]) : 0u;  // (0: below every value)
-    next[q] = keep ? order_bits(lane2[q]) : 0u;
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) head[q][d] = keep ? best[q][d] : -INFINITY;
     pops[q] = 0;
-    low[q] = 0u;
+    low[q] = -INFINITY;
   }
 #pragma unroll 1
   for (int k = 1; k <= r.K; ++k) {
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
-      low[q] = __reduce_max_sync(all, head[q]);
-      if (head[q] == low[q]) {
+      low[q] = warp_top(head[q][0]);
+      if (head[q][0] == low[q]) {
         pops[q] = pops[q] * 64 + k;
-        head[q] = next[q];
-        next[q] = 0u;
+#pragma unroll
+        for (int d = 0; d + 1 < DEPTH; ++d) head[q][d] = head[q][d + 1];
+        head[q][DEPTH - 1] = -INFINITY;
       }
     }
   }
   unsigned ranked = 0;  // rows whose candidates are to be ranked
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
-    // (0: the heads ran out)
-    float bound = low[q] == 0u ? -INFINITY
-                               : __uint_as_float((low[q] & 0x80000000u) ? (low[q] & 0x7FFFFFFFu) : ~low[q]);
-    bound = (mine >> q & 1) ? fmaxf(bound, -3.402823466e38f) : __int_as_float(0x7fffffff);  // (NaN: none)
-    unsigned reach = 0, best = 0;
+    // how many reach the last maximum (every open expert of the kept groups
+    // where the heads ran out), and of this lane's which are its best
+    const bool keep = mine >> q & 1;
+    const float bound = keep ? fmaxf(low[q], -3.402823466e38f) : INFINITY;
+    float n_lane = 0.0f, place1 = 0.0f, place2 = 0.0f, place3 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      if (v[q][i] >= bound) reach |= 1u << i;
-      if (v[q][i] == lane1[q]) best |= 1u << i;
+      n_lane += reaches(v[q][i], bound);
+      place1 = fmaf(reaches(v[q][i], best[q][0]), (float)i, place1);
+      place2 = fmaf(reaches(v[q][i], best[q][1]), (float)i, place2);
+      if constexpr (DEPTH > 2) place3 = fmaf(reaches(v[q][i], best[q][2]), (float)i, place3);
     }
-    const int n = __reduce_add_sync(all, __popc(reach));
+    const int n = __reduce_add_sync(all, whole(n_lane));
     if (n < r.K || n > 32) odd |= 1u << q;
+    // Settled if the last maximum is an open expert's and K experts reach it:
+    // each is one of its lane's best and won a round of its own.  Their places
+    // are the sums' differences, if no two of them are equal.
+    const bool twice = keep && ((best[q][1] >= bound && best[q][0] == best[q][1]) ||
+                                (DEPTH > 2 && best[q][DEPTH - 1] >= bound && best[q][1] == best[q][DEPTH - 1]));
+    float least = fminf(fabsf(bound), limited ? fabsf(group[q]) : INFINITY);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) least = fminf(least, fabsf(best[q][d]));
+    const bool unsafe = least < TINY;
+    bool settles = n == r.K && low[q] > -INFINITY;
+    if (__any_sync(all, twice || unsafe)) {
+      settles = false;
+      if (__any_sync(all, unsafe)) odd |= 1u << q;
+    }
     if (q >= valid || (odd >> q & 1)) continue;
-    // the last maximum an open expert's: each expert that reaches it is one of
-    // a lane's two best and won a round of its own
-    if (n == r.K && low[q] > order_bits(-INFINITY)) {
-      if (reach) {
-        // one expert, or the best first
-        const int i1 = __ffs(reach & best) - 1;
-        const unsigned rest = reach & ~(1u << i1);
-        const unsigned first = pops[q] >= 64 ? pops[q] >> 6 : pops[q];
-        sm.slot_e[q][first - 1] = g * r.size + select_place(r, lane, i1);
-        if (rest) sm.slot_e[q][(pops[q] & 63) - 1] = g * r.size + select_place(r, lane, __ffs(rest) - 1);
-      }
+    if (settles) {
+      const unsigned won = pops[q];
+      const int count = whole(n_lane);
+      auto put = [&](float place, int digit) {
+        sm.slot_e[q][(won >> 6 * digit & 63) - 1] = g * r.size + select_place(r, lane, whole(place));
+      };
+      if (count > 0) put(place1, count - 1);
+      if (count > 1) put(place2 - place1, count - 2);
+      if (DEPTH > 2 && count > 2) put(place3 - place2, 0);
     } else {
       ranked |= 1u << q;
+      unsigned reach = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) reach |= v[q][i] >= bound ? 1u << i : 0u;
       sm.reach[q][lane] = reach;
     }
   }

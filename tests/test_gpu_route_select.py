@@ -346,3 +346,39 @@ def test_refusals():
         wide = _logits(8, 65)
         r.select_backward(wide[:, :64], ids, w, w, dlogits=wide[:, 1:])
     assert e.value.status == 5
+
+
+def test_values_next_to_each_other():
+    # logits that differ in their last bit, denormal ones among them, and -0
+    base = torch.tensor([0.0, 1e-45, 3e-45, 1e-40, -1e-45, -1e-40, 1.1754944e-38, -0.0, 1.0, 1.0000001, 0.99999994, -1.0,
+                         -1.0000001, 3.4028235e38, -3.4028235e38, 1e-30], device="cuda")
+    g = torch.Generator().manual_seed(2)
+    rows = torch.stack([base[torch.randint(0, 16, (128,), generator=g).cuda()] for _ in range(3000)])
+    for K in (1, 5, 8, 20):
+        _check(3000, 128, K, logits=rows)
+        _check(3000, 128, K, logits=rows, num_groups=8, top_groups=6)
+    tiny = (torch.randint(0, 40, (3000, 64), generator=g) * 1e-45).float().cuda()
+    _check(3000, 64, 6, logits=tiny, num_groups=4, top_groups=2)
+    deep = (torch.rand(3000, 64, generator=g) * -20 - 70).cuda()        # scores down to 1e-39
+    ids, _ = _router(64, 6, score="sigmoid", num_groups=4, top_groups=2, group_score="top2").select(deep)
+    assert all(len(set(r)) == 6 for r in ids.tolist())
+
+
+@pytest.mark.parametrize("E,G,top,K", [(128, 1, 1, 8), (256, 8, 4, 8), (160, 8, 3, 6), (64, 1, 1, 16), (255, 17, 5, 9),
+                                       (512, 1, 1, 10), (512, 16, 4, 12), (97, 1, 1, 5)])
+def test_many_rows_equal_few_rows(E, G, top, K):
+    # rows taken several at a time give the bits that a row alone gives
+    T = 12001
+    for score in ("softmax", "sigmoid"):
+        for dtype in (torch.float32, torch.bfloat16):
+            r = _router(E, K, score=score, num_groups=G, top_groups=top, group_score="top2", scale=1.5)
+            l, b = _logits(T, E, dtype, closed=0.02 if G == 1 else 0.0), _bias(E)
+            for bias in (None, b):
+                ids, w = r.select(l, bias=bias)
+                for lo in (0, 5003, T - 900):
+                    i2, w2 = r.select(l[lo:lo + 900], bias=bias)
+                    assert torch.equal(ids[lo:lo + 900], i2) and torch.equal(w[lo:lo + 900], w2)
+                dw = torch.randn(T, K, device="cuda")
+                dl = r.select_backward(l, ids, w, dw)
+                d2 = r.select_backward(l[5003:5903], ids[5003:5903], w[5003:5903], dw[5003:5903])
+                assert torch.equal(dl[5003:5903], d2)
