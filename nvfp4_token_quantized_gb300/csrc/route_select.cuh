@@ -175,7 +175,7 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
 // Scratch of one warp for RB rows.
 template <int RB>
 struct alignas(16) SelectScratch {  // (read 16 bytes at a time)
-  int slot_e[RB][32];              // experts of the slots
+  int slot_e[RB][32];              // of the slots: lane << 5 | place, or a ranked row's experts
   float slot_s[32];                // a ranked row's scores
   uint32_t key[32];                // a ranked row's candidates: what they are compared by
   int e[32];                       // and their experts
@@ -365,6 +365,18 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
         for (int i = 0; i < NE; ++i) v[q][i] = sigmoid ? s[i] + b[i] : fmaf(s[i], k, b[i]);
       }
     }
+    if (!by_score && dtype != MOE_DTYPE_F32) {
+      // Equal logits are common in 16 bits.  Their FP32 values end in 13 zero
+      // bits or more: the expert's id there makes each its own, the lower id
+      // the larger value.
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const float f = v[q][i] + 0.0f;  // (-0 to +0)
+        const unsigned id = g * r.size + select_place(r, lane, i);
+        const unsigned bits = __float_as_uint(f) | (f < 0.0f ? id : id ^ 511u);
+        if (f > -INFINITY) v[q][i] = __uint_as_float(bits);
+      }
+    }
     lane_best<NE, DEPTH>(v[q], best[q]);
     if (limited) {
       float b1 = best[q][0], b2 = best[q][1];
@@ -442,25 +454,25 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
   unsigned ranked = 0;  // rows whose candidates are to be ranked
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
-    // how many reach the last maximum (every open expert of the kept groups
-    // where the heads ran out), and of this lane's which are its best
+    // How many of this lane's reach the last maximum (every open expert of the
+    // kept groups where the heads ran out), the sum of their places, and the
+    // place of its best.
     const bool keep = mine >> q & 1;
     const float bound = keep ? fmaxf(low[q], -3.402823466e38f) : INFINITY;
-    float n_lane = 0.0f, place1 = 0.0f, place2 = 0.0f, place3 = 0.0f;
+    float both_sums = 0.0f, first = 0.0f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      n_lane += reaches(v[q][i], bound);
-      place1 = fmaf(reaches(v[q][i], best[q][0]), (float)i, place1);
-      place2 = fmaf(reaches(v[q][i], best[q][1]), (float)i, place2);
-      if constexpr (DEPTH > 2) place3 = fmaf(reaches(v[q][i], best[q][2]), (float)i, place3);
+      both_sums = fmaf(reaches(v[q][i], bound), (float)(1 + 64 * i), both_sums);
+      first = fmaf(reaches(v[q][i], best[q][0]), (float)i, first);
     }
-    const int n = __reduce_add_sync(all, whole(n_lane));
+    const int count = whole(both_sums) & 63, places = whole(both_sums) >> 6;
+    const int n = __reduce_add_sync(all, count);
     if (n < r.K || n > 32) odd |= 1u << q;
     // Settled if the last maximum is an open expert's and K experts reach it:
     // each is one of its lane's best and won a round of its own.  Their places
-    // are the sums' differences, if no two of them are equal.
-    const bool twice = keep && ((best[q][1] >= bound && best[q][0] == best[q][1]) ||
-                                (DEPTH > 2 && best[q][DEPTH - 1] >= bound && best[q][1] == best[q][DEPTH - 1]));
+    // follow from the sums, if no two of a lane's are equal.
+    const bool twice = (best[q][1] >= bound && best[q][0] == best[q][1]) ||
+                       (DEPTH > 2 && best[q][DEPTH - 1] >= bound && best[q][1] == best[q][DEPTH - 1]);
     float least = fminf(fabsf(bound), limited ? fabsf(group[q]) : INFINITY);
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) least = fminf(least, fabsf(best[q][d]));
@@ -472,14 +484,19 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
     }
     if (q >= valid || (odd >> q & 1)) continue;
     if (settles) {
-      const unsigned won = pops[q];
-      const int count = whole(n_lane);
-      auto put = [&](float place, int digit) {
-        sm.slot_e[q][(won >> 6 * digit & 63) - 1] = g * r.size + select_place(r, lane, whole(place));
-      };
-      if (count > 0) put(place1, count - 1);
-      if (count > 1) put(place2 - place1, count - 2);
-      if (DEPTH > 2 && count > 2) put(place3 - place2, 0);
+      // slots hold lane and place; the best won the first of the lane's rounds
+      const int here = lane << 5, best_at = whole(first);
+      if (count > 0) sm.slot_e[q][(pops[q] >> 6 * (count - 1)) - 1] = here + best_at;
+      if (count == 2) sm.slot_e[q][(pops[q] & 63) - 1] = here + places - best_at;
+      if (DEPTH > 2 && __any_sync(all, count > 2)) {
+        float second = 0.0f;  // places of the two best
+#pragma unroll
+        for (int i = 0; i < NE; ++i) second = fmaf(reaches(v[q][i], best[q][1]), (float)i, second);
+        if (count > 2) {
+          sm.slot_e[q][(pops[q] >> 6 & 63) - 1] = here + whole(second) - best_at;
+          sm.slot_e[q][(pops[q] & 63) - 1] = here + places - whole(second);
+        }
+      }
     } else {
       ranked |= 1u << q;
       unsigned reach = 0;
@@ -502,7 +519,8 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       float s = 0.0f;
       int e = 0;
       if (slot) {
-        e = sm.slot_e[q][c];
+        const int x = sm.slot_e[q][c];  // lane and place
+        e = (x >> 5 >> r.lane_shift) * r.size + select_place(r, x >> 5, x & 31);
         const float l = logit_at(row_at(rows, dtype, q * stride), dtype, e);
         s = sigmoid ? sigmoid_ieee(l) : expf(l - sm.top[q]) / sm.total[q];
       }
