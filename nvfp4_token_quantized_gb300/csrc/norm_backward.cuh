@@ -21,8 +21,8 @@ namespace moe {
 
 namespace {
 
-// Rows come through the ring (VEC up to two chunks a thread) or from global
-// memory, where L1 serves the later passes.
+// Rows come through a ring, of pieces or of granules, up to two chunks a
+// thread; wider ones from global memory, where L1 serves the later passes.
 template <typename T, typename R, int V, bool VEC, int LANES, bool WIDE, bool LAYER, int GATE, int PARTS>
 __global__ void __launch_bounds__(512, 1)
     block_norm_backward_kernel(const NormShape s, const moe_norm_grad_io io, int64_t rows, int n_sums,
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(512, 1)
   __shared__ __align__(16) float red[Sums::WORDS];
   extern __shared__ uint4 ring[];
   constexpr bool RING = VEC && V <= 2;
+  constexpr bool LINEAR = !VEC && V <= 2;  // rows in granules
   constexpr bool KEEP = V <= 2;  // column sums and weights in registers
   using Run = BackwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>;
   constexpr int STAGES = RING ? ring_stages(Run::UNITS) : 1;
@@ -104,7 +105,25 @@ __global__ void __launch_bounds__(512, 1)
   const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups;
   const int warp_group = WIDE ? 0 : (threadIdx.x & ~31) / lanes;
   auto run_of = [&](int stage) { return ring + stage * Run::UNITS * blockDim.x + threadIdx.x; };
+  constexpr int ROWS = Run::linear(LANES);
+  const int r_bytes = linear_bytes(s.H, sizeof(R)), t_bytes = linear_bytes(s.H, sizeof(T));
+  const int linear_row = 2 * r_bytes + ((pre ? 1 : 0) + (branch ? 1 : 0) + (full ? 1 : 0)) * t_bytes;
+  const int at_dh = 2 * r_bytes, at_y = at_dh + (pre ? t_bytes : 0), at_gate = at_y + (branch ? t_bytes : 0);
+  auto region_of = [&](int stage) { return reinterpret_cast<char*>(ring) + (stage * groups + group) * linear_row; };
   auto fetch = [&](int64_t t, int stage) {
+    if constexpr (LINEAR) {
+      if (t < rows) {
+        char* region = region_of(stage);
+        if (pre) {
+          copy_granules(region, x_in + t * io.residual_out_stride, s.H, p.i, LANES);
+          copy_granules(region + at_dh, dh_in + t * io.dh_stride, s.H, p.i, LANES);
+        }
+        if (has_d) copy_granules(region + r_bytes, d_in + t * io.dresidual_out_stride, s.H, p.i, LANES);
+        if (branch) copy_granules(region + at_y, y_in + t * io.y_stride, s.H, p.i, LANES);
+        if (full) copy_granules(region + at_gate, gate + t * io.gate_stride, s.H, p.i, LANES);
+      }
+      copies_commit();
+    }
     if constexpr (RING) {
       if (t < rows) {
         uint4* run = run_of(stage);
@@ -122,6 +141,7 @@ __global__ void __launch_bounds__(512, 1)
   int64_t t = first + group;
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * step, i);
+  if constexpr (LINEAR && ROWS == 2) fetch(t, 0);
   int stage = 0;
 #pragma unroll 1
   for (int64_t w = first + warp_group; w < rows; w += step, t += step) {
@@ -132,29 +152,54 @@ __global__ void __launch_bounds__(512, 1)
       copies_wait<STAGES - 1>();
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    // a chunk of a row (of the last row where this group has none)
+    // the rows (the last one where this group has none)
     const int64_t tr = live ? t : rows - 1;
+    const R* x_row = x_in + tr * io.residual_out_stride;
+    const R* d_row = d_in + tr * io.dresidual_out_stride;
+    const T* dh_row = dh_in + tr * io.dh_stride;
+    const T* y_row = y_in + tr * io.y_stride;
+    const T* g_row = gate + tr * io.gate_stride;
+    if constexpr (LINEAR) {
+      const char* region = region_of(stage);
+      if constexpr (ROWS == 2) {
+        // this row has landed for all its threads, who have left the other stage
+        copies_wait<0>();
+        row_barrier<WIDE>();
+        fetch(t + step, stage ^ 1);
+        stage ^= 1;
+      } else {
+        row_barrier<WIDE>();
+        fetch(t, 0);
+        copies_wait<0>();
+        row_barrier<WIDE>();
+      }
+      x_row = in_granules(region, x_row);
+      d_row = in_granules(region + r_bytes, d_row);
+      dh_row = in_granules(region + at_dh, dh_row);
+      y_row = in_granules(region + at_y, y_row);
+      g_row = in_granules(region + at_gate, g_row);
+    }
     auto get_x = [&](int v) {
       if constexpr (RING) return Run::X::read(run, v, p);
-      else return load_pairs<R>(x_in + tr * io.residual_out_stride, v, p);
+      else return load_pairs<R>(x_row, v, p);
     };
     auto get_d = [&](int v) {
       if constexpr (RING) return Run::D::read(run, v, p);
-      else return load_pairs<R>(d_in + tr * io.dresidual_out_stride, v, p);
+      else return load_pairs<R>(d_row, v, p);
     };
     auto get_dh = [&](int v) {
       if constexpr (RING) return Run::DH::read(run, v, p);
-      else return load_pairs<T>(dh_in + tr * io.dh_stride, v, p);
+      else return load_pairs<T>(dh_row, v, p);
     };
     auto get_y = [&](int v) {
       if constexpr (RING) return Run::Y::read(run, v, p);
-      else return load_pairs<T>(y_in + tr * io.y_stride, v, p);
+      else return load_pairs<T>(y_row, v, p);
     };
     auto get_gate = [&](int v) {
       Pairs g;
       if (!full) g = load_pairs<T>(gate, v, p);
       else if constexpr (RING) g = Run::G::read(run, v, p);
-      else g = load_pairs<T>(gate + tr * io.gate_stride, v, p);
+      else g = load_pairs<T>(g_row, v, p);
       gate_pairs(s, g);
       return g;
     };
@@ -350,7 +395,7 @@ __global__ void __launch_bounds__(512, 1)
       if (live) put_pairs<T>(dyrow, v, p, y);
     }
   }
-  if constexpr (RING) copies_wait<0>();
+  copies_wait<0>();
   pdl_trigger();
   if (n_sums == 0) return;
   float* out = partial + (size_t)blockIdx.x * n_sums * hpad;
@@ -392,8 +437,8 @@ __global__ void __launch_bounds__(512, 1)
 template <typename T, typename R, int V, bool VEC, int LANES, bool WIDE, bool LAYER, int GATE, int PARTS>
 cudaError_t launch_gradient_rows(const moe_norm_config& c, NormShape s, const moe_norm_grad_io& io, int64_t rows,
                                  cudaStream_t stream) {
-  constexpr int RUN = BackwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>::UNITS;
-  const BackwardPlan b = plan_backward(c, VEC && V <= 2, V, LANES, RUN);
+  using Run = BackwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>;
+  const BackwardPlan b = plan_backward(c, VEC, V, LANES, Run::UNITS, Run::linear(LANES));
   s.lanes = b.lanes;
   auto kernel = block_norm_backward_kernel<T, R, V, VEC, LANES, WIDE, LAYER, GATE, PARTS>;
   static std::atomic<uint64_t> raised{0};

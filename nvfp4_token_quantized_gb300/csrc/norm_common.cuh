@@ -85,8 +85,11 @@ cudaError_t raise_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
 template <bool WIDE>
 struct RowSums {
   static constexpr int WARPS = 16;
-  static constexpr int WORDS = 2 * 4 * WARPS;
-  float* red;  // [2][warp][value]: entries past the last warp are 0 (clear())
+  // Sums of one, two and four values have places of their own, [warp][value]:
+  // entries past the last warp stay 0 (clear()).
+  static constexpr int HALF = (1 + 2 + 4) * WARPS;
+  static constexpr int WORDS = 2 * HALF;
+  float* red;  // [2][HALF]
   int lanes;  // threads of a row
   int turn = 0;
   __device__ __forceinline__ void clear() {
@@ -94,14 +97,18 @@ struct RowSums {
     __syncthreads();
   }
   __device__ __forceinline__ static float swap(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-  __device__ __forceinline__ float* next() { return red + (turn ^= 1) * (WORDS / 2); }
+  // N: 1, 2 or 4; the smaller ones' places come first
+  template <int N>
+  __device__ __forceinline__ float* next() {
+    return red + (turn ^= 1) * HALF + (N - 1) * WARPS;
+  }
 
   __device__ __forceinline__ void operator()(float (&v)[1]) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       if (WIDE || o < lanes) v[0] += swap(v[0], o);
     if constexpr (!WIDE) return;
-    float* buf = next();
+    float* buf = next<1>();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v[0];
     __syncthreads();
     // (every thread adds all partials, four at a read: half the latency of a
@@ -130,7 +137,7 @@ struct RowSums {
     float mine = (odd ? v[1] : v[0]) + swap(odd ? v[0] : v[1], 1);
 #pragma unroll
     for (int o = 16; o > 1; o >>= 1) mine += swap(mine, o);
-    float* buf = next();
+    float* buf = next<2>();
     if (lane < 2) buf[(threadIdx.x >> 5) * 2 + lane] = mine;
     __syncthreads();
     mine = buf[lane];  // warp lane / 2, value lane % 2
@@ -158,7 +165,7 @@ struct RowSums {
     float mine = (high ? b : a) + swap(high ? a : b, 2);
 #pragma unroll
     for (int o = 16; o > 2; o >>= 1) mine += swap(mine, o);
-    float* buf = next();
+    float* buf = next<4>();
     if (lane < 4) buf[(threadIdx.x >> 5) * 4 + lane] = mine;  // value 2 (lane & 1) + (lane >> 1)
     __syncthreads();
     // lane: warps lane / 4 and 8 + lane / 4, value as above
@@ -236,6 +243,37 @@ struct RingPieces {
   }
 };
 
+// Rows without 16-byte accesses: a row's threads copy the 16-byte granules that
+// hold it, at the offset it has in them, and read it after a barrier.  (The
+// first and last granule may hold bytes of the neighbouring rows or of what
+// lies next to the array: memory is allocated in larger pieces, and nothing
+// uses them.)
+__host__ __device__ constexpr int linear_bytes(int H, int element) { return ((H * element + 30) >> 4) << 4; }
+template <typename T>
+__device__ __forceinline__ void copy_granules(char* region, const T* row, int H, int i, int lanes) {
+  const int offset = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+  const char* from = reinterpret_cast<const char*>(row) - offset;
+  const int units = (offset + H * (int)sizeof(T) + 15) >> 4;
+  for (int u = i; u < units; u += lanes) copy16(region + 16 * u, from + 16 * u);
+}
+template <typename T>
+__device__ __forceinline__ const T* in_granules(const char* region, const T* row) {
+  return reinterpret_cast<const T*>(region + (reinterpret_cast<uintptr_t>(row) & 15));
+}
+template <bool WIDE>
+__device__ __forceinline__ void row_barrier() {
+  if constexpr (WIDE) __syncthreads();
+  else __syncwarp();
+}
+// Rows in their ring: two if the widest rows of a kernel leave room for the
+// CTAs that 512 threads make (elements: bytes of a column over all arrays).
+__host__ __device__ constexpr int linear_stages(int columns, int lanes, int column_bytes, int arrays) {
+  return 2 * (columns * column_bytes + 32 * arrays) * (512 / (lanes < 128 ? 128 : lanes)) *
+                     (lanes < 128 ? 128 / lanes : 1) <= 224 * 1024
+             ? 2
+             : 1;
+}
+
 // Chunk v of a row in global memory, zeros past its end.
 template <typename T, bool VEC, int LANES>
 __device__ __forceinline__ Pairs load_pairs(const T* row, int v, const Place<VEC, LANES>& p) {
@@ -298,6 +336,7 @@ __device__ __forceinline__ float sum_pairs(float2 a) { return a.x + a.y; }
 // A kernel's instantiation for a width: f(chunks, vec, constant lanes, wide).
 // With 16-byte accesses a thread holds one chunk up to `narrow` columns, two
 // up to 8192, four above; rows of up to 256 columns take a warp or less.
+// Without, the row's threads are constants that leave few of them idle.
 template <typename F>
 cudaError_t with_width(int H, int narrow, bool vec, F&& f) {
   using std::integral_constant;
@@ -313,14 +352,22 @@ cudaError_t with_width(int H, int narrow, bool vec, F&& f) {
     if (H <= 8192) return f(two, yes, any, yes);
     return f(four, yes, any, yes);
   }
-  constexpr auto half = integral_constant<int, 256>{};
-  constexpr auto full = integral_constant<int, 512>{};
   if (H <= 256) return f(one, no, integral_constant<int, 32>{}, no);
-  if (H <= 1024) return f(one, no, integral_constant<int, 128>{}, yes);
-  if (H <= 2048) return f(one, no, half, yes);
-  if (H <= 4096) return f(two, no, half, yes);
-  if (H <= 8192) return f(two, no, full, yes);
-  return f(four, no, full, yes);
+#define MOE_NORM_LANES(V, L) \
+  if (H <= V::value * 8 * L) return f(V{}, no, integral_constant<int, L>{}, yes)
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  MOE_NORM_LANES(One, 64);
+  MOE_NORM_LANES(One, 128);
+  MOE_NORM_LANES(One, 192);
+  MOE_NORM_LANES(One, 256);
+  MOE_NORM_LANES(Two, 192);
+  MOE_NORM_LANES(Two, 256);
+  MOE_NORM_LANES(Two, 320);
+  MOE_NORM_LANES(Two, 384);
+  MOE_NORM_LANES(Two, 512);
+#undef MOE_NORM_LANES
+  return f(four, no, integral_constant<int, 512>{}, yes);
 }
 
 // Which parts a call has: ALL of post-norm, pre-norm and block output (for
@@ -369,8 +416,10 @@ struct BackwardPlan {
   int64_t ctas(int64_t rows) const { return std::min<int64_t>((rows + groups - 1) / groups, 152 * ctas_per_sm); }
 };
 
-// units: of 16 bytes a thread has in a ring stage.
-inline BackwardPlan plan_backward(const moe_norm_config& c, bool ring, int V, int fixed_lanes, int units) {
+// units: of 16 bytes a thread has in a ring stage; linear_rows: stages of rows
+// without 16-byte accesses.
+inline BackwardPlan plan_backward(const moe_norm_config& c, bool vec, int V, int fixed_lanes, int units,
+                                  int linear_rows) {
   BackwardPlan b{};
   b.lanes = row_lanes(c.hidden, V, fixed_lanes);
   b.threads = row_cta_threads(b.lanes);
@@ -385,8 +434,11 @@ inline BackwardPlan plan_backward(const moe_norm_config& c, bool ring, int V, in
   }
   // (the ring's memory serves to add the groups' column sums at the end)
   b.smem = b.groups > 1 ? b.sums * b.groups * b.hpad * 4 : 0;
-  if (!ring) return b;
-  const int ring_bytes = ring_stages(units) * units * b.threads * 16;
+  const int tb = c.dtype == MOE_DTYPE_F32 ? 4 : 2, rb = c.residual_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const int arrays_t = (c.pre != 0) + (c.branch != 0) + (c.branch && c.gate == MOE_GATE_FULL);
+  const int ring_bytes =
+      vec ? ring_stages(units) * units * b.threads * 16
+          : linear_rows * b.groups * (arrays_t * linear_bytes(c.hidden, tb) + 2 * linear_bytes(c.hidden, rb));
   while (b.ctas_per_sm > 1 && ring_bytes > ring_room(b.ctas_per_sm)) --b.ctas_per_sm;
   b.smem = std::max(b.smem, ring_bytes);
   return b;
@@ -402,6 +454,9 @@ struct BackwardRun {
   using Y = RingPieces<T, V, DH::END>;
   using G = RingPieces<T, V, Y::END>;
   static constexpr int UNITS = WITH_GATE ? G::END : Y::END;
+  __host__ __device__ static constexpr int linear(int lanes) {
+    return lanes ? linear_stages(V * 8 * lanes, lanes, 3 * sizeof(T) + 2 * sizeof(R), 5) : 1;
+  }
 };
 
 // The gradient's grid for a call: ctas of the kernel that serves it.
@@ -413,8 +468,9 @@ int64_t gradient_ctas(const moe_norm_config& c, int64_t rows, bool vec, bool all
     constexpr int V = decltype(chunks)::value;
     constexpr bool VEC = decltype(v)::value;
     return with_kind<VEC, V>(s, all, [&](auto, auto gate, auto) {
-      constexpr int RUN = BackwardRun<T, R, V, (decltype(gate)::value & GATE_BY_ELEMENT) != 0>::UNITS;
-      n = plan_backward(c, VEC && V <= 2, V, decltype(fixed)::value, RUN).ctas(rows);
+      using Run = BackwardRun<T, R, V, (decltype(gate)::value & GATE_BY_ELEMENT) != 0>;
+      constexpr int LANES = decltype(fixed)::value;
+      n = plan_backward(c, VEC, V, LANES, Run::UNITS, Run::linear(LANES)).ctas(rows);
       return cudaSuccess;
     });
   });

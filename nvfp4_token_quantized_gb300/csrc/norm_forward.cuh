@@ -54,6 +54,9 @@ struct ForwardRun {
   using Y = RingPieces<T, V, X::END>;
   using G = RingPieces<T, V, Y::END>;
   static constexpr int UNITS = WITH_GATE ? G::END : Y::END;
+  __host__ __device__ static constexpr int linear(int lanes) {
+    return lanes ? linear_stages(V * 8 * lanes, lanes, 2 * sizeof(T) + sizeof(R), 3) : 1;
+  }
 };
 
 // A group of s.lanes threads walks rows; each CTA holds blockDim.x / s.lanes
@@ -87,32 +90,41 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
   const int64_t first = (int64_t)blockIdx.x * groups;
   const int warp_group = WIDE ? 0 : (threadIdx.x & ~31) / lanes;
 
-  Pairs ahead_r[VEC ? 1 : V], ahead_y[VEC ? 1 : V];
+  // Rows without 16-byte accesses lie in granules; the widest stay in global
+  // memory.
+  constexpr bool LINEAR = !VEC && V <= 2;
+  constexpr int ROWS = Run::linear(LANES);
+  const int r_bytes = linear_bytes(s.H, sizeof(R)), t_bytes = linear_bytes(s.H, sizeof(T));
+  const int linear_row = r_bytes + ((branch ? 1 : 0) + (full ? 1 : 0)) * t_bytes;
   auto run_of = [&](int stage) { return ring + stage * Run::UNITS * blockDim.x + threadIdx.x; };
+  auto region_of = [&](int stage) { return reinterpret_cast<char*>(ring) + (stage * groups + group) * linear_row; };
+  auto r_row = [&](int64_t t) { return static_cast<const R*>(io.residual) + t * io.residual_stride; };
+  auto y_row = [&](int64_t t) { return static_cast<const T*>(io.y) + t * io.y_stride; };
+  auto g_row = [&](int64_t t) { return gate + t * io.gate_stride; };
   auto fetch = [&](int64_t t, int stage) {
-    const R* r_row = static_cast<const R*>(io.residual) + t * io.residual_stride;
-    const T* y_row = static_cast<const T*>(io.y) + t * io.y_stride;
     if constexpr (VEC) {
       if (t < rows) {
         uint4* run = run_of(stage);
-        Run::X::fetch(run, r_row, p);
-        if (branch) Run::Y::fetch(run, y_row, p);
-        if (full) Run::G::fetch(run, gate + t * io.gate_stride, p);
+        Run::X::fetch(run, r_row(t), p);
+        if (branch) Run::Y::fetch(run, y_row(t), p);
+        if (full) Run::G::fetch(run, g_row(t), p);
       }
       copies_commit();
-    } else if (t < rows) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        ahead_r[v] = load_pairs<R>(r_row, v, p);
-        if (branch) ahead_y[v] = load_pairs<T>(y_row, v, p);
+    } else if constexpr (LINEAR) {
+      if (t < rows) {
+        char* region = region_of(stage);
+        copy_granules(region, r_row(t), s.H, p.i, LANES);
+        if (branch) copy_granules(region + r_bytes, y_row(t), s.H, p.i, LANES);
+        if (full) copy_granules(region + r_bytes + t_bytes, g_row(t), s.H, p.i, LANES);
       }
+      copies_commit();
     }
   };
   int64_t t = first + group;
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * step, i);
-  } else {
+  } else if constexpr (LINEAR && ROWS == 2) {
     fetch(t, 0);
   }
   if constexpr (KEEP) {
@@ -128,6 +140,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
     const bool live = WIDE || t < rows;
     const uint4* run = run_of(stage);
     Pairs r[V], y[V];
+    const T* from_gate = nullptr;
     if constexpr (VEC) {
       // into the stage of the row before this one (or, with one stage, this
       // row's), whose values this thread has used
@@ -141,12 +154,33 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
         for (int v = 0; v < V; ++v) y[v] = Run::Y::read(run, v, p);
       }
     } else {
+      const int64_t tr = live ? t : rows - 1;
+      const R* from_r = r_row(tr);
+      const T* from_y = y_row(tr);
+      from_gate = g_row(tr);
+      if constexpr (LINEAR) {
+        char* region = region_of(stage);
+        if constexpr (ROWS == 2) {
+          // this row has landed for all its threads, who have left the other stage
+          copies_wait<0>();
+          row_barrier<WIDE>();
+          fetch(t + step, stage ^ 1);
+          stage ^= 1;
+        } else {
+          row_barrier<WIDE>();
+          fetch(t, 0);
+          copies_wait<0>();
+          row_barrier<WIDE>();
+        }
+        from_r = in_granules(region, from_r);
+        from_y = in_granules(region + r_bytes, from_y);
+        from_gate = in_granules(region + r_bytes + t_bytes, from_gate);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        r[v] = ahead_r[v];
-        y[v] = ahead_y[v];
+        r[v] = load_pairs<R>(from_r, v, p);
+        if (branch) y[v] = load_pairs<T>(from_y, v, p);
       }
-      fetch(t + step, 0);
     }
     if (branch) {
       float scale = s.scale;
@@ -165,7 +199,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
           Pairs g;
           if (!full) g = load_pairs<T>(gate, v, p);
           else if constexpr (VEC) g = Run::G::read(run, v, p);
-          else g = load_pairs<T>(gate + t * io.gate_stride, v, p);
+          else g = load_pairs<T>(from_gate, v, p);
           gate_pairs(s, g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[v].p[j] = mul2(y[v].p[j], g.p[j]);
@@ -187,24 +221,35 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
       }
     }
   }
-  if constexpr (VEC) copies_wait<0>();
+  copies_wait<0>();
 }
 
 template <typename T, typename R, int V, bool VEC, int LANES, bool WIDE, bool LAYER, int GATE, int PARTS>
 cudaError_t launch_rows(NormShape s, const moe_norm_io& io, int64_t rows, cudaStream_t stream) {
   s.lanes = row_lanes(s.H, V, LANES);
   const int threads = row_cta_threads(s.lanes), groups = rows_per_cta(s.lanes);
-  constexpr int UNITS = ForwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>::UNITS;
-  const int smem = VEC ? ring_stages(UNITS) * UNITS * threads * 16 : 0;
+  using Run = ForwardRun<T, R, V, (GATE & GATE_BY_ELEMENT) != 0>;
+  constexpr int UNITS = Run::UNITS;
+  constexpr bool LINEAR = !VEC && V <= 2;
+  const int linear_row = linear_bytes(s.H, sizeof(R)) +
+                         (s.branch + (s.gate == MOE_GATE_FULL)) * linear_bytes(s.H, sizeof(T));
+  const int smem = VEC      ? ring_stages(UNITS) * UNITS * threads * 16
+                   : LINEAR ? Run::linear(LANES) * groups * linear_row
+                            : 0;
   auto kernel = block_norm_kernel<T, R, V, VEC, LANES, WIDE, LAYER, GATE, PARTS>;
   static std::atomic<uint64_t> raised{0};
   static std::atomic<int> resident[17];  // CTAs an SM holds, by warps; 0: not asked yet
-  cudaError_t e = raise_shared(kernel, VEC ? RING_ROOM : 0, raised);
+  cudaError_t e = raise_shared(kernel, VEC || LINEAR ? RING_ROOM : 0, raised);
   if (e != cudaSuccess) return e;
   std::atomic<int>& slot = resident[threads / 32];
   int ctas = slot.load(std::memory_order_relaxed);
   if (ctas == 0) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, smem);
+    // (granules: of the widest rows the kernel serves)
+    constexpr int WIDEST = V * 8 * LANES;
+    const int most = LINEAR ? Run::linear(LANES) * groups *
+                                  (linear_bytes(WIDEST, sizeof(R)) + 2 * linear_bytes(WIDEST, sizeof(T)))
+                            : smem;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, most);
     if (e != cudaSuccess) return e;
     ctas = std::max(ctas, 1);
     slot.store(ctas, std::memory_order_relaxed);

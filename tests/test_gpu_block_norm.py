@@ -370,3 +370,33 @@ def test_refusals():
     with pytest.raises(ValueError):
         n.backward(r, y, big[:4], r.clone(), post_weight=w, pre_weight=w,
                    workspace=torch.zeros(8, device="cuda"))
+
+
+@pytest.mark.parametrize("H", [17, 250, 511, 700, 1023, 1535, 1801, 3001, 4095, 5001, 6143, 8191])
+def test_odd_widths_over_many_rows(H):
+    # rows that start anywhere in a 16-byte granule, more of them than CTAs
+    T = 700
+    _check(T, H, gate="full", rdtype=F32)
+    _check(T, H, F16, kind="layer", gate="channel", pad=3, backward=H < 5000)
+    if H < 2000:
+        _check(T, H, F32, post=False, gate="token")
+
+
+def test_views_at_every_offset():
+    # rows of a view whose base is 2, 4, ... bytes into a granule
+    for off in range(1, 9):
+        a = _make(50, 264, BF16, BF16, BF16, None, True, True, pad=24)
+        for k in ("residual", "y", "dres", "dh"):
+            wide = torch.full((50, 300), 55.0, dtype=BF16, device="cuda")
+            wide[:, off:off + 264] = a[k]
+            a[k] = wide[:, off:off + 264]
+        _check(50, 264, arrays=a)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("H", [64, 256, 264, 512, 1024, 2048, 4096, 6144])
+def test_many_rows_a_cta(H, kind):
+    # more rows than CTAs at every width, so that each CTA walks several
+    T = 5000 if H <= 256 else 1500
+    _check(T, H, kind=kind, gate="channel", rdtype=F32)
+    _check(T, H, kind=kind, gate="token", post=H != 512, pre=H != 1024)
