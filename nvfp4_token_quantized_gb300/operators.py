@@ -47,29 +47,32 @@ def _device(t, name: str) -> int:
 
 def _rows(t, dtype, rows: int, width: int, name: str, dev: int) -> int:
     """Checks a [rows, width] tensor; returns its row stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+    try:
+        if t.shape == (rows, width) and t.dtype is dtype and t.get_device() == dev:
+            s0, s1 = t.stride()
+            if s0 >= width and s1 == 1:
+                return s0
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
     if t.shape != (rows, width):
         raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
     if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor on cuda:{dev}")
-    s0, s1 = t.stride()
     if s1 != 1 and width > 1:
         raise ValueError(f"{name}: the elements of a row must be next to each other")
-    if s0 >= width:
-        return s0
-    if rows > 1:
+    if rows > 1 and s0 < width:
         raise ValueError(f"{name}: rows overlap (row stride {s0}, width {width})")
-    return width
+    return max(s0, width)
 
 
 def _vector(t, dtype, n: int, name: str, dev: int) -> int:
     """Checks a contiguous tensor of n elements; returns its address."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{dev}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{dev}")
 
 
 class _OnStream:
@@ -91,11 +94,25 @@ class _OnStream:
         return self._ctx.__exit__(*a)
 
 
-# The current stream's handle and the current device, by torch's own cheap
-# getters where it has them (a Stream object costs more than a launch).
+# The current stream's handle, the current device and new tensors on it, by
+# torch's own cheap calls where it has them (a Stream object costs as much as a
+# launch, torch.empty two thirds of one).
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+try:
+    _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:  # pragma: no cover
+    def _empty_strided(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _new_rows(rows: int, width: int, dtype):
+    return _empty_strided((rows, width), (width, 1), dtype)
+
+
+def _new_vector(n: int, dtype):
+    return _empty_strided((n,), (1,), dtype)
 
 
 def _ok(st: int, what: str) -> None:
@@ -149,14 +166,14 @@ class ExpertRouter:
         n = T * self.K
         b = None if bias is None else _vector(bias, torch.float32, self.E, "bias", dev)
         if ids is None:
-            ids = torch.empty((T, self.K), dtype=torch.int32, device=logits.device)
+            ids = _new_rows(T, self.K, torch.int32)
             pi = ids.data_ptr()
         elif ids.shape != (T, self.K):
             raise ValueError(f"ids must be [{T}, {self.K}], got {tuple(ids.shape)}")
         else:
             pi = _vector(ids, torch.int32, n, "ids", dev)
         if weights is None:
-            weights = torch.empty((T, self.K), dtype=torch.float32, device=logits.device)
+            weights = _new_rows(T, self.K, torch.float32)
             pw = weights.data_ptr()
         elif weights.shape != (T, self.K):
             raise ValueError(f"weights must be [{T}, {self.K}], got {tuple(weights.shape)}")
@@ -181,7 +198,7 @@ class ExpertRouter:
         dev, dt, T, ld = self._logits(logits)
         n = T * self.K
         if dlogits is None:
-            dlogits, ldd = torch.empty((T, self.E), dtype=logits.dtype, device=logits.device), self.E
+            dlogits, ldd = _new_rows(T, self.E, logits.dtype), self.E
         else:
             ldd = _rows(dlogits, logits.dtype, T, self.E, "dlogits", dev)
         st = self._lib.moe_route_select_backward(
@@ -271,7 +288,7 @@ class BlockNorm:
         shape = residual.shape
         if len(shape) != 2:
             raise ValueError(f"residual must be [num_tokens, {self.H}], got {tuple(shape)}")
-        T, rt, place = shape[0], residual.dtype, residual.device
+        T, rt = shape[0], residual.dtype
         branch = y is not None
         dt = y.dtype if branch else rt if h is None else h.dtype
         r_ld = _rows(residual, rt, T, self.H, "residual", dev)
@@ -284,7 +301,7 @@ class BlockNorm:
             y_ld = _rows(y, dt, T, self.H, "y", dev)
             py = y.data_ptr()
             if residual_out is None:
-                residual_out = torch.empty((T, self.H), dtype=rt, device=place)
+                residual_out = _new_rows(T, self.H, rt)
             else:
                 o_ld = _rows(residual_out, rt, T, self.H, "residual_out", dev)
             po = residual_out.data_ptr()
@@ -292,7 +309,7 @@ class BlockNorm:
             residual_out = None
         if self.pre:
             if h is None:
-                h = torch.empty((T, self.H), dtype=dt, device=place)
+                h = _new_rows(T, self.H, dt)
             else:
                 h_ld = _rows(h, dt, T, self.H, "h", dev)
             ph = h.data_ptr()
@@ -334,7 +351,7 @@ class BlockNorm:
         dev = _device(first, "the incoming gradient")
         if len(first.shape) != 2:
             raise ValueError(f"gradients must be [num_tokens, {H}], got {tuple(first.shape)}")
-        T, branch, place = first.shape[0], y is not None, first.device
+        T, branch = first.shape[0], y is not None
         rt = dresidual_out.dtype if residual_out is None else residual_out.dtype
         dt = y.dtype if branch else dh.dtype if dh is not None else rt
         wp, wn, wt = self._weights(branch, post_weight, pre_weight, dt, dev)
@@ -350,7 +367,7 @@ class BlockNorm:
             x_ld = _rows(residual_out, rt, T, H, "residual_out", dev)
             ph, px = dh.data_ptr(), residual_out.data_ptr()
         if dresidual is None:
-            dresidual = torch.empty((T, H), dtype=rt, device=place)
+            dresidual = _new_rows(T, H, rt)
         else:
             dr_ld = _rows(dresidual, rt, T, H, "dresidual", dev)
         dgate = dpost = dpre = None
@@ -358,26 +375,26 @@ class BlockNorm:
             y_ld = _rows(y, dt, T, H, "y", dev)
             py = y.data_ptr()
             if dy is None:
-                dy = torch.empty((T, H), dtype=dt, device=place)
+                dy = _new_rows(T, H, dt)
             else:
                 dy_ld = _rows(dy, dt, T, H, "dy", dev)
             pdy = dy.data_ptr()
             if g is not None:
-                dgate = (torch.empty((T, H), dtype=dt, device=place) if self.gate == MOE_GATE_FULL else
+                dgate = (_new_rows(T, H, dt) if self.gate == MOE_GATE_FULL else
                          torch.empty_like(gate, dtype=torch.float32 if self.gate == MOE_GATE_CHANNEL else dt))
                 pdg = dgate.data_ptr()
             if wp is not None:
-                dpost = torch.empty(H, dtype=torch.float32, device=place)
+                dpost = _new_vector(H, torch.float32)
                 pdp = dpost.data_ptr()
         else:
             dy = None
         if wn is not None:
-            dpre = torch.empty(H, dtype=torch.float32, device=place)
+            dpre = _new_vector(H, torch.float32)
             pdn = dpre.data_ptr()
         need = int(lib.moe_block_norm_workspace_bytes(cfg, T))
         if need:
             if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=place)
+                workspace = _new_vector(need, torch.uint8)
             elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
                 raise ValueError(f"workspace must be a contiguous tensor of {need} bytes or more on cuda:{dev}")
             ws = workspace.data_ptr()
