@@ -95,11 +95,7 @@ __global__ void __launch_bounds__(512, 1)
   };
   // takes a mean off the values within the row
   auto centre = [&](Pairs& x, int v, float mean) {
-    if (layer) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x.p[j] = add2(x.p[j], make_float2(p.in_row(v, 2 * j) ? -mean : 0.0f, p.in_row(v, 2 * j + 1) ? -mean : 0.0f));
-    }
+    if (layer) add_in_row(x, -mean, v, p);
   };
 
   const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups;

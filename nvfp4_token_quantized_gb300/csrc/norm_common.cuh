@@ -283,8 +283,13 @@ __device__ __forceinline__ Pairs load_pairs(const T* row, int v, const Place<VEC
     return unpack(r);
   } else {
     float x[8];
+    if (p.in_row(v, 7)) {  // (all but a row's last warps)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = p.in_row(v, k) ? to_f32(row[p.column(v, k)]) : 0.0f;
+      for (int k = 0; k < 8; ++k) x[k] = to_f32(row[p.column(v, k)]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = p.in_row(v, k) ? to_f32(row[p.column(v, k)]) : 0.0f;
+    }
     Pairs o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.p[j] = make_float2(x[2 * j], x[2 * j + 1]);
@@ -296,9 +301,14 @@ __device__ __forceinline__ void put_pairs(T* row, int v, const Place<VEC, LANES>
   if constexpr (VEC) {
     if (p.in_row(v, 0)) store_pairs(row + p.column(v, 0), x);
   } else {
+    if (p.in_row(v, 7)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (p.in_row(v, k)) row[p.column(v, k)] = from_f32<T>(k & 1 ? x.p[k >> 1].y : x.p[k >> 1].x);
+      for (int k = 0; k < 8; ++k) row[p.column(v, k)] = from_f32<T>(k & 1 ? x.p[k >> 1].y : x.p[k >> 1].x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p.in_row(v, k)) row[p.column(v, k)] = from_f32<T>(k & 1 ? x.p[k >> 1].y : x.p[k >> 1].x);
+    }
   }
 }
 
@@ -319,6 +329,21 @@ __device__ __forceinline__ Pairs weight_pairs(const NormShape& s, const void* w,
   for (int j = 0; j < 4; ++j)
     o.p[j] = add2(o.p[j], make_float2(p.in_row(v, 2 * j) ? add : 0.0f, p.in_row(v, 2 * j + 1) ? add : 0.0f));
   return o;
+}
+
+// Adds a to the values within the row.
+template <bool VEC, int LANES>
+__device__ __forceinline__ void add_in_row(Pairs& x, float a, int v, const Place<VEC, LANES>& p) {
+  if (p.in_row(v, 7)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x.p[j] = add2(x.p[j], both(a));
+  } else if constexpr (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (p.in_row(v, 2 * j)) x.p[j].x += a;
+      if (p.in_row(v, 2 * j + 1)) x.p[j].y += a;
+    }
+  }
 }
 
 __device__ __forceinline__ float gate_value(const NormShape& s, float g) {
@@ -378,7 +403,7 @@ constexpr int GATE_BY_CHANNEL = 1, GATE_BY_ELEMENT = 2, GATE_ANY = 3;
 
 // f(layer, gate, parts): the kernels for rows with 16-byte accesses of all
 // parts come without the code of what a call leaves out; other calls share
-// one that has it all.
+// one that has it all, or all but a gate by channel or element.
 template <bool VEC, int V, typename F>
 cudaError_t with_kind(const NormShape& s, bool all, F&& f) {
   using std::integral_constant;
@@ -393,7 +418,12 @@ cudaError_t with_kind(const NormShape& s, bool all, F&& f) {
       return s.layer ? gate(std::true_type{}) : gate(std::false_type{});
     }
   }
-  return f(std::true_type{}, integral_constant<int, GATE_ANY>{}, integral_constant<int, PARTS_ANY>{});
+  constexpr auto any = integral_constant<int, PARTS_ANY>{};
+  if constexpr (!VEC) {  // (whose registers the sums of a gate would overflow)
+    if (s.gate == MOE_GATE_NONE || s.gate == MOE_GATE_TOKEN)
+      return f(std::true_type{}, integral_constant<int, 0>{}, any);
+  }
+  return f(std::true_type{}, integral_constant<int, GATE_ANY>{}, any);
 }
 
 // Shared memory of an SM for the rings of n CTAs each: of 228 KB, less the

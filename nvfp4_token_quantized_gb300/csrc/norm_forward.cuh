@@ -32,11 +32,7 @@ __device__ __forceinline__ float centre_and_scale(const NormShape& s, const Plac
     sums(a);
     const float mean = -a[0] * s.inv_h;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[v].p[j] = add2(x[v].p[j], make_float2(p.in_row(v, 2 * j) ? mean : 0.0f,
-                                                p.in_row(v, 2 * j + 1) ? mean : 0.0f));
+    for (int v = 0; v < V; ++v) add_in_row(x[v], mean, v, p);
   }
   float2 q = both(0.0f);
 #pragma unroll
