@@ -17,9 +17,16 @@ __device__ __forceinline__ constexpr int type_of(float) { return MOE_DTYPE_F32; 
 __device__ __forceinline__ constexpr int type_of(__half) { return MOE_DTYPE_F16; }
 __device__ __forceinline__ constexpr int type_of(__nv_bfloat16) { return MOE_DTYPE_BF16; }
 
+// CTAs an SM should hold: groups take registers that a fourth would have to
+// spill (131072 x 256 in 8 groups: 66 us with three, 69 with four; ungrouped
+// the fourth gains 3 to 8 %).
+constexpr int select_ctas(int NE, int MODE) {
+  return NE > 8 ? 1 : MODE >= 0 && (MODE & SELECT_LIMITED) ? 3 : 4;
+}
+
 // RB rows a warp.
 template <int NE, int RB, int MODE>
-__global__ void __launch_bounds__(32 * SELECT_WARPS, NE <= 8 ? 3 : 1)
+__global__ void __launch_bounds__(32 * SELECT_WARPS, select_ctas(NE, MODE))
     select_kernel(const RouteRule r, const void* __restrict__ logits, int dtype, int64_t stride,
                   const float* __restrict__ bias, int64_t rows, int32_t* __restrict__ ids, float* __restrict__ w) {
   __shared__ __align__(16) SelectScratch<RB> scratch[SELECT_WARPS];
