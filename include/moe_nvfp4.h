@@ -53,6 +53,10 @@
  * stream order; the caller keeps them alive until the stream reaches the
  * work.  The handle owns the quantized weights and all workspace.
  *
+ * Streams: weights, scales and a routing bias are written in the order of the
+ * stream they are set on; a forward on another stream waits for them on the
+ * device (not inside a stream capture, which cannot wait for work outside).
+ *
  * Errors: every entry point returns a moe_status and never aborts; the text
  * of the last error on a handle is available from moe_get_last_error.
  * Kernel-side waits are bounded: a wait that runs out records

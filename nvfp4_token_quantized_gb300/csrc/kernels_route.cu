@@ -977,8 +977,9 @@ cudaError_t with_front(int T, int E, F&& f) {
 template <int TPC, int UPW>
 cudaError_t launch_front_t(const FrontArgs& a, cudaStream_t s) {
   // first kernel of a forward: ordinary stream order
-  return launch_k(a.ruled ? front_small_kernel<TPC, UPW, true> : front_small_kernel<TPC, UPW, false>, dim3((a.T + TPC - 1) / TPC), dim3(256),
-                  (size_t)front_smem_bytes(a.H, a.E, TPC), s, false, a);
+  auto kernel = a.ruled ? front_small_kernel<TPC, UPW, true> : front_small_kernel<TPC, UPW, false>;
+  return launch_k(kernel, dim3((a.T + TPC - 1) / TPC), dim3(256), (size_t)front_smem_bytes(a.H, a.E, TPC), s, false,
+                  a);
 }
 
 }  // namespace

@@ -70,6 +70,11 @@ struct moe_handle {
   int s_clusters[2] = {0, 0};
   cudaStream_t side = nullptr;
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
+  // Weights, scales and the routing bias are written in the order of the
+  // stream they were set on: a forward on another one waits for the event.
+  cudaEvent_t ev_state = nullptr;
+  cudaStream_t state_stream = nullptr, state_seen = nullptr;
+  bool state_recorded = false;
   // moe_set_routing: the rule of the choice of experts and its balance bias [E]
   bool ruled = false, rule_bias = false;
   RouteRule rule{};
@@ -226,7 +231,11 @@ bool same_desc(const moe_weight_desc& a, const moe_weight_desc& b) {
          a.device == b.device;
 }
 
+cudaError_t await_state(moe_handle* h, cudaStream_t s);
+cudaError_t state_written(moe_handle* h, cudaStream_t s);
+
 moe_status quantize_weights(moe_handle* h, const void* w13, const void* w2, cudaStream_t s) {
+  CK(h, await_state(h, s));
   CK(h, cudaMemsetAsync(h->amax_bits, 0, sizeof(uint32_t) * 2 * h->E, s));
   CK(h, launch_weight_amax(w13, h->E, 2 * h->I, h->H, h->amax_bits, s));
   CK(h, launch_weight_amax(w2, h->E, h->H, h->I, h->amax_bits + h->E, s));
@@ -234,6 +243,7 @@ moe_status quantize_weights(moe_handle* h, const void* w13, const void* w2, cuda
                             s));
   CK(h, launch_weight_quant(w2, h->E, h->H, h->I, h->Ipad, 0, h->amax_bits + h->E, h->w2_codes, h->w2_sf, h->gs_w2,
                             s));
+  CK(h, state_written(h, s));
   return MOE_OK;
 }
 
@@ -248,6 +258,31 @@ struct DeviceGuard {
     if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
   }
 };
+
+bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(s, &cs) == cudaSuccess && cs != cudaStreamCaptureStatusNone;
+}
+
+// Orders stream s after the last writes of the handle's state.  (A capture
+// cannot wait for work outside it; its replays come after whatever the caller
+// ordered them after.)
+cudaError_t await_state(moe_handle* h, cudaStream_t s) {
+  if (!h->state_recorded || s == h->state_stream || s == h->state_seen || capturing(s)) return cudaSuccess;
+  const cudaError_t e = cudaStreamWaitEvent(s, h->ev_state, 0);
+  if (e == cudaSuccess) h->state_seen = s;
+  return e;
+}
+
+// The handle's state has been written in stream s.
+cudaError_t state_written(moe_handle* h, cudaStream_t s) {
+  if (capturing(s)) return cudaSuccess;
+  const cudaError_t e = cudaEventRecord(h->ev_state, s);
+  if (e != cudaSuccess) return e;
+  h->state_stream = h->state_seen = s;
+  h->state_recorded = true;
+  return cudaSuccess;
+}
 
 // Stage boundary i.  Inside a stream capture the record becomes an external
 // event node (re-recorded on every replay); outside it is a plain record.
@@ -335,6 +370,7 @@ moe_status forward_impl(moe_handle* h, const void* x, const void* gate_w, const 
                         cudaStream_t s) {
   const int H = h->H, E = h->E, K = h->K;
   if (T > 0) {
+    CK(h, await_state(h, s));
     const int tile_rows = tile_rows_for(T);
     const bool small = T <= SMALL_BATCH_TOKENS;
     if (h->Is > 0) TRY(shared_branch(h, x, T, s));
@@ -647,7 +683,9 @@ moe_status moe_create(const moe_config* cfg, moe_handle** out) {
     if (e != cudaSuccess) return fail(cuda_fail(h, e, "cudaHostGetDevicePointer"));
   }
   {
-    cudaError_t e = gemm_setup_attributes(I / 128);
+    cudaError_t e = cudaEventCreateWithFlags(&h->ev_state, cudaEventDisableTiming);
+    if (e != cudaSuccess) return fail(cuda_fail(h, e, "cudaEventCreate"));
+    e = gemm_setup_attributes(I / 128);
     if (e != cudaSuccess) return fail(cuda_fail(h, e, "cudaFuncSetAttribute"));
     e = router_setup(H, E);
     if (e == cudaSuccess) e = front_setup(H, E);
@@ -686,8 +724,10 @@ moe_status moe_set_static_scales(moe_handle* h, const float* x_gs, const float* 
   }
   DeviceGuard dg(h->cfg.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CK(h, await_state(h, s));
   CK(h, cudaMemcpyAsync(h->static_x_gs, x_gs, sizeof(float), cudaMemcpyDeviceToDevice, s));
   CK(h, cudaMemcpyAsync(h->static_h_gs, h_gs, sizeof(float) * h->E, cudaMemcpyDeviceToDevice, s));
+  CK(h, state_written(h, s));
   h->static_set = true;
   return MOE_OK;
 }
@@ -715,8 +755,10 @@ moe_status moe_set_routing(moe_handle* h, const moe_route_config* cfg, const flo
       set_err(h, "moe_set_routing: the bias is not on device %d", h->cfg.device);
       return MOE_ERR_INVALID_ARG;
     }
-    CK(h, cudaMemcpyAsync(h->route_bias, bias, sizeof(float) * h->E, cudaMemcpyDeviceToDevice,
-                          reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    CK(h, await_state(h, s));
+    CK(h, cudaMemcpyAsync(h->route_bias, bias, sizeof(float) * h->E, cudaMemcpyDeviceToDevice, s));
+    CK(h, state_written(h, s));
   }
   h->rule = rule;
   h->rule_bias = bias != nullptr;
@@ -732,6 +774,7 @@ moe_status moe_destroy(moe_handle* h) {
   if (h->status_host) cudaFreeHost(h->status_host);
   for (cudaEvent_t ev : h->events)
     if (ev) cudaEventDestroy(ev);
+  if (h->ev_state) cudaEventDestroy(h->ev_state);
   if (h->ev_fork) cudaEventDestroy(h->ev_fork);
   if (h->ev_join) cudaEventDestroy(h->ev_join);
   if (h->side) cudaStreamDestroy(h->side);
@@ -753,6 +796,7 @@ moe_status moe_load_shared_weights(moe_handle* h, const void* w13s, const moe_we
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // one expert: the routed experts' conversion (gate / up rows interleaved
   // in chunks of 64 for the w13 epilogue), into the same buffers every time
+  CK(h, await_state(h, s));
   CK(h, cudaMemsetAsync(h->s_amax_bits, 0, sizeof(uint32_t) * 2, s));
   CK(h, launch_weight_amax(w13s, 1, 2 * h->Is, h->H, h->s_amax_bits, s));
   CK(h, launch_weight_amax(w2s, 1, h->H, h->Is, h->s_amax_bits + 1, s));
@@ -760,6 +804,7 @@ moe_status moe_load_shared_weights(moe_handle* h, const void* w13s, const moe_we
                             h->gs_sw13, s));
   CK(h, launch_weight_quant(w2s, 1, h->H, h->Is, h->Ipad_s, 0, h->s_amax_bits + 1, h->sw2_codes, h->sw2_codes,
                             h->gs_sw2, s));
+  CK(h, state_written(h, s));
   h->shared_loaded = true;
   h->err.clear();
   return MOE_OK;

@@ -181,3 +181,37 @@ def test_example_runs_them_together():
         losses.append(stack.router_step({"layer": 0, **trace[0]}, target, lr=20.0).item())
         _, trace = stack.forward(x)
     assert losses[2] < losses[0]
+
+
+def test_state_set_on_one_stream_is_seen_on_another(setup):
+    # weights, then a bias, set behind a long kernel of their stream: forwards
+    # on other streams wait for them
+    from nvfp4_token_quantized_gb300 import ExpertRouter, MoE
+
+    _, d, _, _ = setup
+    r = ExpertRouter(SHAPE.E, SHAPE.K, **RULES[0])
+    ref = _layer(d)
+    ref.set_routing(r, _bias(5))
+    want = {T: ref.forward(d["x"][:T], d["gate_w"]) for T in (40, 150)}
+    big = torch.zeros(1 << 30, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for T in (40, 150):
+        a, b, c = (torch.cuda.Stream() for _ in range(3))
+        layer = MoE.from_shape(SHAPE, deterministic=True)
+        with torch.cuda.stream(a):
+            for _ in range(20):
+                big.add_(1)
+            layer.load_weights(d["w13"], d["w2"])
+        with torch.cuda.stream(b):
+            layer.set_routing(r, _bias(5))
+            got_b = layer.forward(d["x"][:T], d["gate_w"])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(a):
+            for _ in range(20):
+                big.add_(1)
+            layer.set_routing(r, _bias(6))
+            layer.set_routing(r, _bias(5))
+        with torch.cuda.stream(c):
+            got_c = layer.forward(d["x"][:T], d["gate_w"])
+        torch.cuda.synchronize()
+        assert torch.equal(got_b, want[T]) and torch.equal(got_c, want[T])
