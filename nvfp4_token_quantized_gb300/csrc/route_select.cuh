@@ -219,6 +219,32 @@ __device__ __forceinline__ void merge2(float& b1, float& b2, float c1, float c2)
   b1 = fmaxf(b1, c1);
 }
 
+// The sum over the warp of one value a row; lane l gets row
+// row_of_lane(l % 4 or 2)'s.  Each step hands half of the rows to the other
+// half of the lanes; the order of additions is the same for every RB.
+template <int RB>
+__device__ __forceinline__ constexpr int row_of_lane(int l) {
+  return RB == 4 ? 2 * (l & 1) + (l >> 1 & 1) : RB == 2 ? l & 1 : 0;
+}
+template <int RB>
+__device__ __forceinline__ float sum_rows(const float (&v)[RB], int lane) {
+  constexpr unsigned all = 0xffffffffu;
+  const bool odd = lane & 1, high = lane & 2;
+  float mine;
+  if constexpr (RB == 4) {
+    const float a = (odd ? v[2] : v[0]) + __shfl_xor_sync(all, odd ? v[0] : v[2], 1);
+    const float b = (odd ? v[3] : v[1]) + __shfl_xor_sync(all, odd ? v[1] : v[3], 1);
+    mine = (high ? b : a) + __shfl_xor_sync(all, high ? a : b, 2);
+  } else {
+    if constexpr (RB == 2) mine = (odd ? v[1] : v[0]) + __shfl_xor_sync(all, odd ? v[0] : v[1], 1);
+    else mine = v[0] + __shfl_xor_sync(all, v[0], 1);
+    mine += __shfl_xor_sync(all, mine, 2);
+  }
+#pragma unroll
+  for (int o = 16; o > 2; o >>= 1) mine += __shfl_xor_sync(all, mine, o);
+  return mine;
+}
+
 // The logits of this lane's experts, -inf where it has none.
 template <int NE>
 __device__ __forceinline__ void load_logits(const RouteRule& r, const void* row, int dtype, int lane,
@@ -319,7 +345,7 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
   }
   // this lane's best, and its group's score
   constexpr int DEPTH = MODE < 0 || (MODE & SELECT_LIMITED) ? 3 : 2;
-  float best[RB][DEPTH], group[RB];
+  float best[RB][DEPTH], group[RB], part[RB];
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
     // A finite sum means finite logits.  Otherwise some are closed (fine), or
@@ -334,37 +360,45 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       for (int i = 0; i < NE; ++i) bad |= !(v[q][i] < INFINITY);
       if (__any_sync(all, bad)) odd |= 1u << q;
     }
-    float top = 0.0f, total = 1.0f;
-    if (!sigmoid) {
-      float m = v[q][0];
+    part[q] = 0.0f;
+    if (sigmoid ? by_score : need_total) {
+      float top = 0.0f;
+      if (!sigmoid) {
+        float m = v[q][0];
 #pragma unroll
-      for (int i = 1; i < NE; ++i) m = fmaxf(m, v[q][i]);
-      m = max_lanes(m);
-      top = m == -INFINITY ? 0.0f : m;
-    }
-    if (by_score || need_total) {
-      float s[NE];
-      float sum = 0.0f;
+        for (int i = 1; i < NE; ++i) m = fmaxf(m, v[q][i]);
+        m = warp_top(m);
+        top = m == -INFINITY ? 0.0f : m;
+        if (lane == 0) sm.top[q] = top;
+      }
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        s[i] = sigmoid ? sigmoid_fast(v[q][i]) : exp_fast(v[q][i] - top);
-        if (need_total) sum += s[i];
-      }
-      if (need_total) {
-        sum = sum_lanes(sum);
-        total = sum == 0.0f ? 1.0f : sum;
-      }
-      if (by_score) {
-        if (closed) {
-#pragma unroll
-          for (int i = 0; i < NE; ++i)
-            if (v[q][i] == -INFINITY) s[i] = -INFINITY;
-        }
-        const float k = sigmoid ? 1.0f : 1.0f / total;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) v[q][i] = sigmoid ? s[i] + b[i] : fmaf(s[i], k, b[i]);
+        const float s = sigmoid ? sigmoid_fast(v[q][i]) + b[i] : exp_fast(v[q][i] - top);
+        part[q] += s;
+        if (by_score && (!closed || v[q][i] != -INFINITY)) v[q][i] = s;
       }
     }
+  }
+  if (need_total) {
+    // sums over the experts; a lane goes on with one of the rows
+    float total = sum_rows<RB>(part, lane);
+    if (total == 0.0f) total = 1.0f;
+    if (lane < RB) sm.total[row_of_lane<RB>(lane)] = total;
+    if (by_score) {
+#pragma unroll
+      for (int q = 0; q < RB; ++q) {
+        const float k = 1.0f / __shfl_sync(all, total, row_of_lane<RB>(q));  // (its own inverse)
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[q][i] = fmaf(v[q][i], k, b[i]);  // (-inf stays)
+      }
+    }
+  } else if (!sigmoid && lane < RB) {
+    // The sum cancels from renormalised weights (the best logit is among the
+    // chosen, so their sum is far above the 1e-20).
+    sm.total[lane] = 1.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < RB; ++q) {
     if (!by_score && dtype != MOE_DTYPE_F32) {
       // Equal logits are common in 16 bits.  Their FP32 values end in 13 zero
       // bits or more: the expert's id there makes each its own, the lower id
@@ -385,9 +419,10 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
         if (s < r.lane_shift) merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
       group[q] = r.top2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
-    if (!sigmoid && lane == 0) {
-      sm.top[q] = top;
-      sm.total[q] = total;
+    if (!sigmoid && !need_total) {
+      float m = warp_top(best[q][0]);
+      if (dtype != MOE_DTYPE_F32) m = __uint_as_float(__float_as_uint(m) & ~0x1fffu);  // (without the id)
+      if (lane == 0) sm.top[q] = m == -INFINITY ? 0.0f : m;
     }
   }
   // Which groups each row keeps.  A group's score is in all its lanes: lane d
