@@ -408,11 +408,12 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
 
 /* The choice of top_k of num_experts experts from logits l:
  *   s_e = softmax over all experts of l, or sigmoid(l_e);
- *   v_e = s_e + bias_e with a balance bias or with MOE_GROUP_TOP2 groups,
- *         else l_e (which orders as s_e does);
+ *   v_e = s_e + bias_e with a balance bias, else l_e (which orders as s_e
+ *         does);
  *   groups: the experts form num_groups runs of equal length, and only those
  *         of the top_groups best groups may be chosen.  A group scores its
- *         largest v, or the sum of its two largest;
+ *         largest v (MOE_GROUP_MAX), or the sum of its two largest s, plus
+ *         their biases (MOE_GROUP_TOP2);
  *   ids:  the top_k largest v, ties to the lower expert id (between groups
  *         to the lower group);
  *   w_k = scale * s / (sum of the chosen s + 1e-20) with renormalize, else

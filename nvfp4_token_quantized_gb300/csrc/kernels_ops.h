@@ -21,7 +21,7 @@ struct RouteRule {
   int E, K;
   int groups, size, top_groups, lane_shift;
   int sigmoid, top2, renormalize;
-  int by_score;  // the choice compares scores (plus bias), not logits
+  int by_score;  // the choice compares scores plus bias, not logits (which order as scores do)
   int slot_shift;  // 2^slot_shift >= K: lanes of a row's slots
   float scale;
   // A lane's experts of its group: chunks of four neighbours (rows that take

@@ -32,7 +32,7 @@ moe_status make_route_rule(const moe_route_config* cfg, bool has_bias, RouteRule
   r.top_groups = limited ? cfg->top_groups : 1;
   r.size = E / r.groups;
   r.top2 = cfg->group_score == MOE_GROUP_TOP2;
-  r.by_score = has_bias || (G > 1 && r.top2);
+  r.by_score = has_bias;
   r.lane_shift = 5;
   while ((r.groups << r.lane_shift) > 32) --r.lane_shift;
   while ((1 << r.slot_shift) < K) ++r.slot_shift;

@@ -126,7 +126,15 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
       b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
       b1 = fmaxf(b1, c1);
     }
-    const float gs = r.top2 && b2 > -INFINITY ? b1 + b2 : b1;
+    float gs = b1;
+    if (r.top2 && b1 > -INFINITY) {
+      // (of a softmax, what its sum would divide)
+      if (!r.by_score) {
+        b1 = r.sigmoid ? sigmoid_ieee(b1) : expf(b1 - m);
+        b2 = r.sigmoid ? sigmoid_ieee(b2) : expf(b2 - m);
+      }
+      gs = b2 > -INFINITY ? b1 + b2 : b1;
+    }
     int rank = 0;
     for (int j = 0; j < r.groups; ++j) {
       const float other = __shfl_sync(0xffffffffu, gs, j << r.lane_shift);
@@ -345,7 +353,10 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
   }
   // this lane's best, and its group's score
   constexpr int DEPTH = MODE < 0 || (MODE & SELECT_LIMITED) ? 3 : 2;
-  float best[RB][DEPTH], group[RB], part[RB];
+  float best[RB][DEPTH], group[RB], part[RB], top[RB];
+  auto without_id = [&](float f) {
+    return dtype == MOE_DTYPE_F32 ? f : __uint_as_float(__float_as_uint(f) & ~0x1fffu);
+  };
 #pragma unroll
   for (int q = 0; q < RB; ++q) {
     // A finite sum means finite logits.  Otherwise some are closed (fine), or
@@ -360,20 +371,18 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       for (int i = 0; i < NE; ++i) bad |= !(v[q][i] < INFINITY);
       if (__any_sync(all, bad)) odd |= 1u << q;
     }
-    part[q] = 0.0f;
+    part[q] = top[q] = 0.0f;
     if (sigmoid ? by_score : need_total) {
-      float top = 0.0f;
       if (!sigmoid) {
         float m = v[q][0];
 #pragma unroll
         for (int i = 1; i < NE; ++i) m = fmaxf(m, v[q][i]);
         m = warp_top(m);
-        top = m == -INFINITY ? 0.0f : m;
-        if (lane == 0) sm.top[q] = top;
+        top[q] = m == -INFINITY ? 0.0f : m;
       }
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        const float s = sigmoid ? sigmoid_fast(v[q][i]) + b[i] : exp_fast(v[q][i] - top);
+        const float s = sigmoid ? sigmoid_fast(v[q][i]) + b[i] : exp_fast(v[q][i] - top[q]);
         part[q] += s;
         if (by_score && (!closed || v[q][i] != -INFINITY)) v[q][i] = s;
       }
@@ -412,17 +421,28 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       }
     }
     lane_best<NE, DEPTH>(v[q], best[q]);
+    if (!sigmoid && !need_total) {
+      const float m = without_id(warp_top(best[q][0]));
+      top[q] = m == -INFINITY ? 0.0f : m;
+    }
+    if (!sigmoid && lane == 0) sm.top[q] = top[q];
     if (limited) {
       float b1 = best[q][0], b2 = best[q][1];
 #pragma unroll
       for (int s = 0; s < 5; ++s)
         if (s < r.lane_shift) merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
-      group[q] = r.top2 && b2 > -INFINITY ? b1 + b2 : b1;
-    }
-    if (!sigmoid && !need_total) {
-      float m = warp_top(best[q][0]);
-      if (dtype != MOE_DTYPE_F32) m = __uint_as_float(__float_as_uint(m) & ~0x1fffu);  // (without the id)
-      if (lane == 0) sm.top[q] = m == -INFINITY ? 0.0f : m;
+      group[q] = b1;
+      if (r.top2) {
+        if (!by_score) {
+          b1 = without_id(b1), b2 = without_id(b2);
+          // (of a softmax, what its sum would divide)
+          const float s1 = sigmoid ? sigmoid_fast(b1) : exp_fast(b1 - top[q]);
+          const float s2 = sigmoid ? sigmoid_fast(b2) : exp_fast(b2 - top[q]);
+          group[q] = b1 > -INFINITY ? s1 + s2 : -INFINITY;
+        } else if (b2 > -INFINITY) {
+          group[q] = b1 + b2;
+        }
+      }
     }
   }
   // Which groups each row keeps.  A group's score is in all its lanes: lane d
