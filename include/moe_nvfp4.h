@@ -400,7 +400,8 @@ MOE_API moe_status moe_debug_block_scaled_gemm(const uint8_t* a_codes, const uin
  * must be an sm_103a device (else MOE_ERR_UNSUPPORTED).  Row strides are in
  * elements and at least the row's length; rows need no alignment beyond
  * their element's (aligned rows whose length is a multiple of 8, for the
- * routing of 4, take wider loads).  Zero tokens are a no-op.
+ * routing of 4, take wider loads; of other rows whole 16-byte granules may be
+ * read, whose bytes outside the row are not used).  Zero tokens are a no-op.
  * ------------------------------------------------------------------------ */
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
@@ -449,7 +450,8 @@ MOE_API moe_status moe_route_select(const moe_route_config* cfg, const void* log
 
 /* Gradient of the weights with respect to the logits, the choice held fixed
  * (the bias gets none).  logits, topk_ids and topk_w are moe_route_select's
- * input and outputs, dweights FP32 [num_tokens, top_k]; dlogits gets every
+ * input and its own outputs (the sigmoid's gradient takes the scores from the
+ * weights), dweights FP32 [num_tokens, top_k]; dlogits gets every
  * element of [num_tokens, num_experts] in the logits' type.  A slot of weight
  * 0, or whose id is outside [0, num_experts), passes no gradient; a token's
  * ids must be distinct.  dlogits may be logits itself (same stride). */
@@ -527,7 +529,8 @@ typedef struct {
 } moe_norm_grad_io;
 
 /* Device bytes moe_block_norm_backward needs for its column sums; 0 for a
- * refused cfg.  Never more than 152 * 2 rows of 3 * hidden floats. */
+ * refused cfg.  At most a row of floats, hidden rounded up to 8, for each CTA
+ * of one wave and each weight or channel gate with a gradient. */
 MOE_API size_t moe_block_norm_workspace_bytes(const moe_norm_config* cfg, int64_t rows);
 
 /* The statistics are those of the stored residual_out.  dresidual may be

@@ -43,36 +43,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight consecutive values from / to 16-byte aligned memory (plain accesses:
-// an operand may be overwritten in place by the same thread later).
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&o)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2(w[i], T());
-    o[2 * i] = f.x;
-    o[2 * i + 1] = f.y;
-  }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&o)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
-  o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
-                                            pack2(v[6], v[7], T()));
-}
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 // Eight values as four pairs for the two-lane FP32 instructions.
 struct Pairs {
   float2 p[4];
@@ -124,7 +94,8 @@ __device__ __forceinline__ Pairs unpack<float>(const Raw8<float>& r) {
   o.p[3] = make_float2(__uint_as_float(r.q[1].z), __uint_as_float(r.q[1].w));
   return o;
 }
-// 16-byte aligned accesses.
+// 16-byte aligned accesses (plain ones: an operand may be overwritten in place
+// by the same thread later).
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_raw(const T* p) {
   Raw8<T> r;

@@ -82,9 +82,9 @@ cudaError_t launch_block_norm_backward(const moe_norm_config& c, const moe_norm_
   if (sh.post) o.out[n++] = io.dpost_weight;
   if (sh.pre) o.out[n++] = io.dpre_weight;
   if (sh.gate == MOE_GATE_CHANNEL) o.out[n++] = static_cast<float*>(io.dgate);
+  const int ctas = (int)plan_ctas(c, rows, vec, sh.post && sh.pre && io.dresidual_out);
   return launch_k(column_sum_kernel, dim3((c.hidden + 31) / 32, sums), dim3(32, 32), 0, s, true,
-                  static_cast<const float*>(io.workspace), (int)plan_ctas(c, rows, vec, sh.post && sh.pre && io.dresidual_out), sums, c.hidden,
-                  (c.hidden + 7) & ~7, o);
+                  static_cast<const float*>(io.workspace), ctas, sums, c.hidden, (c.hidden + 7) & ~7, o);
 }
 
 }  // namespace moe
