@@ -581,13 +581,13 @@ __device__ __forceinline__ void quantize_token_row(const uint4* xr, int t, int H
 // memory (E <= 256; 16 experts a lane cover every group count).
 template <int NE>
 __device__ __forceinline__ void front_select_n(const RouteRule& r, const float* lrow, const float* __restrict__ bias,
-                                               int lane, SelectScratch<1>& sm, int32_t* ids, float* w) {
+                                               int lane, SelectScratch& sm, int32_t* ids, float* w) {
   float b[NE];
   const bool finite = load_bias<NE>(r, bias, lane, b);
-  select_rows<NE, 1, SELECT_ANY>(r, lrow, MOE_DTYPE_F32, 0, 1, bias, b, finite, lane, sm, ids, w);
+  select_row<NE>(r, lrow, MOE_DTYPE_F32, bias, b, finite, lane, sm, ids, w);
 }
 __device__ __forceinline__ void front_select(RouteRule r, const float* lrow, const float* __restrict__ bias,
-                                             int lane, SelectScratch<1>& sm, int32_t* ids, float* w) {
+                                             int lane, SelectScratch& sm, int32_t* ids, float* w) {
   set_select_loads(r, true);  // (rows of 8n floats, 16-byte aligned)
   if (select_per_lane(r) <= 8) front_select_n<8>(r, lrow, bias, lane, sm, ids, w);
   else front_select_n<16>(r, lrow, bias, lane, sm, ids, w);
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(256, 1) front_small_kernel(const __grid_consta
     const int t = t0 + warp;
     if (t < T) {
       if constexpr (RULED) {
-        __shared__ __align__(16) SelectScratch<1> scratch[TPC];
+        __shared__ __align__(16) SelectScratch scratch[TPC];
         int32_t* ids = p.topk_ids + (size_t)t * K;
         front_select(p.rule, slog + warp * E, p.route_bias, lane, scratch[warp], ids, p.topk_w + (size_t)t * K);
         if (lane < K) chosen[warp][lane] = ids[lane];

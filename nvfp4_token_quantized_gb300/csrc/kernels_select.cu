@@ -6,6 +6,7 @@
 #include "elem_types.cuh"
 #include "kernels_ops.h"
 #include "route_select.cuh"
+#include "select_parts.cuh"
 
 namespace moe {
 
@@ -17,28 +18,21 @@ __device__ __forceinline__ constexpr int type_of(float) { return MOE_DTYPE_F32; 
 __device__ __forceinline__ constexpr int type_of(__half) { return MOE_DTYPE_F16; }
 __device__ __forceinline__ constexpr int type_of(__nv_bfloat16) { return MOE_DTYPE_BF16; }
 
-// CTAs an SM should hold: groups take registers that a fourth would have to
-// spill (131072 x 256 in 8 groups: 66 us with three, 69 with four; ungrouped
-// the fourth gains 3 to 8 %).
-constexpr int select_ctas(int NE, int MODE) {
-  return NE > 8 ? 1 : MODE >= 0 && (MODE & SELECT_LIMITED) ? 3 : 4;
-}
-
-// RB rows a warp.
-template <int NE, int RB, int MODE>
-__global__ void __launch_bounds__(32 * SELECT_WARPS, select_ctas(NE, MODE))
+// A warp a row.
+template <int NE>
+__global__ void __launch_bounds__(32 * SELECT_WARPS)
     select_kernel(const RouteRule r, const void* __restrict__ logits, int dtype, int64_t stride,
                   const float* __restrict__ bias, int64_t rows, int32_t* __restrict__ ids, float* __restrict__ w) {
-  __shared__ __align__(16) SelectScratch<RB> scratch[SELECT_WARPS];
+  __shared__ __align__(16) SelectScratch scratch[SELECT_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = ((int64_t)blockIdx.x * SELECT_WARPS + warp) * RB;
+  const int64_t t = (int64_t)blockIdx.x * SELECT_WARPS + warp;
   pdl_trigger();
   pdl_wait();
   if (t >= rows) return;
   float b[NE];
   const bool finite = load_bias<NE>(r, bias, lane, b);
-  select_rows<NE, RB, MODE>(r, row_at(logits, dtype, t * stride), dtype, stride, (int)(rows - t < RB ? rows - t : RB),
-                            bias, b, finite, lane, scratch[warp], ids + t * r.K, w + t * r.K);
+  select_row<NE>(r, row_at(logits, dtype, t * stride), dtype, bias, b, finite, lane, scratch[warp], ids + t * r.K,
+                 w + t * r.K);
 }
 
 // Gradient.  A warp takes RB rows at a time, whose slots fit its lanes: first
@@ -174,40 +168,23 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
   }
 }
 
-template <int NE, int RB, int MODE>
+template <int NE>
 cudaError_t launch_select_rows(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
                                int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
-  const int64_t per_cta = SELECT_WARPS * RB;
-  return launch_k(select_kernel<NE, RB, MODE>, dim3((unsigned)((rows + per_cta - 1) / per_cta)),
+  return launch_k(select_kernel<NE>, dim3((unsigned)((rows + SELECT_WARPS - 1) / SELECT_WARPS)),
                   dim3(32 * SELECT_WARPS), 0, s, pdl, r, logits, dtype, stride, bias, rows, ids, w);
 }
 
-// Rows a warp takes together: four (two of up to 16 experts a lane) once that
-// still leaves every scheduler a few warps, by kernels compiled for the kind of
-// rule; one below, where latency counts, by one kernel for all.
-template <int NE, int RB>
-cudaError_t select_n(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
-                     int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
-  if (RB == 1 || rows < 152 * 4 * 4 * RB)
-    return launch_select_rows<NE, 1, SELECT_ANY>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
-  if constexpr (RB > 1) {
-    const int mode = (r.sigmoid ? SELECT_SIGMOID : 0) | (r.by_score ? SELECT_BY_SCORE : 0) |
-                     (r.top_groups < r.groups ? SELECT_LIMITED : 0);
-#define MOE_SELECT_MODE(M) \
-  case M: return launch_select_rows<NE, RB, M>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s)
-    switch (mode) {
-      MOE_SELECT_MODE(0);
-      MOE_SELECT_MODE(1);
-      MOE_SELECT_MODE(2);
-      MOE_SELECT_MODE(3);
-      MOE_SELECT_MODE(4);
-      MOE_SELECT_MODE(5);
-      MOE_SELECT_MODE(6);
-      MOE_SELECT_MODE(7);
-    }
-#undef MOE_SELECT_MODE
-  }
-  return cudaErrorInvalidValue;
+// More parts a row leave more warps, whose loads hide one another's latency,
+// and fewer columns a thread: 65536 x 128 takes 17.4 us with four of 32, 23.9
+// with two of 64 and 36.4 with one of 128; 131072 x 256 in eight groups 69, 71
+// (eight of 32) and 87 (two of 128).
+template <int R, int P>
+cudaError_t launch_select_parts(const RouteRule& r, const void* logits, int dtype, int64_t stride, const float* bias,
+                                int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
+  using L = PartLayout<R, P>;
+  return launch_k(select_parts_kernel<R, P>, dim3((unsigned)((rows + L::ROWS - 1) / L::ROWS)), dim3(32),
+                  L::words(r) * sizeof(float), s, pdl, r, logits, dtype, stride, bias, rows, ids, w);
 }
 
 template <typename T, int NE, int RB, bool SIGMOID>
@@ -264,12 +241,24 @@ cudaError_t launch_select(const RouteRule& rule, const void* logits, int dtype, 
                           int64_t rows, int32_t* ids, float* w, bool pdl, cudaStream_t s) {
   RouteRule r = rule;
   const int bytes = dtype == MOE_DTYPE_F32 ? 4 : 2;
-  set_select_loads(r, stride % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (4 * bytes - 1)) == 0);
+  const bool aligned = stride % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (4 * bytes - 1)) == 0;
+  // Parts of rows once they make five warps an SM, which is where the two
+  // meet (128 experts: 4096 rows 5.2 us against a warp a row's 4.6, 8192 rows
+  // 6.1 against 7.5, 16384 7.5 against 12.3).
+  const int parts = r.E <= 64 ? 2 : 4;
+  if (rows * parts >= 32 * 5 * 152) {
+    r.vec = aligned && r.E % 4 == 0;
+    if (r.E <= 64) return launch_select_parts<1, 2>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+    if (r.E <= 128) return launch_select_parts<1, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+    if (r.E <= 256) return launch_select_parts<2, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+    return launch_select_parts<4, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  }
+  set_select_loads(r, aligned);
   const int n = select_per_lane(r);
-  if (n <= 4) return select_n<4, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
-  if (n <= 8) return select_n<8, 4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
-  if (n <= 16) return select_n<16, 2>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
-  return select_n<32, 1>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if (n <= 4) return launch_select_rows<4>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if (n <= 8) return launch_select_rows<8>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  if (n <= 16) return launch_select_rows<16>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
+  return launch_select_rows<32>(r, logits, dtype, stride, bias, rows, ids, w, pdl, s);
 }
 
 cudaError_t launch_select_backward(const RouteRule& r, const void* logits, int dtype, int64_t stride,

@@ -1,20 +1,17 @@
 // route_select.cuh - the choice of experts of one token by one warp: scores,
-// balance bias, groups, top-k, renormalised weights.  Used by the standalone
-// kernel (kernels_select.cu) and the small-batch front kernel
-// (kernels_route.cu).
+// balance bias, groups, top-k, renormalised weights.  Used by the kernel for
+// small batches (kernels_select.cu), where latency counts, and the fused front
+// of a small forward (kernels_route.cu); larger batches take select_parts.cuh,
+// which gives the same bits.
 //
-// A row of 256 experts and 8 slots costs a few hundred instructions a warp
-// while its bytes take the memory system far less, so what bounds the choice
-// is instructions.  The usual row takes this path, several rows of a warp
-// together:
+// Instructions bound it, a chain of some hundreds:
 //  - scores by the hardware's exponential and reciprocal;
-//  - the two best of each lane (three where groups leave fewer lanes) and, with
-//    groups, the two best of each group, by min and max;
+//  - the three best of each lane and, with groups, the two best of each group,
+//    by min and max;
 //  - K rounds of a maximum over the lanes' heads, each lane moving on to its
 //    next best.  If exactly K experts reach the last maximum, no two lanes
-//    tied and none held one more: the rounds are the slots;
-//  - the slots of all rows, one a lane: their scores at full accuracy, and the
-//    weights.
+//    tied and none held one more: the rounds are the slots, whose scores are
+//    then taken at full accuracy.
 // Comparisons, selections and logic take two issue slots a warp, additions and
 // fused multiply-adds one: counts, ranks and the places of a lane's best are
 // therefore sums of reaches(), not bit masks.
@@ -49,6 +46,39 @@ __device__ __forceinline__ float max_lanes(float v) {
 }
 
 __device__ __forceinline__ float sigmoid_ieee(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// exp(x) and 1 / (1 + exp(-x)) for the choice: relative errors of a few
+// 2^-24 and absolute ones under 2e-7.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp_fast(-x)));
+  return y;
+}
+
+// A sum of up to 512 values of [0, 1] that does not depend on their order, so
+// that a row's weights do not depend on how many rows a call has: each value
+// is split into a multiple of 2^-14 and one of 2^-29 (what is left, under
+// 2^-30, is dropped), whose sums are exact in FP32.
+struct OrderFree {
+  float2 high = {0.0f, 0.0f}, low = {0.0f, 0.0f};
+  __device__ __forceinline__ void add(float2 e) {
+    const float2 h = add2(add2(e, both(768.0f)), both(-768.0f));
+    const float2 rest = fma2(h, both(-1.0f), e);
+    high = add2(high, h);
+    low = add2(low, add2(add2(rest, both(0.0234375f)), both(-0.0234375f)));
+  }
+  // of the warp's lanes
+  __device__ __forceinline__ float over_warp() const {
+    const int h = __reduce_add_sync(0xffffffffu, __float2int_rn((high.x + high.y) * 16384.0f));
+    const int l = __reduce_add_sync(0xffffffffu, __float2int_rn((low.x + low.y) * 536870912.0f));
+    return fmaf((float)l, 1.0f / 536870912.0f, (float)h * (1.0f / 16384.0f));
+  }
+};
 
 // The place of local slot i of this lane in its group, and its expert or -1.
 __device__ __forceinline__ int select_place(const RouteRule& r, int lane, int i) {
@@ -94,22 +124,23 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
     // The sum cancels from renormalised weights (the best logit is among the
     // chosen, so their sum is far above the 1e-20).
     if (r.by_score || !r.renormalize) {
-      total = 0.0f;
+      OrderFree sum;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) total += expf(raw[i] - m);
-      total = sum_lanes(total);
+      for (int i = 0; i < NE; i += 2) sum.add(make_float2(exp_fast(raw[i] - m), exp_fast(raw[i + 1] - m)));
+      total = sum.over_warp();
       if (total == 0.0f) total = 1.0f;
     }
   }
   // what the choice compares; -inf: closed
+  const float k = 1.0f / total;
   float v[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     v[i] = raw[i];
     if (r.by_score && raw[i] != -INFINITY) {
-      const float s = r.sigmoid ? sigmoid_ieee(raw[i]) : expf(raw[i] - m) / total;
       const int e = select_expert(r, lane, i);
-      v[i] = s + (bias && e >= 0 ? __ldg(bias + e) : 0.0f);
+      const float b = bias && e >= 0 ? __ldg(bias + e) : 0.0f;
+      v[i] = r.sigmoid ? sigmoid_fast(raw[i]) + b : fmaf(exp_fast(raw[i] - m), k, b);
       if (!(v[i] > -INFINITY)) v[i] = -INFINITY;  // (NaN too)
     }
   }
@@ -130,8 +161,8 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
     if (r.top2 && b1 > -INFINITY) {
       // (of a softmax, what its sum would divide)
       if (!r.by_score) {
-        b1 = r.sigmoid ? sigmoid_ieee(b1) : expf(b1 - m);
-        b2 = r.sigmoid ? sigmoid_ieee(b2) : expf(b2 - m);
+        b1 = r.sigmoid ? sigmoid_fast(b1) : exp_fast(b1 - m);
+        b2 = r.sigmoid ? sigmoid_fast(b2) : exp_fast(b2 - m);
       }
       gs = b2 > -INFINITY ? b1 + b2 : b1;
     }
@@ -180,29 +211,13 @@ __device__ __noinline__ void select_by_rounds(const RouteRule& r, const void* ro
 }
 
 
-// Scratch of one warp for RB rows.
-template <int RB>
+// Shared memory of a warp's row.
 struct alignas(16) SelectScratch {  // (read 16 bytes at a time)
-  int slot_e[RB][32];              // of the slots: lane << 5 | place, or a ranked row's experts
-  float slot_s[32];                // a ranked row's scores
-  uint32_t key[32];                // a ranked row's candidates: what they are compared by
-  int e[32];                       // and their experts
-  uint32_t reach[RB][32];          // each lane's experts that reach a row's bound
-  float top[RB], total[RB];        // softmax: the largest logit, the sum
+  uint32_t key[32];  // candidates: what they are compared by
+  int e[32];         // and their experts
+  int slot_e[32];    // the slots' experts
+  float slot_s[32];  // and scores
 };
-
-// exp(x) and 1 / (1 + exp(-x)) for the choice: relative errors of a few
-// 2^-24 and absolute ones under 2e-7.
-__device__ __forceinline__ float exp_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp_fast(-x)));
-  return y;
-}
 
 // The largest over the warp.
 __device__ __forceinline__ float warp_top(float v) {
@@ -225,32 +240,6 @@ __device__ __forceinline__ int whole(float v) { return __float_as_int(v + 838860
 __device__ __forceinline__ void merge2(float& b1, float& b2, float c1, float c2) {
   b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
   b1 = fmaxf(b1, c1);
-}
-
-// The sum over the warp of one value a row; lane l gets row
-// row_of_lane(l % 4 or 2)'s.  Each step hands half of the rows to the other
-// half of the lanes; the order of additions is the same for every RB.
-template <int RB>
-__device__ __forceinline__ constexpr int row_of_lane(int l) {
-  return RB == 4 ? 2 * (l & 1) + (l >> 1 & 1) : RB == 2 ? l & 1 : 0;
-}
-template <int RB>
-__device__ __forceinline__ float sum_rows(const float (&v)[RB], int lane) {
-  constexpr unsigned all = 0xffffffffu;
-  const bool odd = lane & 1, high = lane & 2;
-  float mine;
-  if constexpr (RB == 4) {
-    const float a = (odd ? v[2] : v[0]) + __shfl_xor_sync(all, odd ? v[0] : v[2], 1);
-    const float b = (odd ? v[3] : v[1]) + __shfl_xor_sync(all, odd ? v[1] : v[3], 1);
-    mine = (high ? b : a) + __shfl_xor_sync(all, high ? a : b, 2);
-  } else {
-    if constexpr (RB == 2) mine = (odd ? v[1] : v[0]) + __shfl_xor_sync(all, odd ? v[0] : v[1], 1);
-    else mine = v[0] + __shfl_xor_sync(all, v[0], 1);
-    mine += __shfl_xor_sync(all, mine, 2);
-  }
-#pragma unroll
-  for (int o = 16; o > 2; o >>= 1) mine += __shfl_xor_sync(all, mine, o);
-  return mine;
 }
 
 // The logits of this lane's experts, -inf where it has none.
@@ -287,22 +276,21 @@ __device__ __forceinline__ void load_logits(const RouteRule& r, const void* row,
   }
 }
 
-// The two or three best (DEPTH) of NE values, each as often as it occurs, by
-// merging sorted runs: the k-th of two runs is the largest min(a_i, b_j) with
-// i + j = k, a_0 and b_0 taken as infinite.
-template <int NE, int DEPTH>
-__device__ __forceinline__ void lane_best(const float (&v)[NE], float (&b)[DEPTH]) {
+// The three best of NE values, each as often as it occurs, by merging sorted
+// runs: the k-th of two runs is the largest min(a_i, b_j) with i + j = k, a_0
+// and b_0 taken as infinite.
+template <int NE>
+__device__ __forceinline__ void lane_best(const float (&v)[NE], float (&b)[3]) {
 #pragma unroll
   for (int i = 0; i < NE; i += 4) {
     const float p1 = fmaxf(v[i], v[i + 1]), p2 = fminf(v[i], v[i + 1]);
     const float q1 = fmaxf(v[i + 2], v[i + 3]), q2 = fminf(v[i + 2], v[i + 3]);
     const float c1 = fmaxf(p1, q1), c2 = fmaxf(fmaxf(p2, q2), fminf(p1, q1));
-    const float c3 = DEPTH > 2 ? fmaxf(fminf(p1, q2), fminf(p2, q1)) : 0.0f;
+    const float c3 = fmaxf(fminf(p1, q2), fminf(p2, q1));
     if (i == 0) {
-      b[0] = c1, b[1] = c2;
-      if constexpr (DEPTH > 2) b[2] = c3;
+      b[0] = c1, b[1] = c2, b[2] = c3;
     } else {
-      if constexpr (DEPTH > 2) b[2] = fmaxf(fmaxf(fmaxf(b[2], c3), fminf(b[0], c2)), fminf(b[1], c1));
+      b[2] = fmaxf(fmaxf(fmaxf(b[2], c3), fminf(b[0], c2)), fminf(b[1], c1));
       b[1] = fmaxf(fmaxf(b[1], c2), fminf(b[0], c1));
       b[0] = fmaxf(b[0], c1);
     }
@@ -322,281 +310,191 @@ __device__ __forceinline__ bool load_bias(const RouteRule& r, const float* bias,
   return __all_sync(0xffffffffu, x < INFINITY);
 }
 
-// What a kernel is compiled for: the score, what the choice compares, and
-// whether groups limit it; SELECT_ANY asks the rule.
-constexpr int SELECT_SIGMOID = 1, SELECT_BY_SCORE = 2, SELECT_LIMITED = 4, SELECT_ANY = -1;
-
-// The choice for `valid` <= RB rows by one warp.  Row q's logits start
-// q * stride elements on, its ids and weights go to ids / w + q * K.
-template <int NE, int RB, int MODE>
-__device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows, int dtype, int64_t stride, int valid,
-                                            const float* bias, const float (&b)[NE], bool bias_finite, int lane,
-                                            SelectScratch<RB>& sm, int32_t* ids, float* w) {
-  static_assert(RB == 1 || RB == 2 || RB == 4, "rows in pairs");
+// The choice for one row by one warp, for its latency.  b: the balance bias
+// of this lane's experts.
+template <int NE>
+__device__ __forceinline__ void select_row(const RouteRule& r, const void* row, int dtype, const float* bias,
+                                           const float (&b)[NE], bool bias_finite, int lane, SelectScratch& sm,
+                                           int32_t* ids, float* w) {
   constexpr unsigned all = 0xffffffffu;
-  const bool sigmoid = MODE < 0 ? r.sigmoid != 0 : (MODE & SELECT_SIGMOID) != 0;
-  const bool by_score = MODE < 0 ? r.by_score != 0 : (MODE & SELECT_BY_SCORE) != 0;
-  const bool limited = MODE < 0 ? r.top_groups < r.groups : (MODE & SELECT_LIMITED) != 0;
+  const bool sigmoid = r.sigmoid, by_score = r.by_score, limited = r.top_groups < r.groups;
   const bool need_total = !sigmoid && (by_score || !r.renormalize);
   const int lanes = 1 << r.lane_shift, g = lane >> r.lane_shift;
-  unsigned odd = bias_finite ? 0u : (1u << valid) - 1u;  // rows for select_by_rounds
 
-  float v[RB][NE];
+  float v[NE];
+  load_logits<NE>(r, row, dtype, lane, v);
+  // A finite sum means finite logits.  Otherwise some are closed (fine), or
+  // NaN or +inf, which select_by_rounds sorts out.
+  bool odd = !bias_finite;  // for select_by_rounds
+  float2 x = make_float2(v[0], v[1]);
 #pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    if (q < valid) {
-      load_logits<NE>(r, row_at(rows, dtype, q * stride), dtype, lane, v[q]);
-    } else {
+  for (int i = 2; i < NE; i += 2) x = add2(x, make_float2(v[i], v[i + 1]));
+  const bool closed = __any_sync(all, !(fabsf(x.x + x.y) < INFINITY));
+  if (closed) {
+    bool bad = false;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) v[q][i] = -INFINITY;
-    }
+    for (int i = 0; i < NE; ++i) bad |= !(v[i] < INFINITY);
+    odd |= __any_sync(all, bad) != 0;
   }
-  // this lane's best, and its group's score
-  constexpr int DEPTH = MODE < 0 || (MODE & SELECT_LIMITED) ? 3 : 2;
-  float best[RB][DEPTH], group[RB], part[RB], top[RB];
-  auto without_id = [&](float f) {
-    return dtype == MOE_DTYPE_F32 ? f : __uint_as_float(__float_as_uint(f) & ~0x1fffu);
-  };
+  float top = 0.0f, total = 1.0f, k = 1.0f;
+  if (sigmoid && by_score) {
 #pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    // A finite sum means finite logits.  Otherwise some are closed (fine), or
-    // NaN or +inf, which select_by_rounds sorts out.
-    float2 x = make_float2(v[q][0], v[q][1]);
-#pragma unroll
-    for (int i = 2; i < NE; i += 2) x = add2(x, make_float2(v[q][i], v[q][i + 1]));
-    const bool closed = __any_sync(all, !(fabsf(x.x + x.y) < INFINITY));
-    if (closed) {
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) bad |= !(v[q][i] < INFINITY);
-      if (__any_sync(all, bad)) odd |= 1u << q;
-    }
-    part[q] = top[q] = 0.0f;
-    if (sigmoid ? by_score : need_total) {
-      if (!sigmoid) {
-        float m = v[q][0];
-#pragma unroll
-        for (int i = 1; i < NE; ++i) m = fmaxf(m, v[q][i]);
-        m = warp_top(m);
-        top[q] = m == -INFINITY ? 0.0f : m;
-      }
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const float s = sigmoid ? sigmoid_fast(v[q][i]) + b[i] : exp_fast(v[q][i] - top[q]);
-        part[q] += s;
-        if (by_score && (!closed || v[q][i] != -INFINITY)) v[q][i] = s;
-      }
+    for (int i = 0; i < NE; ++i) {
+      const float s = sigmoid_fast(v[i]) + b[i];
+      if (!closed || v[i] != -INFINITY) v[i] = s;
     }
   }
   if (need_total) {
-    // sums over the experts; a lane goes on with one of the rows
-    float total = sum_rows<RB>(part, lane);
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) m = fmaxf(m, v[i]);
+    m = warp_top(m);
+    top = m == -INFINITY ? 0.0f : m;
+    OrderFree sum;
+#pragma unroll
+    for (int i = 0; i < NE; i += 2) {
+      const float2 e = make_float2(exp_fast(v[i] - top), exp_fast(v[i + 1] - top));
+      sum.add(e);
+      if (by_score && (!closed || v[i] != -INFINITY)) v[i] = e.x;
+      if (by_score && (!closed || v[i + 1] != -INFINITY)) v[i + 1] = e.y;
+    }
+    total = sum.over_warp();
     if (total == 0.0f) total = 1.0f;
-    if (lane < RB) sm.total[row_of_lane<RB>(lane)] = total;
     if (by_score) {
+      k = 1.0f / total;
 #pragma unroll
-      for (int q = 0; q < RB; ++q) {
-        const float k = 1.0f / __shfl_sync(all, total, row_of_lane<RB>(q));  // (its own inverse)
-#pragma unroll
-        for (int i = 0; i < NE; ++i) v[q][i] = fmaf(v[q][i], k, b[i]);  // (-inf stays)
-      }
-    }
-  } else if (!sigmoid && lane < RB) {
-    // The sum cancels from renormalised weights (the best logit is among the
-    // chosen, so their sum is far above the 1e-20).
-    sm.total[lane] = 1.0f;
-  }
-#pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    if (!by_score && dtype != MOE_DTYPE_F32) {
-      // Equal logits are common in 16 bits.  Their FP32 values end in 13 zero
-      // bits or more: the expert's id there makes each its own, the lower id
-      // the larger value.
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const float f = v[q][i] + 0.0f;  // (-0 to +0)
-        const unsigned id = g * r.size + select_place(r, lane, i);
-        const unsigned bits = __float_as_uint(f) | (f < 0.0f ? id : id ^ 511u);
-        if (f > -INFINITY) v[q][i] = __uint_as_float(bits);
-      }
-    }
-    lane_best<NE, DEPTH>(v[q], best[q]);
-    if (!sigmoid && !need_total) {
-      const float m = without_id(warp_top(best[q][0]));
-      top[q] = m == -INFINITY ? 0.0f : m;
-    }
-    if (!sigmoid && lane == 0) sm.top[q] = top[q];
-    if (limited) {
-      float b1 = best[q][0], b2 = best[q][1];
-#pragma unroll
-      for (int s = 0; s < 5; ++s)
-        if (s < r.lane_shift) merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
-      group[q] = b1;
-      if (r.top2) {
-        if (!by_score) {
-          b1 = without_id(b1), b2 = without_id(b2);
-          // (of a softmax, what its sum would divide)
-          const float s1 = sigmoid ? sigmoid_fast(b1) : exp_fast(b1 - top[q]);
-          const float s2 = sigmoid ? sigmoid_fast(b2) : exp_fast(b2 - top[q]);
-          group[q] = b1 > -INFINITY ? s1 + s2 : -INFINITY;
-        } else if (b2 > -INFINITY) {
-          group[q] = b1 + b2;
-        }
-      }
+      for (int i = 0; i < NE; ++i) v[i] = fmaf(v[i], k, b[i]);  // (-inf stays)
     }
   }
-  // Which groups each row keeps.  A group's score is in all its lanes: lane d
-  // of a group ranks the groups of row d, all rows at once.  (Every lane takes
-  // part, also those of groups past the last one, whose score of -inf at a
-  // higher index outranks none.)
-  unsigned kept = all;  // bit of lane (group's first + d): row d keeps the group
-  const bool together = lanes >= RB;
-  auto rank_of = [&](float mine) {
+  if (!by_score && dtype != MOE_DTYPE_F32) {
+    // Equal logits are common in 16 bits.  Their FP32 values end in 13 zero
+    // bits or more: the expert's id there makes each its own, the lower id
+    // the larger value.
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float f = v[i] + 0.0f;  // (-0 to +0)
+      const unsigned id = g * r.size + select_place(r, lane, i);
+      const unsigned bits = __float_as_uint(f) | (f < 0.0f ? id : id ^ 511u);
+      if (f > -INFINITY) v[i] = __uint_as_float(bits);
+    }
+  }
+  auto without_id = [&](float f) {
+    return dtype == MOE_DTYPE_F32 ? f : __uint_as_float(__float_as_uint(f) & ~0x1fffu);
+  };
+  // this lane's best three, and its group's score
+  float best[3];
+  lane_best<NE>(v, best);
+  if (!sigmoid && !need_total) {
+    // (The sum cancels from renormalised weights: the best logit is among the
+    // chosen, so their sum is far above the 1e-20.)
+    const float m = without_id(warp_top(best[0]));
+    top = m == -INFINITY ? 0.0f : m;
+  }
+  bool keep = g < r.groups;
+  float group = INFINITY;
+  if (limited) {
+    float b1 = best[0], b2 = best[1];
+#pragma unroll
+    for (int s = 0; s < 5; ++s)
+      if (s < r.lane_shift) merge2(b1, b2, __shfl_xor_sync(all, b1, 1 << s), __shfl_xor_sync(all, b2, 1 << s));
+    group = b1;
+    if (r.top2) {
+      if (!by_score) {
+        b1 = without_id(b1), b2 = without_id(b2);
+        // (of a softmax, what its sum would divide)
+        const float s1 = sigmoid ? sigmoid_fast(b1) : exp_fast(b1 - top);
+        const float s2 = sigmoid ? sigmoid_fast(b2) : exp_fast(b2 - top);
+        group = b1 > -INFINITY ? s1 + s2 : -INFINITY;
+      } else if (b2 > -INFINITY) {
+        group = b1 + b2;
+      }
+    }
+    // Its rank.  (Every lane takes part, also those of groups past the last
+    // one, whose score of -inf at a higher index outranks none.)
     float rank = 0.0f;
     const int others = 32 >> r.lane_shift;
 #pragma unroll
-    for (int k = 1; k < 32; ++k) {
-      if (k >= others) break;
+    for (int j = 1; j < 32; ++j) {
+      if (j >= others) break;
       // (an equal score at a lower index outranks; of groups without an open
       // expert it does not matter which are kept)
-      rank += reaches(__shfl_xor_sync(all, mine, k << r.lane_shift), mine, (g ^ k) < g ? 1.0f : 0.0f);
+      rank += reaches(__shfl_xor_sync(all, group, j << r.lane_shift), group, (g ^ j) < g ? 1.0f : 0.0f);
     }
-    return rank;
-  };
-  const float top_groups = (float)r.top_groups;
-  if (limited && together) {
-    float mine = group[0];
-#pragma unroll
-    for (int q = 1; q < RB; ++q) mine = (lane & (RB - 1)) == q ? group[q] : mine;
-    const float rank = rank_of(mine);
-    kept = __ballot_sync(all, g < r.groups && rank < top_groups);
+    keep = keep && rank < (float)r.top_groups;
   }
-  // K rounds for all rows at once.  pops: the rounds this lane's best won, k
-  // (from 1) as digits of base 64, the best's highest.
-  float head[RB][DEPTH], low[RB];
-  unsigned pops[RB];
-  unsigned mine = 0;  // rows that keep this lane's group
-#pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    bool keep = g < r.groups;
-    if (limited) {
-      if (together) {
-        keep = kept >> ((lane & ~(lanes - 1)) + q) & 1;
-      } else {
-        const float rank = rank_of(group[q]);
-        keep = keep && rank < top_groups;
-      }
-    }
-    mine |= (unsigned)keep << q;
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) head[q][d] = keep ? best[q][d] : -INFINITY;
-    pops[q] = 0;
-    low[q] = -INFINITY;
-  }
+  // K rounds.  pops: the rounds this lane's best won, as digits of base 64
+  // (from 1), the best's highest.
+  float h0 = keep ? best[0] : -INFINITY, h1 = keep ? best[1] : -INFINITY, h2 = keep ? best[2] : -INFINITY;
+  float low = -INFINITY;
+  unsigned pops = 0;
 #pragma unroll 1
-  for (int k = 1; k <= r.K; ++k) {
-#pragma unroll
-    for (int q = 0; q < RB; ++q) {
-      low[q] = warp_top(head[q][0]);
-      if (head[q][0] == low[q]) {
-        pops[q] = pops[q] * 64 + k;
-#pragma unroll
-        for (int d = 0; d + 1 < DEPTH; ++d) head[q][d] = head[q][d + 1];
-        head[q][DEPTH - 1] = -INFINITY;
-      }
+  for (int j = 1; j <= r.K; ++j) {
+    low = warp_top(h0);
+    if (h0 == low) {
+      pops = pops * 64 + j;
+      h0 = h1, h1 = h2, h2 = -INFINITY;
     }
   }
-  unsigned ranked = 0;  // rows whose candidates are to be ranked
+  // How many of this lane's reach the last maximum (every open expert of the
+  // kept groups where the heads ran out), the sum of their places, and the
+  // place of its best.
+  const float bound = keep ? fmaxf(low, -3.402823466e38f) : INFINITY;
+  float both_sums = 0.0f, first = 0.0f;
 #pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    // How many of this lane's reach the last maximum (every open expert of the
-    // kept groups where the heads ran out), the sum of their places, and the
-    // place of its best.
-    const bool keep = mine >> q & 1;
-    const float bound = keep ? fmaxf(low[q], -3.402823466e38f) : INFINITY;
-    float both_sums = 0.0f, first = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      both_sums = fmaf(reaches(v[q][i], bound), (float)(1 + 64 * i), both_sums);
-      first = fmaf(reaches(v[q][i], best[q][0]), (float)i, first);
-    }
-    const int count = whole(both_sums) & 63, places = whole(both_sums) >> 6;
-    const int n = __reduce_add_sync(all, count);
-    if (n < r.K || n > 32) odd |= 1u << q;
-    // Settled if the last maximum is an open expert's and K experts reach it:
-    // each is one of its lane's best and won a round of its own.  Their places
-    // follow from the sums, if no two of a lane's are equal.
-    const bool twice = (best[q][1] >= bound && best[q][0] == best[q][1]) ||
-                       (DEPTH > 2 && best[q][DEPTH - 1] >= bound && best[q][1] == best[q][DEPTH - 1]);
-    float least = fminf(fabsf(bound), limited ? fabsf(group[q]) : INFINITY);
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) least = fminf(least, fabsf(best[q][d]));
-    const bool unsafe = least < TINY;
-    bool settles = n == r.K && low[q] > -INFINITY;
-    if (__any_sync(all, twice || unsafe)) {
-      settles = false;
-      if (__any_sync(all, unsafe)) odd |= 1u << q;
-    }
-    if (q >= valid || (odd >> q & 1)) continue;
-    if (settles) {
-      // slots hold lane and place; the best won the first of the lane's rounds
-      const int here = lane << 5, best_at = whole(first);
-      if (count > 0) sm.slot_e[q][(pops[q] >> 6 * (count - 1)) - 1] = here + best_at;
-      if (count == 2) sm.slot_e[q][(pops[q] & 63) - 1] = here + places - best_at;
-      if (DEPTH > 2 && __any_sync(all, count > 2)) {
-        float second = 0.0f;  // places of the two best
-#pragma unroll
-        for (int i = 0; i < NE; ++i) second = fmaf(reaches(v[q][i], best[q][1]), (float)i, second);
-        if (count > 2) {
-          sm.slot_e[q][(pops[q] >> 6 & 63) - 1] = here + whole(second) - best_at;
-          sm.slot_e[q][(pops[q] & 63) - 1] = here + places - whole(second);
-        }
-      }
-    } else {
-      ranked |= 1u << q;
-      unsigned reach = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) reach |= v[q][i] >= bound ? 1u << i : 0u;
-      sm.reach[q][lane] = reach;
-    }
+  for (int i = 0; i < NE; ++i) {
+    both_sums = fmaf(reaches(v[i], bound), (float)(1 + 64 * i), both_sums);
+    first = fmaf(reaches(v[i], best[0]), (float)i, first);
   }
-  const unsigned rows_here = (1u << valid) - 1u;
-  odd &= rows_here;
-  __syncwarp();
-  // the slots of the rows that the rounds settled
-  const unsigned settled = rows_here & ~odd & ~ranked;
-  const int slots = 1 << r.slot_shift, at_once = 32 >> r.slot_shift;
-  if (settled) {
-#pragma unroll 1
-    for (int q0 = 0; q0 < RB; q0 += at_once) {
-      const int q = q0 + (lane >> r.slot_shift), c = lane & (slots - 1);
-      const bool slot = q < RB && (settled >> q & 1) && c < r.K;
-      float s = 0.0f;
-      int e = 0;
-      if (slot) {
-        const int x = sm.slot_e[q][c];  // lane and place
-        e = (x >> 5 >> r.lane_shift) * r.size + select_place(r, x >> 5, x & 31);
-        const float l = logit_at(row_at(rows, dtype, q * stride), dtype, e);
-        s = sigmoid ? sigmoid_ieee(l) : expf(l - sm.top[q]) / sm.total[q];
-      }
-      if (r.renormalize) {
-        float sum = s;
-#pragma unroll 1
-        for (int o = slots >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
-        s = s / (sum + SELECT_SUM_EPS);
-      }
-      if (slot) {
-        ids[q * r.K + c] = e;
-        w[q * r.K + c] = s * r.scale;
+  const int count = whole(both_sums) & 63, places = whole(both_sums) >> 6;
+  int n = __reduce_add_sync(all, count);
+  // Settled if the last maximum is an open expert's and K experts reach it:
+  // each is one of its lane's best and won a round of its own.  Their places
+  // follow from the sums, if no two of a lane's are equal.
+  const bool twice = (best[1] >= bound && best[0] == best[1]) || (best[2] >= bound && best[1] == best[2]);
+  float least = fminf(fabsf(bound), fabsf(group));
+  least = fminf(fminf(least, fabsf(best[0])), fminf(fabsf(best[1]), fabsf(best[2])));
+  const bool tied = __any_sync(all, twice);
+  odd |= __any_sync(all, least < TINY) || n < r.K || n > 32;
+  if (odd) {
+    float raw[NE];
+    load_logits<NE>(r, row, dtype, lane, raw);
+    int e;
+    float wj;
+    select_by_rounds<NE>(r, row, dtype, bias, lane, raw, e, wj);
+    if (lane < r.K) {
+      ids[lane] = e;
+      w[lane] = wj;
+    }
+    return;
+  }
+  auto score_of = [&](float l) { return sigmoid ? sigmoid_ieee(l) : expf(l - top) / total; };
+  int e = 0;
+  float s = 0.0f;
+  if (n == r.K && low > -INFINITY && !tied) {
+    // slots hold experts; the best won the first of the lane's rounds
+    const int best_at = whole(first);
+    auto expert = [&](int place) { return g * r.size + select_place(r, lane, place); };
+    if (count > 0) sm.slot_e[(pops >> 6 * (count - 1)) - 1] = expert(best_at);
+    if (count == 2) sm.slot_e[(pops & 63) - 1] = expert(places - best_at);
+    if (__any_sync(all, count > 2)) {
+      float second = 0.0f;  // places of the two best
+#pragma unroll
+      for (int i = 0; i < NE; ++i) second = fmaf(reaches(v[i], best[1]), (float)i, second);
+      if (count > 2) {
+        sm.slot_e[(pops >> 6 & 63) - 1] = expert(whole(second) - best_at);
+        sm.slot_e[(pops & 63) - 1] = expert(places - whole(second));
       }
     }
-  }
-  // rows with ties or a lane with three: the candidates, one a lane
-  while (ranked) {
-    const int q = __ffs(ranked) - 1;
-    ranked &= ranked - 1;
-    const void* row = row_at(rows, dtype, q * stride);
-    unsigned reach = sm.reach[q][lane];
+    __syncwarp();
+    if (lane < r.K) {
+      e = sm.slot_e[lane];
+      s = score_of(logit_at(row, dtype, e));
+    }
+  } else {
+    // ties, or a lane with more: the candidates, one a lane
+    unsigned reach = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) reach |= v[i] >= bound ? 1u << i : 0u;
     int upto = __popc(reach);
     int at = -upto;
 #pragma unroll
@@ -604,7 +502,7 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
       const int t = __shfl_up_sync(all, upto, o);
       if (lane >= o) upto += t;
     }
-    const int n = __shfl_sync(all, upto, 31);
+    n = __shfl_sync(all, upto, 31);
     at += upto;
     while (reach) {
       const int i = __ffs(reach) - 1;
@@ -615,13 +513,16 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
     // they compare as (value, lower id first)
     float score = 0.0f;
     uint32_t key = 0;
-    int e = 0;
+    int mine = 0;
     if (lane < n) {
-      e = sm.e[lane];
-      const float l = logit_at(row, dtype, e);
+      mine = sm.e[lane];
+      const float l = logit_at(row, dtype, mine);
       float value = l;
-      score = sigmoid ? sigmoid_ieee(l) : expf(l - sm.top[q]) / sm.total[q];
-      if (by_score) value = score + (bias ? __ldg(bias + e) : 0.0f);
+      score = score_of(l);
+      if (by_score) {
+        const float bb = bias ? __ldg(bias + mine) : 0.0f;
+        value = sigmoid ? sigmoid_fast(l) + bb : fmaf(exp_fast(l - top), k, bb);
+      }
       key = order_bits(value);
     }
     sm.key[lane] = key;
@@ -631,38 +532,25 @@ __device__ __forceinline__ void select_rows(const RouteRule& r, const void* rows
     for (int j = 0; j < n; j += 4) {
       const uint4 o = *reinterpret_cast<const uint4*>(&sm.key[j]);
       const int4 oe = *reinterpret_cast<const int4*>(&sm.e[j]);
-      rank += o.x > key || (o.x == key && oe.x < e);
-      rank += o.y > key || (o.y == key && oe.y < e);
-      rank += o.z > key || (o.z == key && oe.z < e);
-      rank += o.w > key || (o.w == key && oe.w < e);
+      rank += o.x > key || (o.x == key && oe.x < mine);
+      rank += o.y > key || (o.y == key && oe.y < mine);
+      rank += o.z > key || (o.z == key && oe.z < mine);
+      rank += o.w > key || (o.w == key && oe.w < mine);
     }
     if (lane < n && rank < r.K) {
       sm.slot_s[rank] = score;
-      sm.slot_e[q][rank] = e;
+      sm.slot_e[rank] = mine;
     }
     __syncwarp();
-    float s = lane < r.K ? sm.slot_s[lane] : 0.0f;
-    if (r.renormalize) s = s / (sum_lanes(s) + SELECT_SUM_EPS);
     if (lane < r.K) {
-      ids[q * r.K + lane] = sm.slot_e[q][lane];
-      w[q * r.K + lane] = s * r.scale;
+      e = sm.slot_e[lane];
+      s = sm.slot_s[lane];
     }
-    __syncwarp();
   }
-  // the rows left over
-  while (odd) {
-    const int q = __ffs(odd) - 1;
-    odd &= odd - 1;
-    const void* row = row_at(rows, dtype, q * stride);
-    float raw[NE];
-    load_logits<NE>(r, row, dtype, lane, raw);
-    int e;
-    float wj;
-    select_by_rounds<NE>(r, row, dtype, bias, lane, raw, e, wj);
-    if (lane < r.K) {
-      ids[q * r.K + lane] = e;
-      w[q * r.K + lane] = wj;
-    }
+  if (r.renormalize) s = s / (sum_lanes(s) + SELECT_SUM_EPS);
+  if (lane < r.K) {
+    ids[lane] = e;
+    w[lane] = s * r.scale;
   }
   __syncwarp();
 }
