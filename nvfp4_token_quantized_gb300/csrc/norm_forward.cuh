@@ -8,7 +8,11 @@
 // in FP32.
 //
 // Bytes bound it: y, r, r' and h move once, a row stays on the SM between its
-// two sums.
+// two sums.  Rows arrive two ahead of the arithmetic by asynchronous copies, each
+// thread its own pieces (no barrier), and their sums take one barrier each.
+// 16384 x 8192 bf16: 165 us, 6.5 TB/s (one row a CTA of 1024 threads: 407); 4096
+// x 2048 with an FP32 residual and a gate by channel: 21 us, 4.8 TB/s; a single
+// row of 2048: 2.4 us, a launch and two sums.
 #pragma once
 
 #include "norm_common.cuh"
