@@ -382,3 +382,40 @@ def test_many_rows_equal_few_rows(E, G, top, K):
                 dl = r.select_backward(l, ids, w, dw)
                 d2 = r.select_backward(l[5003:5903], ids[5003:5903], w[5003:5903], dw[5003:5903])
                 assert torch.equal(dl[5003:5903], d2)
+
+
+@pytest.mark.parametrize("E,G,top,K,pad", [(1, 1, 1, 1, 0), (6, 3, 2, 2, 0), (16, 16, 5, 1, 0), (32, 1, 1, 32, 0),
+                                           (33, 1, 1, 4, 3), (60, 5, 4, 10, 3), (64, 8, 3, 6, 0), (120, 4, 2, 3, 8),
+                                           (129, 3, 1, 32, 0), (328, 8, 4, 12, 0), (481, 13, 2, 9, 1),
+                                           (512, 32, 7, 16, 0)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_large_batches_with_odd_rows_equal_few_rows(E, G, top, K, pad, score):
+    # few open experts, rows without weights and equal values among many rows
+    T = 12307
+    b = _bias(E)
+    if E > 40:
+        b[3], b[5], b[7] = float("inf"), float("nan"), -float("inf")
+    for dtype in (torch.float32, torch.float16):
+        l = _logits(T, E, dtype, closed=0.6, pad=pad)
+        l[1::11] = (l[1::11] * 2).round() / 2
+        l[3::97, E // 2] = float("nan")
+        l[5::89, E - 1] = float("inf")
+        for renormalize in (True, False):
+            for group_score in ("max", "top2"):
+                r = _router(E, K, score=score, num_groups=G, top_groups=top, group_score=group_score,
+                            renormalize=renormalize, scale=0.5)
+                for bias in (None, _bias(E), b):
+                    ids, w = r.select(l, bias=bias)
+                    for lo in (0, 4001, T - 700):
+                        i2, w2 = r.select(l[lo:lo + 700], bias=bias)
+                        assert torch.equal(ids[lo:lo + 700], i2)
+                        assert torch.equal(w[lo:lo + 700].view(torch.int32), w2.view(torch.int32))
+
+
+@pytest.mark.parametrize("E,G,top", [(24, 1, 1), (100, 1, 1), (100, 5, 2), (256, 1, 1)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_large_batches(E, G, top, biased):
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            _check(12200, E, 5, biased=biased, closed=0.1, pad=1, score=score, num_groups=G, top_groups=top,
+                   group_score="top2", renormalize=renormalize)
