@@ -518,7 +518,8 @@ MOE_API moe_status moe_block_norm(const moe_norm_config* cfg, const moe_norm_io*
  * a channel gate) and FP32 dpost_weight, dpre_weight [H].
  * dpost_weight, dpre_weight and dgate may be NULL.  Without `branch`,
  * residual_out is r, dy is not written, and dresidual = dresidual_out + the
- * pre-norm's part. */
+ * pre-norm's part.  y itself is only read for a post-norm or a gate's
+ * gradient. */
 typedef struct {
   const void *dresidual_out, *dh, *residual_out, *y, *gate, *post_weight, *pre_weight;
   void *dresidual, *dy, *dgate;

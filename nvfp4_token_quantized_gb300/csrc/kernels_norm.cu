@@ -38,10 +38,10 @@ cudaError_t with_types(const moe_norm_config& c, F&& f) {
   return wide ? f(__nv_bfloat16(), float()) : f(__nv_bfloat16(), __nv_bfloat16());
 }
 
-int64_t plan_ctas(const moe_norm_config& c, int64_t rows, bool vec, bool all) {
+int64_t plan_ctas(const moe_norm_config& c, int64_t rows, bool vec, bool with_gradient) {
   int64_t n = 0;
   with_types(c, [&](auto t, auto r) {
-    n = gradient_ctas<decltype(t), decltype(r)>(c, rows, vec, all);
+    n = gradient_ctas<decltype(t), decltype(r)>(c, rows, vec, with_gradient);
     return cudaSuccess;
   });
   return n;
@@ -63,9 +63,8 @@ cudaError_t launch_block_norm(const moe_norm_config& c, const moe_norm_io& io, i
 // (room for every kernel that may serve the configuration: rows may turn out
 // to take 16-byte accesses or not, a gradient of r' may come in or not)
 size_t norm_backward_workspace(const moe_norm_config& c, int64_t rows) {
-  const bool all = c.branch && c.post && c.pre;
   const int64_t ctas =
-      std::max({plan_ctas(c, rows, false, false), plan_ctas(c, rows, true, false), plan_ctas(c, rows, true, all)});
+      std::max({plan_ctas(c, rows, false, false), plan_ctas(c, rows, true, false), plan_ctas(c, rows, true, true)});
   return sizeof(float) * (size_t)ctas * column_sums(c) * ((c.hidden + 7) & ~7);
 }
 
@@ -82,7 +81,7 @@ cudaError_t launch_block_norm_backward(const moe_norm_config& c, const moe_norm_
   if (sh.post) o.out[n++] = io.dpost_weight;
   if (sh.pre) o.out[n++] = io.dpre_weight;
   if (sh.gate == MOE_GATE_CHANNEL) o.out[n++] = static_cast<float*>(io.dgate);
-  const int ctas = (int)plan_ctas(c, rows, vec, sh.post && sh.pre && io.dresidual_out);
+  const int ctas = (int)plan_ctas(c, rows, vec, io.dresidual_out != nullptr);
   return launch_k(column_sum_kernel, dim3((c.hidden + 31) / 32, sums), dim3(32, 32), 0, s, true,
                   static_cast<const float*>(io.workspace), ctas, sums, c.hidden, (c.hidden + 7) & ~7, o);
 }

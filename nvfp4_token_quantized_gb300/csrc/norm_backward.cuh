@@ -51,11 +51,14 @@ __global__ void __launch_bounds__(512, 1)
   const T* dh_in = static_cast<const T*>(io.dh);
   const T* y_in = static_cast<const T*>(io.y);
   const T* gate = static_cast<const T*>(io.gate);
-  const bool branch = PARTS == PARTS_ALL || s.branch, post = PARTS == PARTS_ALL || s.post;
-  const bool pre = PARTS == PARTS_ALL || s.pre, has_d = PARTS == PARTS_ALL || d_in;
+  const bool branch = PARTS != PARTS_ANY || s.branch, has_d = PARTS != PARTS_ANY || d_in;
+  const bool post = PARTS == PARTS_ANY ? s.post : PARTS != PARTS_PRE;
+  const bool pre = PARTS == PARTS_ANY ? s.pre : PARTS != PARTS_POST;
   const bool full = (GATE & GATE_BY_ELEMENT) && (GATE != GATE_ANY || s.gate == MOE_GATE_FULL);
   const bool channel = (GATE & GATE_BY_CHANNEL) && (GATE != GATE_ANY || s.gate == MOE_GATE_CHANNEL);
   const bool by_element = full || channel, token = s.gate == MOE_GATE_TOKEN;
+  // (without a post-norm y is needed for a gate's gradient only)
+  const bool needs_y = branch && (post || (s.gate != MOE_GATE_NONE && io.dgate));
 
   Pairs sum_post[KEEP ? V : 1], sum_pre[KEEP ? V : 1], sum_gate[KEEP && (GATE & GATE_BY_CHANNEL) ? V : 1];
   Pairs wp[KEEP ? V : 1], wn[KEEP ? V : 1];
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(512, 1)
           copy_granules(region + at_dh, dh_in + t * io.dh_stride, s.H, p.i, LANES);
         }
         if (has_d) copy_granules(region + r_bytes, d_in + t * io.dresidual_out_stride, s.H, p.i, LANES);
-        if (branch) copy_granules(region + at_y, y_in + t * io.y_stride, s.H, p.i, LANES);
+        if (needs_y) copy_granules(region + at_y, y_in + t * io.y_stride, s.H, p.i, LANES);
         if (full) copy_granules(region + at_gate, gate + t * io.gate_stride, s.H, p.i, LANES);
       }
       copies_commit();
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(512, 1)
           Run::DH::fetch(run, dh_in + t * io.dh_stride, p);
         }
         if (has_d) Run::D::fetch(run, d_in + t * io.dresidual_out_stride, p);
-        if (branch) Run::Y::fetch(run, y_in + t * io.y_stride, p);
+        if (needs_y) Run::Y::fetch(run, y_in + t * io.y_stride, p);
         if (full) Run::G::fetch(run, gate + t * io.gate_stride, p);
       }
       copies_commit();
@@ -251,7 +254,15 @@ __global__ void __launch_bounds__(512, 1)
           for (int j = 0; j < 4; ++j) yy = fma2(y.p[j], y.p[j], yy);
         }
       }
-      if constexpr (LAYER) {
+      if constexpr (PARTS == PARTS_POST) {
+        float q[1] = {sum_pairs(yy)};
+        sums(q);
+        yy.x = q[0];
+      } else if constexpr (PARTS == PARTS_PRE && !LAYER) {
+        float q[2] = {sum_pairs(xx), sum_pairs(ax)};
+        sums(q);
+        xx.x = q[0], ax.x = q[1];
+      } else if constexpr (LAYER) {
         float q[4] = {sum_pairs(xx), sum_pairs(yy), sum_pairs(ax), sum_pairs(sa)};
         sums(q);
         xx.x = q[0], yy.x = q[1], ax.x = q[2];
@@ -299,7 +310,13 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (live) put_pairs<R>(dres, v, p, dr[v]);
       if (!branch) continue;
-      Pairs y = get_y(v);
+      Pairs y;
+      if (needs_y) {
+        y = get_y(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.p[j] = both(0.0f);
+      }
       if (!post) {
         Pairs g;
         if (by_element) g = get_gate(v);
@@ -458,7 +475,7 @@ cudaError_t launch_block_norm_backward_t(const moe_norm_config& c, const moe_nor
   return with_width(s.H, BACKWARD_NARROW, vec, [&](auto chunks, auto v, auto fixed, auto wide) {
     constexpr int V = decltype(chunks)::value;
     constexpr bool VEC = decltype(v)::value;
-    return with_kind<VEC, V>(s, s.post && s.pre && io.dresidual_out, [&](auto layer, auto gate, auto parts) {
+    return with_kind<VEC, V>(s, parts_of(s, io.dresidual_out != nullptr), [&](auto layer, auto gate, auto parts) {
       return launch_gradient_rows<T, R, V, VEC, decltype(fixed)::value, decltype(wide)::value, decltype(layer)::value,
                                   decltype(gate)::value, decltype(parts)::value>(c, s, io, rows, stream);
     });

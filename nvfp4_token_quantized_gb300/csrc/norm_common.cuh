@@ -395,27 +395,43 @@ cudaError_t with_width(int H, int narrow, bool vec, F&& f) {
   return f(four, no, integral_constant<int, 512>{}, yes);
 }
 
-// Which parts a call has: ALL of post-norm, pre-norm and block output (for
-// the gradient also a gradient of r'), or any.
-constexpr int PARTS_ANY = 0, PARTS_ALL = 1;
+// Which parts a call has: a block output with both norms, only the pre-norm or
+// only the post-norm (and, for the gradient, one of r'), or any.
+constexpr int PARTS_ANY = 0, PARTS_ALL = 1, PARTS_PRE = 2, PARTS_POST = 3;
+// with_gradient: of r' (true for the forward)
+inline int parts_of(const NormShape& s, bool with_gradient) {
+  if (!s.branch || !with_gradient) return PARTS_ANY;
+  return s.post ? (s.pre ? PARTS_ALL : PARTS_POST) : s.pre ? PARTS_PRE : PARTS_ANY;
+}
 // Kinds of gate a kernel has code for, besides none and one value a token.
 constexpr int GATE_BY_CHANNEL = 1, GATE_BY_ELEMENT = 2, GATE_ANY = 3;
 
-// f(layer, gate, parts): the kernels for rows with 16-byte accesses of all
-// parts come without the code of what a call leaves out; other calls share
-// one that has it all, or all but a gate by channel or element.
+// f(layer, gate, parts): the kernels for rows with 16-byte accesses come without
+// the code of what a call leaves out, for both norms with any gate and for one
+// norm with none or one value a token (8192 x 4096 bf16, only the pre-norm: the
+// gradient 114 us with the code of all parts, 64 without); other calls
+// share one that has it all, or all but a gate by channel or element.
 template <bool VEC, int V, typename F>
-cudaError_t with_kind(const NormShape& s, bool all, F&& f) {
+cudaError_t with_kind(const NormShape& s, int parts, F&& f) {
   using std::integral_constant;
   if constexpr (VEC && V <= 2) {
-    if (all) {
+    const bool by_element = s.gate == MOE_GATE_CHANNEL || s.gate == MOE_GATE_FULL;
+    if (parts == PARTS_ALL && by_element) {
       auto gate = [&](auto layer) {
-        constexpr auto parts = integral_constant<int, PARTS_ALL>{};
-        if (s.gate == MOE_GATE_CHANNEL) return f(layer, integral_constant<int, GATE_BY_CHANNEL>{}, parts);
-        if (s.gate == MOE_GATE_FULL) return f(layer, integral_constant<int, GATE_BY_ELEMENT>{}, parts);
-        return f(layer, integral_constant<int, 0>{}, parts);
+        constexpr auto all = integral_constant<int, PARTS_ALL>{};
+        if (s.gate == MOE_GATE_CHANNEL) return f(layer, integral_constant<int, GATE_BY_CHANNEL>{}, all);
+        return f(layer, integral_constant<int, GATE_BY_ELEMENT>{}, all);
       };
       return s.layer ? gate(std::true_type{}) : gate(std::false_type{});
+    }
+    if (parts != PARTS_ANY && !by_element) {
+      auto kind = [&](auto some) {
+        constexpr auto none = integral_constant<int, 0>{};
+        return s.layer ? f(std::true_type{}, none, some) : f(std::false_type{}, none, some);
+      };
+      if (parts == PARTS_PRE) return kind(integral_constant<int, PARTS_PRE>{});
+      if (parts == PARTS_POST) return kind(integral_constant<int, PARTS_POST>{});
+      return kind(integral_constant<int, PARTS_ALL>{});
     }
   }
   constexpr auto any = integral_constant<int, PARTS_ANY>{};
@@ -491,13 +507,13 @@ struct BackwardRun {
 
 // The gradient's grid for a call: ctas of the kernel that serves it.
 template <typename T, typename R>
-int64_t gradient_ctas(const moe_norm_config& c, int64_t rows, bool vec, bool all) {
+int64_t gradient_ctas(const moe_norm_config& c, int64_t rows, bool vec, bool with_gradient) {
   const NormShape s = norm_shape(c);
   int64_t n = 0;
   with_width(c.hidden, BACKWARD_NARROW, vec, [&](auto chunks, auto v, auto fixed, auto) {
     constexpr int V = decltype(chunks)::value;
     constexpr bool VEC = decltype(v)::value;
-    return with_kind<VEC, V>(s, all, [&](auto, auto gate, auto) {
+    return with_kind<VEC, V>(s, parts_of(s, with_gradient), [&](auto, auto gate, auto) {
       using Run = BackwardRun<T, R, V, (decltype(gate)::value & GATE_BY_ELEMENT) != 0>;
       constexpr int LANES = decltype(fixed)::value;
       n = plan_backward(c, VEC, V, LANES, Run::UNITS, Run::linear(LANES)).ctas(rows);

@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1) block_norm_kernel(const N
   sums.clear();
   const int groups = WIDE ? 1 : blockDim.x / lanes, group = WIDE ? 0 : threadIdx.x / lanes;
   const Place<VEC, LANES> p((int)threadIdx.x - group * lanes, lanes, s.H);
-  const bool branch = PARTS == PARTS_ALL || s.branch, post = PARTS == PARTS_ALL || s.post;
-  const bool pre = PARTS == PARTS_ALL || s.pre;
+  const bool branch = PARTS != PARTS_ANY || s.branch;
+  const bool post = PARTS == PARTS_ANY ? s.post : PARTS != PARTS_PRE;
+  const bool pre = PARTS == PARTS_ANY ? s.pre : PARTS != PARTS_POST;
   const bool full = (GATE & GATE_BY_ELEMENT) && (GATE != GATE_ANY || s.gate == MOE_GATE_FULL);
   const bool channel = (GATE & GATE_BY_CHANNEL) && (GATE != GATE_ANY || s.gate == MOE_GATE_CHANNEL);
   const bool by_element = full || channel, token = s.gate == MOE_GATE_TOKEN;
@@ -268,7 +269,7 @@ cudaError_t launch_block_norm_t(const moe_norm_config& c, const moe_norm_io& io,
   return with_width(s.H, 4096, vec, [&](auto chunks, auto v, auto fixed, auto wide) {
     constexpr int V = decltype(chunks)::value;
     constexpr bool VEC = decltype(v)::value;
-    return with_kind<VEC, V>(s, s.post && s.pre, [&](auto layer, auto gate, auto parts) {
+    return with_kind<VEC, V>(s, parts_of(s, true), [&](auto layer, auto gate, auto parts) {
       return launch_rows<T, R, V, VEC, decltype(fixed)::value, decltype(wide)::value, decltype(layer)::value,
                          decltype(gate)::value, decltype(parts)::value>(s, io, rows, stream);
     });
