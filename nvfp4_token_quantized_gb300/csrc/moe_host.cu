@@ -20,6 +20,19 @@
 
 using namespace moe;
 
+namespace moe {
+
+// What names a stream: its id.  (A handle's value does not: that of a destroyed
+// stream may come back, and cudaStreamPerThread is another stream in every
+// thread, so that one is taken as unknown.)
+struct StreamId {
+  bool known = false;
+  unsigned long long id = 0;
+  bool is(const StreamId& o) const { return known && o.known && id == o.id; }
+};
+
+}  // namespace moe
+
 struct moe_handle {
   moe_config cfg{};
   int H = 0, I = 0, E = 0, K = 0, Tmax = 0;
@@ -73,7 +86,7 @@ struct moe_handle {
   // Weights, scales and the routing bias are written in the order of the
   // stream they were set on: a forward on another one waits for the event.
   cudaEvent_t ev_state = nullptr;
-  cudaStream_t state_stream = nullptr, state_seen = nullptr;
+  StreamId state_stream, state_seen;
   bool state_recorded = false;
   // moe_set_routing: the rule of the choice of experts and its balance bias [E]
   bool ruled = false, rule_bias = false;
@@ -264,13 +277,24 @@ bool capturing(cudaStream_t s) {
   return cudaStreamIsCapturing(s, &cs) == cudaSuccess && cs != cudaStreamCaptureStatusNone;
 }
 
+// (not of a capturing stream: the question itself would end its capture)
+StreamId stream_id(cudaStream_t s) {
+  StreamId r;
+  if (s == cudaStreamPerThread) return r;
+  r.known = cudaStreamGetId(s, &r.id) == cudaSuccess;
+  if (!r.known) cudaGetLastError();
+  return r;
+}
+
 // Orders stream s after the last writes of the handle's state.  (A capture
 // cannot wait for work outside it; its replays come after whatever the caller
 // ordered them after.)
 cudaError_t await_state(moe_handle* h, cudaStream_t s) {
-  if (!h->state_recorded || s == h->state_stream || s == h->state_seen || capturing(s)) return cudaSuccess;
+  if (!h->state_recorded || capturing(s)) return cudaSuccess;
+  const StreamId id = stream_id(s);
+  if (id.is(h->state_stream) || id.is(h->state_seen)) return cudaSuccess;
   const cudaError_t e = cudaStreamWaitEvent(s, h->ev_state, 0);
-  if (e == cudaSuccess) h->state_seen = s;
+  if (e == cudaSuccess) h->state_seen = id;
   return e;
 }
 
@@ -279,7 +303,7 @@ cudaError_t state_written(moe_handle* h, cudaStream_t s) {
   if (capturing(s)) return cudaSuccess;
   const cudaError_t e = cudaEventRecord(h->ev_state, s);
   if (e != cudaSuccess) return e;
-  h->state_stream = h->state_seen = s;
+  h->state_stream = h->state_seen = stream_id(s);
   h->state_recorded = true;
   return cudaSuccess;
 }
