@@ -63,6 +63,40 @@ def _both(layer, r, biases, d, T):
 
 
 @pytest.mark.parametrize("T", [40, 150])
+def test_a_forward_waits_for_a_bias_set_on_another_stream(setup, T):
+    d, r, biases, big = setup
+    layer = _layer(d)
+    want, _ = _both(layer, r, biases, d, T)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    done = _hold(big, a)
+    layer.set_routing(r, biases[0], stream=a)
+    got = layer.forward(d["x"][:T], d["gate_w"], stream=b)
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [40, 150])
+def test_a_forward_waits_for_weights_loaded_on_another_stream(setup, T):
+    d, r, biases, big = setup
+    layer = _layer(d)
+    w13, w2 = -d["w13"], -d["w2"]
+    outs = []
+    for pair in ((d["w13"], d["w2"]), (w13, w2)):
+        layer.load_weights(*pair)
+        outs.append(layer.forward(d["x"][:T], d["gate_w"]))
+    torch.cuda.synchronize()
+    assert not torch.equal(*outs)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    done = _hold(big, a)
+    layer.load_weights(d["w13"], d["w2"], stream=a)
+    got = layer.forward(d["x"][:T], d["gate_w"], stream=b)
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(got, outs[0])
+
+
+@pytest.mark.parametrize("T", [40, 150])
 def test_the_per_thread_streams_of_two_threads_are_two_streams(setup, T):
     d, r, biases, big = setup
     layer = _layer(d)
