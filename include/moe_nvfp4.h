@@ -55,7 +55,12 @@
  *
  * Streams: weights, scales and a routing bias are written in the order of the
  * stream they are set on; a forward on another stream waits for them on the
- * device (not inside a stream capture, which cannot wait for work outside).
+ * device, and setting them on another stream than the last forward's waits for
+ * that forward.  Neither holds for a forward or a setter inside a stream
+ * capture, which cannot wait for work outside: the caller orders setters after
+ * the replays that read what they overwrite, and replays after setters.  The
+ * forwards of a handle share its workspace: the caller orders those on
+ * different streams, replays among them, one after the other.
  *
  * Errors: every entry point returns a moe_status and never aborts; the text
  * of the last error on a handle is available from moe_get_last_error.

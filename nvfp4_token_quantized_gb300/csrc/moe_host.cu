@@ -88,6 +88,10 @@ struct moe_handle {
   cudaEvent_t ev_state = nullptr;
   StreamId state_stream, state_seen;
   bool state_recorded = false;
+  // ... and a setter on another one for the last forward, which reads them.
+  cudaEvent_t ev_read = nullptr;
+  StreamId read_stream;
+  bool read_recorded = false;
   // moe_set_routing: the rule of the choice of experts and its balance bias [E]
   bool ruled = false, rule_bias = false;
   RouteRule rule{};
@@ -244,11 +248,11 @@ bool same_desc(const moe_weight_desc& a, const moe_weight_desc& b) {
          a.device == b.device;
 }
 
-cudaError_t await_state(moe_handle* h, cudaStream_t s);
+cudaError_t before_state(moe_handle* h, cudaStream_t s);
 cudaError_t state_written(moe_handle* h, cudaStream_t s);
 
 moe_status quantize_weights(moe_handle* h, const void* w13, const void* w2, cudaStream_t s) {
-  CK(h, await_state(h, s));
+  CK(h, before_state(h, s));
   CK(h, cudaMemsetAsync(h->amax_bits, 0, sizeof(uint32_t) * 2 * h->E, s));
   CK(h, launch_weight_amax(w13, h->E, 2 * h->I, h->H, h->amax_bits, s));
   CK(h, launch_weight_amax(w2, h->E, h->H, h->I, h->amax_bits + h->E, s));
@@ -296,6 +300,25 @@ cudaError_t await_state(moe_handle* h, cudaStream_t s) {
   const cudaError_t e = cudaStreamWaitEvent(s, h->ev_state, 0);
   if (e == cudaSuccess) h->state_seen = id;
   return e;
+}
+
+// Orders stream s, which is about to write the handle's state, after earlier
+// writes and after the last forward, which may still be reading it.
+cudaError_t before_state(moe_handle* h, cudaStream_t s) {
+  const cudaError_t e = await_state(h, s);
+  if (e != cudaSuccess || !h->read_recorded || capturing(s) || stream_id(s).is(h->read_stream)) return e;
+  return cudaStreamWaitEvent(s, h->ev_read, 0);
+}
+
+// A forward that reads the state has been launched on stream s.  (Forwards of
+// a handle follow one another: they share its workspace.)
+cudaError_t state_read(moe_handle* h, cudaStream_t s) {
+  if (capturing(s)) return cudaSuccess;
+  const cudaError_t e = cudaEventRecord(h->ev_read, s);
+  if (e != cudaSuccess) return e;
+  h->read_stream = stream_id(s);
+  h->read_recorded = true;
+  return cudaSuccess;
 }
 
 // The handle's state has been written in stream s.
@@ -556,6 +579,7 @@ moe_status forward_impl(moe_handle* h, const void* x, const void* gate_w, const 
     if (ordered) CK(h, launch_finalize_ordered(h->ybuf, h->topk_w, shared, shared_scale, out, T, H, K, s));
     else CK(h, launch_finalize_atomic(h->out_acc, shared, shared_scale, out, T, H, s));
     CK(h, mark(h, 7, s));
+    CK(h, state_read(h, s));
   }
   h->last_T = T;
   h->last_small = T > 0 && T <= SMALL_BATCH_TOKENS;
@@ -708,6 +732,7 @@ moe_status moe_create(const moe_config* cfg, moe_handle** out) {
   }
   {
     cudaError_t e = cudaEventCreateWithFlags(&h->ev_state, cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&h->ev_read, cudaEventDisableTiming);
     if (e != cudaSuccess) return fail(cuda_fail(h, e, "cudaEventCreate"));
     e = gemm_setup_attributes(I / 128);
     if (e != cudaSuccess) return fail(cuda_fail(h, e, "cudaFuncSetAttribute"));
@@ -748,7 +773,7 @@ moe_status moe_set_static_scales(moe_handle* h, const float* x_gs, const float* 
   }
   DeviceGuard dg(h->cfg.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CK(h, await_state(h, s));
+  CK(h, before_state(h, s));
   CK(h, cudaMemcpyAsync(h->static_x_gs, x_gs, sizeof(float), cudaMemcpyDeviceToDevice, s));
   CK(h, cudaMemcpyAsync(h->static_h_gs, h_gs, sizeof(float) * h->E, cudaMemcpyDeviceToDevice, s));
   CK(h, state_written(h, s));
@@ -780,7 +805,7 @@ moe_status moe_set_routing(moe_handle* h, const moe_route_config* cfg, const flo
       return MOE_ERR_INVALID_ARG;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    CK(h, await_state(h, s));
+    CK(h, before_state(h, s));
     CK(h, cudaMemcpyAsync(h->route_bias, bias, sizeof(float) * h->E, cudaMemcpyDeviceToDevice, s));
     CK(h, state_written(h, s));
   }
@@ -799,6 +824,7 @@ moe_status moe_destroy(moe_handle* h) {
   for (cudaEvent_t ev : h->events)
     if (ev) cudaEventDestroy(ev);
   if (h->ev_state) cudaEventDestroy(h->ev_state);
+  if (h->ev_read) cudaEventDestroy(h->ev_read);
   if (h->ev_fork) cudaEventDestroy(h->ev_fork);
   if (h->ev_join) cudaEventDestroy(h->ev_join);
   if (h->side) cudaStreamDestroy(h->side);
@@ -820,7 +846,7 @@ moe_status moe_load_shared_weights(moe_handle* h, const void* w13s, const moe_we
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // one expert: the routed experts' conversion (gate / up rows interleaved
   // in chunks of 64 for the w13 epilogue), into the same buffers every time
-  CK(h, await_state(h, s));
+  CK(h, before_state(h, s));
   CK(h, cudaMemsetAsync(h->s_amax_bits, 0, sizeof(uint32_t) * 2, s));
   CK(h, launch_weight_amax(w13s, 1, 2 * h->Is, h->H, h->s_amax_bits, s));
   CK(h, launch_weight_amax(w2s, 1, h->H, h->Is, h->s_amax_bits + 1, s));

@@ -1,5 +1,6 @@
 """A handle whose state is set on one stream and used on another: forwards
-wait for the state they follow, whatever the streams' handles are.
+wait for the state they follow and setters for the forwards they follow,
+whatever the streams' handles are.
 
 Every case holds one stream back behind long kernels and checks that they were
 still running when the other stream had its work.
@@ -94,6 +95,49 @@ def test_a_forward_waits_for_weights_loaded_on_another_stream(setup, T):
     assert not done.query()
     torch.cuda.synchronize()
     assert torch.equal(got, outs[0])
+
+
+@pytest.mark.parametrize("T", [40, 150])
+def test_a_bias_set_on_another_stream_waits_for_the_forward(setup, T):
+    d, r, biases, big = setup
+    layer = _layer(d)
+    other, kept = _both(layer, r, biases, d, T)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    done = _hold(big, a)
+    got = layer.forward(d["x"][:T], d["gate_w"], stream=a)
+    layer.set_routing(r, biases[0], stream=b)
+    after = layer.forward(d["x"][:T], d["gate_w"], stream=b)
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(got, kept) and torch.equal(after, other)
+
+
+@pytest.mark.parametrize("T", [40, 150])
+@pytest.mark.parametrize("setter", ["load", "refresh", "shared", "scales"])
+def test_state_set_on_another_stream_waits_for_the_forward(setup, setter, T):
+    d, _, _, big = setup
+    layer = _layer(d, static_scales=setter == "scales", shared_inter=128 if setter == "shared" else 0)
+    w13s, w2s = (t.cuda() for t in synthetic.make_shared_weights(SHAPE, 128, seed=2))
+    scales = [(torch.full((1,), v, device="cuda"), torch.full((SHAPE.E,), v, device="cuda")) for v in (300.0, 40.0)]
+    states = {"load": ((d["w13"], d["w2"]), (-d["w13"], -d["w2"])),
+              "refresh": ((d["w13"], d["w2"]), (-d["w13"], -d["w2"])),
+              "shared": ((w13s, w2s), (-w13s, -w2s)), "scales": scales}[setter]
+    put = {"load": layer.load_weights, "refresh": layer.refresh_scales_inplace, "shared": layer.load_shared_weights,
+           "scales": layer.set_static_scales}[setter]
+    outs = []
+    for s in (states[1], states[0]):
+        put(*s)
+        outs.append(layer.forward(d["x"][:T], d["gate_w"]))
+    torch.cuda.synchronize()
+    assert not torch.equal(*outs)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    done = _hold(big, a)
+    got = layer.forward(d["x"][:T], d["gate_w"], stream=a)
+    put(*states[1], stream=b)
+    after = layer.forward(d["x"][:T], d["gate_w"], stream=b)
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(got, outs[1]) and torch.equal(after, outs[0])
 
 
 @pytest.mark.parametrize("T", [40, 150])
