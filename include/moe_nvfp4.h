@@ -490,7 +490,8 @@ typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_
  * is written for it and h is a plain pre-norm; then post and gate are off.
  * y, gate and h are of `dtype`, the residual of that type or FP32, the
  * weights of that type or FP32.  Statistics, sums and the weights' gradients
- * are FP32.  hidden <= 16384. */
+ * are FP32: a row whose sum of squares passes FP32's range is divided by
+ * infinity, so n(x) is 0 there.  hidden <= 16384. */
 typedef struct {
   int hidden;
   int kind;            /* moe_norm_kind */

@@ -16,9 +16,11 @@ namespace moe {
 // 1 / sqrt(v), v > 0: the hardware's approximation (2 units in the last
 // place) and one Newton step, about one unit, without the call and the
 // branches of an IEEE root and quotient that every warp of a row would make.
+// 0 for a sum of squares past FP32, as 1 / sqrt gives (the step would make it
+// 0 times infinity).
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float y = rsqrtf(v);
-  return fmaf(0.5f * y, fmaf(-v * y, y, 1.0f), y);
+  return v < INFINITY ? fmaf(0.5f * y, fmaf(-v * y, y, 1.0f), y) : y;
 }
 
 struct NormShape {
