@@ -53,3 +53,19 @@ def test_rows_whose_squares_overflow(H, dtype, kind):
     ref = n.backward(a["dres"][keep], a["dh"][keep], r[keep], pre_weight=w["pre_weight"])
     assert torch.equal(dr[bad], a["dres"][bad]) and torch.equal(dr[keep], ref[0])
     assert torch.isfinite(dpre).all() and torch.allclose(dpre, ref[4], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("T,H", [(2000, 2048), (300, 8192), (500, 1000), (700, 64), (40, 12288)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_one_row_alone_gives_every_bit_it_gives_in_a_batch(T, H, kind):
+    n, a = _norm(H, kind=kind), _rows(T, H, BF16)
+    w = dict(post_weight=torch.linspace(0.5, 1.5, H, device="cuda").to(BF16),
+             pre_weight=torch.linspace(1.5, 0.5, H, device="cuda").to(BF16))
+    out, h = n.forward(a["residual"], a["y"], **w)
+    dr, dy = n.backward(a["dres"], a["dh"], out, a["y"], **w)[:2]
+    for t in (0, 7, T - 1):
+        one = slice(t, t + 1)
+        o1, h1 = n.forward(a["residual"][one], a["y"][one], **w)
+        assert torch.equal(o1, out[one]) and torch.equal(h1, h[one])
+        r1, y1 = n.backward(a["dres"][one], a["dh"][one], out[one], a["y"][one], **w)[:2]
+        assert torch.equal(r1, dr[one]) and torch.equal(y1, dy[one])
