@@ -455,8 +455,8 @@ MOE_API moe_status moe_route_select(const moe_route_config* cfg, const void* log
 
 /* Gradient of the weights with respect to the logits, the choice held fixed
  * (the bias gets none).  logits, topk_ids and topk_w are moe_route_select's
- * input and its own outputs (the sigmoid's gradient takes the scores from the
- * weights), dweights FP32 [num_tokens, top_k]; dlogits gets every
+ * input and its own outputs (the sigmoid's gradient takes scores away from 1
+ * from the weights, within a few 2^-24), dweights FP32 [num_tokens, top_k]; dlogits gets every
  * element of [num_tokens, num_experts] in the logits' type.  A slot of weight
  * 0, or whose id is outside [0, num_experts), passes no gradient; a token's
  * ids must be distinct.  dlogits may be logits itself (same stride). */

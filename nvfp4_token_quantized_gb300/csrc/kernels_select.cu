@@ -40,15 +40,22 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS)
 // the slots, whose values go to their experts' places in shared memory (zero
 // elsewhere), then whole rows, so that every element is stored once, four at a
 // time where rows allow.  Bytes bound it (131072 x 256 FP32, sigmoid, top-8: 30 us,
-// 5.1 TB/s).  Memory answers a scattered logit
+// 5.0 TB/s).  Memory answers a scattered logit
 // with 64 bytes, so the sigmoid's gradient takes the scores from the weights:
 // w = scale s / (sum + 1e-20), and one logit a row (of the largest weight)
-// gives the quotient; without renormalisation it needs none.
+// gives the quotient; without renormalisation it needs none.  That leaves
+// scores a few 2^-24 off, which 1 - s would magnify where s is near 1: scores
+// above NEAR_ONE take both from their logits.  (FP32, 131072 x 256: error against
+// 64 bits 1.7 times that of scores from all logits and a difference, at 30 us;
+// all logits read: 0.5 times, at 41.)
 template <typename T, int NE, int RB, bool SIGMOID>
 __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
     const RouteRule r, const T* logits, int64_t stride, const int32_t* __restrict__ ids, const float* __restrict__ w,
     const float* __restrict__ dw, int64_t rows, T* dlogits, int64_t dstride) {
   constexpr int WIDTH = NE * 32;
+  // (1 - s keeps 16 bits or more of the FP32 ones, 14 for the 16-bit types,
+  // whose results have 11)
+  constexpr float NEAR_ONE = sizeof(T) == 4 ? 1.0f - 1.0f / 64 : 1.0f - 1.0f / 256;
   __shared__ __align__(16) float place[SELECT_WARPS][RB][WIDTH];
   const unsigned all = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -89,6 +96,7 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
     if (weight == 0.0f || (unsigned)id >= (unsigned)r.E) id = -1;
     if (id < 0) d = 0.0f;
     float score = 0.0f, sum = 1.0f;  // sum: of the chosen scores, plus 1e-20
+    float rest = 1.0f;               // 1 - score (sigmoid)
     if constexpr (SIGMOID) {
       score = id >= 0 ? weight / r.scale : 0.0f;
       if (r.renormalize) {
@@ -102,6 +110,12 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
         if (lane == leader && id >= 0) whole = sigmoid_ieee(to_f32(logits[(t + my_q) * stride + id])) / score;
         sum = __shfl_sync(all, whole, leader);
         score = id >= 0 ? score * sum : 0.0f;
+      }
+      rest = 1.0f - score;
+      if (id >= 0 && !(score < NEAR_ONE)) {
+        const float e = expf(-to_f32(logits[(t + my_q) * stride + id]));
+        score = 1.0f / (1.0f + e);
+        rest = e * score;
       }
     } else {
       float my_top = 0.0f, my_total = 1.0f;
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
       d = id >= 0 ? (d - along) / sum : 0.0f;
     }
     float my_mean = 0.0f;  // of the row of this lane's slot
-    if constexpr (SIGMOID) d *= score * (1.0f - score);
+    if constexpr (SIGMOID) d *= score * rest;
     else my_mean = over_slots(d * score);
     if (id >= 0) buf[my_q][id] = d;
     __syncwarp();
