@@ -206,7 +206,8 @@ struct Place {
 // ---- rows ahead of the arithmetic ----
 // VEC: a ring in shared memory filled by cp.async.  A thread copies and later
 // reads only its own 16-byte pieces, so the ring needs no barrier and no flag.
-// Otherwise: the next row waits in registers.
+// Otherwise: rows as the granules that hold them, behind a barrier (below); rows
+// of more than two chunks a thread are read from global memory.
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -446,8 +447,10 @@ cudaError_t with_kind(const NormShape& s, int parts, F&& f) {
 
 // Shared memory of an SM for the rings of n CTAs each: of 228 KB, less the
 // runtime's 1 KB and the sums' words for each.
-__host__ __device__ constexpr int ring_room(int n) { return (228 * 1024 / n - 1024 - 512 - 15) & ~15; }
-constexpr int RING_ROOM = 226 * 1024;  // (a CTA may have 227 KB, 512 bytes of it the sums')
+constexpr int SUMS_BYTES = RowSums<true>::WORDS * sizeof(float);
+__host__ __device__ constexpr int ring_room(int n) { return (228 * 1024 / n - 1024 - SUMS_BYTES - 15) & ~15; }
+constexpr int RING_ROOM = 226 * 1024;
+static_assert(RING_ROOM + SUMS_BYTES <= 227 * 1024, "what a CTA may have");
 // Rows in a ring: three keep two rows in flight.  Wide operands leave room for
 // fewer, counted for 512 threads an SM.  (A constant: with a count known only
 // at run time the forward ran 1.1x slower.)
