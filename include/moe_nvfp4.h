@@ -542,8 +542,10 @@ MOE_API size_t moe_block_norm_workspace_bytes(const moe_norm_config* cfg, int64_
 
 /* The statistics are those of the stored residual_out.  dresidual may be
  * dresidual_out and dy may be dh or y (same stride and type); other overlaps
- * are MOE_ERR_ALIAS.  Column sums run in an order fixed by rows and hidden:
- * results repeat bit for bit. */
+ * are MOE_ERR_ALIAS.  Column sums run in an order fixed by rows, cfg, whether
+ * dresidual_out is given and whether every row starts on 16 bytes (addresses
+ * and strides): the same call repeats bit for bit, the same values in rows
+ * aligned otherwise give sums that may differ by FP32 rounding. */
 MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const moe_norm_grad_io* io, int64_t rows,
                                            void* stream);
 

@@ -5,6 +5,8 @@ before and after a block, each with its gradient (``moe_route_select`` and
 Argument checks and marshalling only, as in ``binding``.  Tensors live on the
 current CUDA device; rows may be strided, their elements may not.  Results
 that are not passed in are allocated here, on the stream the call runs on.
+Nothing is recorded for autograd: results never require a gradient, and the
+backward calls are the caller's to make.
 """
 
 from __future__ import annotations
