@@ -39,14 +39,14 @@ __global__ void __launch_bounds__(32 * SELECT_WARPS)
 // Gradient.  A warp takes RB rows at a time, whose slots fit its lanes: first
 // the slots, whose values go to their experts' places in shared memory (zero
 // elsewhere), then whole rows, so that every element is stored once, four at a
-// time where rows allow.  Bytes bound it (131072 x 256 FP32, sigmoid, top-8: 30 us,
-// 5.0 TB/s).  Memory answers a scattered logit
+// time where rows allow.  Bytes bound it (131072 x 256 FP32, sigmoid, top-8: 31 us,
+// 4.9 TB/s).  Memory answers a scattered logit
 // with 64 bytes, so the sigmoid's gradient takes the scores from the weights:
 // w = scale s / (sum + 1e-20), and one logit a row (of the largest weight)
 // gives the quotient; without renormalisation it needs none.  That leaves
 // scores a few 2^-24 off, which 1 - s would magnify where s is near 1: scores
 // above NEAR_ONE take both from their logits.  (FP32, 131072 x 256: error against
-// 64 bits 1.7 times that of scores from all logits and a difference, at 30 us;
+// 64 bits 1.7 times that of scores from all logits and a difference, at 31 us;
 // all logits read: 0.5 times, at 41.)
 template <typename T, int NE, int RB, bool SIGMOID>
 __global__ void __launch_bounds__(32 * SELECT_WARPS) select_backward_kernel(
@@ -263,8 +263,8 @@ cudaError_t launch_select(const RouteRule& rule, const void* logits, int dtype, 
   const int bytes = dtype == MOE_DTYPE_F32 ? 4 : 2;
   const bool aligned = stride % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & (4 * bytes - 1)) == 0;
   // Parts of rows once they make five warps an SM, which is where the two
-  // meet (128 experts: 4096 rows 5.2 us against a warp a row's 4.6, 8192 rows
-  // 6.1 against 7.5, 16384 7.5 against 12.3).
+  // meet (128 experts, all open: 4096 rows 5.2 us against a warp a row's 4.6,
+  // 8192 rows 6.1 against 7.5, 16384 7.5 against 12.3).
   const int parts = r.E <= 64 ? 2 : 4;
   if (rows * parts >= 32 * 5 * 152) {
     r.vec = aligned && r.E % 4 == 0;

@@ -12,7 +12,7 @@
 // Bytes bound it: x, dh, dr', y come once (the passes over a row read it from
 // the ring again), dr and dy leave once.  The column sums stay in the
 // registers of the threads that own the columns while a CTA walks its rows;
-// a second kernel adds the CTAs' sums in order.  16384 x 8192 bf16: 250 us, 6.4
+// a second kernel adds the CTAs' sums in order.  16384 x 8192 bf16: 248 us, 6.5
 // TB/s (column sums in shared memory and no ring: 730).  Centred rows with an
 // element gate (4073 x 4096, FP32 residual): 86 us, 4.3 TB/s, bound by latency at
 // the 16 warps an SM that their registers leave.  Rows above 8192 columns take

@@ -18,7 +18,8 @@
 // Otherwise the experts that reach the last maximum, if at most 32, are
 // ranked one a lane; and rows that this does not cover either (NaN, infinite
 // scores or biases, fewer open experts than slots, many equal values) go
-// through select_by_rounds.
+// through select_by_rounds, behind which a grid of few waves ends (4073 x 128 bf16
+// with padding tokens: 6.4 us, 4.6 without them at 4096).
 #pragma once
 
 #include "common.cuh"
