@@ -167,14 +167,16 @@ def test_the_per_thread_streams_of_two_threads_are_two_streams(setup, T):
     assert still and torch.equal(out, want)
 
 
-def test_state_set_and_used_beside_a_capture(setup):
+@pytest.mark.parametrize("beside_on", ["own", "legacy", "per thread"])
+def test_state_set_and_used_beside_a_capture(setup, beside_on):
     # a capture on one stream goes on while the handle works on another
     d, r, biases, _ = setup
     layer = _layer(d)
     want = _both(layer, r, biases, d, 40)
     x = d["x"][:40].contiguous()
     out, beside = torch.empty_like(x), torch.empty_like(x)
-    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    a = torch.cuda.Stream()
+    b = {"own": torch.cuda.Stream(), "legacy": 0, "per thread": PER_THREAD}[beside_on]
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=a):
         layer.forward(x, d["gate_w"], out)
