@@ -549,6 +549,93 @@ MOE_API size_t moe_block_norm_workspace_bytes(const moe_norm_config* cfg, int64_
 MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const moe_norm_grad_io* io, int64_t rows,
                                            void* stream);
 
+/* The balance loss of a choice of experts and what it is made of.  Over the
+ * counted tokens of a sequence, N of them:
+ *   p_te = softmax of token t's logits, or sigmoid(l_te) / (sum over the experts
+ *          of sigmoid(l_te) + 1e-20), by cfg->score (a token whose logits are
+ *          all -inf has p = 0);
+ *   c_e  = how often e stands in the tokens' topk_ids (ids outside
+ *          [0, num_experts) count nowhere);
+ *   L    = coefficient * sum_e (num_experts * c_e / (top_k * N)) * (sum_t p_te / N)
+ * and loss is the mean of L over the sequences that have counted tokens, 0 if
+ * none has.  slope is d loss / d p of each counted token of a sequence:
+ * coefficient * num_experts * c_e / (top_k * N^2 * sequences with tokens), 0 for
+ * a sequence without.  The counts are constants to the gradient.
+ * cfg: num_experts, top_k and score are used (the rest is checked).
+ *   logits:  [num_tokens, num_experts] of moe_dtype dtype, rows logits_stride
+ *            elements apart;
+ *   topk_ids: int32 [num_tokens, top_k];
+ *   offsets: int32 [num_sequences + 1], in ascending order: sequence s holds
+ *            the rows from offsets[s] up to offsets[s + 1] (values outside
+ *            [0, num_tokens] count as its ends).  Rows before the first and
+ *            behind the last sequence are not counted.  NULL (with
+ *            num_sequences 1): all rows are one sequence;
+ *   mask:    one byte a token, 0 for a token that is not counted; NULL: all
+ *            are.  What such a token's logits hold, NaN too, reaches nothing.
+ * Sums are FP32 over runs of a few hundred rows, joined in a fixed order: a
+ * call repeats bit for bit. */
+typedef struct {
+  const void* logits;
+  const int32_t* topk_ids;
+  const int32_t* offsets;
+  const uint8_t* mask;
+  int64_t logits_stride;
+  int64_t num_sequences;
+  int dtype; /* moe_dtype of the logits */
+} moe_balance_io;
+
+/* Device bytes moe_balance_loss needs; 0 for a refused cfg or sizes. */
+MOE_API size_t moe_balance_workspace_bytes(const moe_route_config* cfg, int64_t num_tokens, int64_t num_sequences);
+
+/* loss: FP32 scalar; counts: int32 [num_sequences, num_experts]; slope: FP32 of
+ * the same shape; all written, for zero tokens too (with zeros).  workspace:
+ * moe_balance_workspace_bytes, 16-byte aligned.  num_tokens * top_k < 2^31.
+ * Outputs that overlap an operand or each other are MOE_ERR_ALIAS. */
+MOE_API moe_status moe_balance_loss(const moe_route_config* cfg, const moe_balance_io* io, float coefficient,
+                                    int64_t num_tokens, float* loss, int32_t* counts, float* slope, void* workspace,
+                                    void* stream);
+
+/* dlogits = add + dloss * (gradient of the loss), with slope as the loss call
+ * gave it (or the caller's own, say of counts summed over replicas); rows that
+ * are not counted get add alone.  dloss: FP32 scalar on the device, NULL = 1;
+ * add: rows of the logits' type, add_stride apart, NULL = 0.  io->topk_ids is
+ * not read.  dlogits may be the logits or add (same stride); other overlaps
+ * are MOE_ERR_ALIAS. */
+MOE_API moe_status moe_balance_loss_backward(const moe_route_config* cfg, const moe_balance_io* io, const float* slope,
+                                             const float* dloss, const void* add, int64_t add_stride,
+                                             int64_t num_tokens, void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* One gradient of a set: count elements of moe_dtype dtype, next to each other
+ * in any order of their dimensions. */
+typedef struct {
+  const void* data;
+  void* out;      /* where the clipped values go (data itself: in place) */
+  int64_t count;  /* >= 0 */
+  int64_t dtype;  /* moe_dtype */
+} moe_gradient;
+
+/* Device bytes of the workspace of the two calls below, for any set. */
+MOE_API size_t moe_gradient_workspace_bytes(void);
+
+/* norm (FP32 scalar on the device) = square root of the sum of the squares of
+ * every element of every tensor.  Squares are summed in FP32 by runs and the
+ * runs in FP64; where a run leaves FP32's range its squares are FP64 too, so
+ * the norm is finite and exact to a few 2^-24 whenever it fits FP32.  It is
+ * infinite or NaN if an element is.  `out` is not used.  tensors is read
+ * before the call returns. */
+MOE_API moe_status moe_gradient_norm(const moe_gradient* tensors, int64_t num, float* norm, void* workspace,
+                                     void* stream);
+
+/* norm as above, and out = data * min(1, max_norm / (norm + eps)) for every
+ * tensor, the product rounded once to the tensor's type.  A norm that is NaN
+ * makes every factor NaN, an infinite one 0 (infinities then become NaN): read
+ * norm before the values are used.  Tensors clipped in place are not written
+ * when the factor is 1.  max_norm finite and >= 0, eps finite and > 0.  An out
+ * that overlaps another tensor's data or out, or its own data elsewhere than
+ * at its start, is MOE_ERR_ALIAS; the same tensor twice is such a case. */
+MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, float max_norm, float eps, float* norm,
+                                      void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,6 +46,8 @@ EXPORTED = (
     "moe_stage_name", "moe_route_noalloc", "moe_set_static_scales", "moe_load_shared_weights",
     "moe_debug_shared", "moe_debug_shared_act_quant", "moe_route_select", "moe_route_select_backward",
     "moe_set_routing", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
+    "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward", "moe_gradient_workspace_bytes",
+    "moe_gradient_norm", "moe_clip_gradients",
 )
 MOE_ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 MOE_NUM_STAGES = 7
@@ -90,6 +92,16 @@ class moe_norm_grad_io(ctypes.Structure):
                                                  "dgate_stride")])
 
 
+class moe_balance_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "topk_ids", "offsets", "mask")]
+                + [("logits_stride", ctypes.c_int64), ("num_sequences", ctypes.c_int64), ("dtype", ctypes.c_int)])
+
+
+class moe_gradient(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int64)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{status_string(status)}: {message}")
@@ -113,6 +125,7 @@ def load_library() -> ctypes.CDLL:
         raise RuntimeError(f"CUDA library not built: {path} is missing (run __graft_entry__.build())")
     lib = ctypes.CDLL(path)
     P, I, U, L, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_int64, ctypes.c_size_t
+    F = ctypes.c_float
     sig = {
         "moe_create": (I, [ctypes.POINTER(moe_config), ctypes.POINTER(P)]),
         "moe_destroy": (I, [P]),
@@ -149,6 +162,14 @@ def load_library() -> ctypes.CDLL:
         "moe_block_norm": (I, [ctypes.POINTER(moe_norm_config), ctypes.POINTER(moe_norm_io), L, P]),
         "moe_block_norm_workspace_bytes": (S, [ctypes.POINTER(moe_norm_config), L]),
         "moe_block_norm_backward": (I, [ctypes.POINTER(moe_norm_config), ctypes.POINTER(moe_norm_grad_io), L, P]),
+        "moe_balance_workspace_bytes": (S, [ctypes.POINTER(moe_route_config), L, L]),
+        "moe_balance_loss": (I, [ctypes.POINTER(moe_route_config), ctypes.POINTER(moe_balance_io), F, L, P, P, P, P,
+                                 P]),
+        "moe_balance_loss_backward": (I, [ctypes.POINTER(moe_route_config), ctypes.POINTER(moe_balance_io), P, P, P,
+                                          L, L, P, L, P]),
+        "moe_gradient_workspace_bytes": (S, []),
+        "moe_gradient_norm": (I, [P, L, P, P, P]),
+        "moe_clip_gradients": (I, [P, L, F, F, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

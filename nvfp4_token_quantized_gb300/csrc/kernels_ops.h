@@ -63,4 +63,51 @@ cudaError_t launch_block_norm(const moe_norm_config& c, const moe_norm_io& io, i
 cudaError_t launch_block_norm_backward(const moe_norm_config& c, const moe_norm_grad_io& io, int64_t rows, bool vec,
                                        cudaStream_t s);
 
+// ---- balance loss (kernels_balance.cu) ----
+
+// One call; what a launch does not use is left as it is.
+struct BalanceArgs {
+  const void* logits;
+  int64_t stride;
+  int dtype;
+  const int32_t* ids;
+  const int32_t* offsets;  // NULL: every row is of the one sequence
+  const uint8_t* mask;
+  int64_t rows, sequences;
+  int E, K;
+  bool sigmoid;
+  float coefficient;
+  float* loss;
+  int32_t* counts;
+  float* slope;
+  const float* dloss;
+  const void* add;
+  void* dlogits;
+  int64_t add_stride, dstride;
+  // set by the launch
+  int64_t block_rows;
+  bool small;
+  uint32_t* parts;
+  float* seq_loss;
+  int32_t* seq_tokens;
+};
+
+size_t balance_workspace(int E, int64_t rows, int64_t sequences);
+// vec: four neighbouring logits of every row may be loaded at once.
+cudaError_t launch_balance(BalanceArgs a, bool vec, void* workspace, cudaStream_t s);
+cudaError_t launch_balance_backward(BalanceArgs a, bool vec, cudaStream_t s);
+
+// ---- gradient norm and clipping (kernels_clip.cu) ----
+
+constexpr int CLIP_PARTS = 152 * 4;  // CTAs of one wave, each with a sum of squares
+
+struct ClipArgs {
+  float limit, eps;
+  bool scale;    // clip, not only the norm
+  float* norm;
+  double* sums;  // [CLIP_PARTS]
+};
+
+cudaError_t launch_clip(const moe_gradient* tensors, int64_t num, const ClipArgs& a, cudaStream_t s);
+
 }  // namespace moe

@@ -18,7 +18,7 @@ import torch
 
 from .binding import (MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE,
                       MOE_GATE_TOKEN, MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_NORM_LAYER, MOE_NORM_RMS, MOE_OK,
-                      MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MoEError, load_library, moe_norm_config,
+                      MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MoEError, load_library, moe_balance_io, moe_norm_config,
                       moe_norm_grad_io, moe_norm_io, moe_route_config)
 
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32}
@@ -117,6 +117,10 @@ def _new_vector(n: int, dtype):
     return _empty_strided((n,), (1,), dtype)
 
 
+def _new_scalar():
+    return _empty_strided((), (), torch.float32)
+
+
 def _ok(st: int, what: str) -> None:
     if st != MOE_OK:
         raise MoEError(st, what)
@@ -209,6 +213,88 @@ class ExpertRouter:
             T, dlogits.data_ptr(), ldd, _current(dev) if stream is None else stream)
         if st != MOE_OK:
             raise MoEError(st, f"moe_route_select_backward(T={T}, E={self.E}, K={self.K})")
+        return dlogits
+
+
+    def balance_loss(self, logits: torch.Tensor, ids: torch.Tensor, coefficient: float = 1.0,
+                     offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(loss, counts, slope) of the choice ids (int32 [T, K]) from logits
+        [T, E]: the balance loss (float32 scalar), how often each expert was
+        chosen (int32 [S, E]) and the loss's derivative by the tokens' scores
+        (float32 [S, E]), which ``balance_backward`` takes.
+
+        offsets: int32 [S + 1], the first rows of S sequences and the end of
+        the last, each balanced for itself (none: all rows are one); mask:
+        bool [T], False for tokens that are not counted."""
+        if stream is not None:
+            with _OnStream(stream, _device(logits, "logits")) as on:
+                return self._balance_loss(logits, ids, coefficient, offsets, mask, on.handle)
+        return self._balance_loss(logits, ids, coefficient, offsets, mask, None)
+
+    def _sequences(self, offsets, mask, T, dev):
+        """The number of sequences and the addresses of offsets and mask."""
+        S, po, pm = 1, None, None
+        if offsets is not None:
+            po = _vector(offsets, torch.int32, offsets.numel(), "offsets", dev)
+            S = offsets.numel() - 1
+            if S < 1:
+                raise ValueError("offsets must hold at least two values")
+        if mask is not None:
+            pm = _vector(mask, torch.uint8 if mask.dtype is torch.uint8 else torch.bool, T, "mask", dev)
+        return S, po, pm
+
+    def _balance_loss(self, logits, ids, coefficient, offsets, mask, stream):
+        dev, dt, T, ld = self._logits(logits)
+        if ids.shape != (T, self.K):
+            raise ValueError(f"ids must be [{T}, {self.K}], got {tuple(ids.shape)}")
+        S, po, pm = self._sequences(offsets, mask, T, dev)
+        io = moe_balance_io(logits.data_ptr(), _vector(ids, torch.int32, T * self.K, "ids", dev), po, pm, ld, S, dt)
+        loss, counts, slope = _new_scalar(), _new_rows(S, self.E, torch.int32), _new_rows(S, self.E, torch.float32)
+        need = int(self._lib.moe_balance_workspace_bytes(self._cfg, T, S))
+        ws = _new_vector(max(need, 16), torch.uint8)
+        st = self._lib.moe_balance_loss(self._cfg, ctypes.byref(io), float(coefficient), T, loss.data_ptr(),
+                                        counts.data_ptr(), slope.data_ptr(), ws.data_ptr(),
+                                        _current(dev) if stream is None else stream)
+        if st != MOE_OK:
+            raise MoEError(st, f"moe_balance_loss(T={T}, E={self.E}, K={self.K}, sequences={S}, "
+                               f"coefficient={coefficient})")
+        return loss, counts, slope
+
+    def balance_backward(self, logits: torch.Tensor, slope: torch.Tensor, dloss: Optional[torch.Tensor] = None,
+                         offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                         add: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+        """add + dloss * gradient of the balance loss by the logits, in their
+        type; logits, offsets and mask as in ``balance_loss``, slope (float32
+        [S, E]) from it; dloss: float32 CUDA scalar, the gradient of the loss
+        itself (none: 1); add: rows [T, E] to add to, such as
+        ``select_backward``'s (dlogits may be add)."""
+        if stream is not None:
+            with _OnStream(stream, _device(logits, "logits")) as on:
+                return self._balance_backward(logits, slope, dloss, offsets, mask, add, dlogits, on.handle)
+        return self._balance_backward(logits, slope, dloss, offsets, mask, add, dlogits, None)
+
+    def _balance_backward(self, logits, slope, dloss, offsets, mask, add, dlogits, stream):
+        dev, dt, T, ld = self._logits(logits)
+        S, po, pm = self._sequences(offsets, mask, T, dev)
+        if slope.shape != (S, self.E):
+            raise ValueError(f"slope must be [{S}, {self.E}], got {tuple(slope.shape)}")
+        pa, la = None, self.E
+        if add is not None:
+            la = _rows(add, logits.dtype, T, self.E, "add", dev)
+            pa = add.data_ptr()
+        if dlogits is None:
+            dlogits, ldd = _new_rows(T, self.E, logits.dtype), self.E
+        else:
+            ldd = _rows(dlogits, logits.dtype, T, self.E, "dlogits", dev)
+        io = moe_balance_io(logits.data_ptr(), None, po, pm, ld, S, dt)
+        st = self._lib.moe_balance_loss_backward(
+            self._cfg, ctypes.byref(io), _vector(slope, torch.float32, S * self.E, "slope", dev),
+            None if dloss is None else _vector(dloss, torch.float32, 1, "dloss", dev), pa, la, T, dlogits.data_ptr(),
+            ldd, _current(dev) if stream is None else stream)
+        if st != MOE_OK:
+            raise MoEError(st, f"moe_balance_loss_backward(T={T}, E={self.E}, sequences={S})")
         return dlogits
 
 
