@@ -636,6 +636,71 @@ MOE_API moe_status moe_gradient_norm(const moe_gradient* tensors, int64_t num, f
 MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, float max_norm, float eps, float* norm,
                                       void* workspace, void* stream);
 
+/* Low-rank adapters beside a projection, many of them in one batch.  A row t
+ * with adapter a = ids[t]:
+ *   hidden_t = scales[a] * x_t down[a]^T        [rank]
+ *   out_t    = base_t + hidden_t up[a]          [out_features]
+ * Rows whose id is outside [0, num_adapters) have no adapter: out is base
+ * (zeros without one) and hidden 0.  Both factors hold a row for each rank:
+ *   down: [num_adapters, rank, in_features], up: [num_adapters, rank,
+ *   out_features], contiguous, of `dtype` (bf16 or FP16) as x, base and out.
+ * Adapters of lower rank than the set's have rows of zeros.  Sums are FP32;
+ * hidden keeps 16 bits or more between the products; out is rounded once.
+ * Limits: rank <= 128, features <= 2^20, num_adapters < 65536. */
+typedef struct {
+  int in_features, out_features;
+  int rank;
+  int num_adapters;
+  int dtype; /* MOE_DTYPE_BF16 or MOE_DTYPE_F16 */
+} moe_adapter_config;
+
+/* Operands; strides are row strides in elements.  scales: FP32 [num_adapters],
+ * NULL = 1; base NULL = 0; hidden: FP32 [rows, rank], written for a backward
+ * call, or NULL.  ids: int32 [rows], in any order. */
+typedef struct {
+  const void *x, *base, *down, *up;
+  const int32_t* ids;
+  const float* scales;
+  void* out;
+  float* hidden;
+  void* workspace;     /* moe_adapter_workspace_bytes(cfg, rows, 0), 16-byte aligned */
+  int64_t x_stride, base_stride, out_stride;
+} moe_adapter_io;
+
+/* Device bytes of a forward's (backward 0) or a gradient's workspace; 0 for a
+ * refused cfg or number of rows. */
+MOE_API size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int64_t rows, int backward);
+
+/* out may be base (same stride); other overlaps of an output with another
+ * operand are MOE_ERR_ALIAS.  A row's result does not depend on the rows
+ * around it but through the split of the long axis (by the number of rows and
+ * of the adapter's rows): FP32 rounding of hidden. */
+MOE_API moe_status moe_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows,
+                                       void* stream);
+
+/* Operands of the gradient.  Read: dout [rows, out_features], x, ids, factors
+ * and scales as in the forward, hidden as it wrote it, base [rows, in_features]
+ * or NULL.  Written:
+ *   dx    = base + scales[a] * (dout_t up[a]^T) down[a]
+ *   ddown = sum over the adapter's rows of (scales[a] dout_t up[a]^T)^T x_t
+ *   dup   = sum over the adapter's rows of hidden_t^T dout_t
+ * in the factors' type and layout (zeros for an adapter without rows).  The
+ * scales get no gradient. */
+typedef struct {
+  const void *dout, *x, *base, *down, *up;
+  const int32_t* ids;
+  const float *scales, *hidden;
+  void *dx, *ddown, *dup;
+  void* workspace;     /* moe_adapter_workspace_bytes(cfg, rows, 1), 16-byte aligned */
+  int64_t dout_stride, x_stride, base_stride, dx_stride;
+} moe_adapter_grad_io;
+
+/* dx may be base (same stride); other overlaps are MOE_ERR_ALIAS.  Sums over
+ * rows run in an order fixed by ids and the number of rows: a call repeats bit
+ * for bit. */
+MOE_API moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows,
+                                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

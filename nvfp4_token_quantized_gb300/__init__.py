@@ -29,5 +29,6 @@ from .binding import (  # noqa: F401
     moe_route_noalloc,
     moe_set_static_scales,
 )
+from .adapters import LowRankAdapters  # noqa: F401
 from .gradients import GradientClip  # noqa: F401
 from .operators import BlockNorm, ExpertRouter  # noqa: F401

@@ -47,7 +47,8 @@ EXPORTED = (
     "moe_debug_shared", "moe_debug_shared_act_quant", "moe_route_select", "moe_route_select_backward",
     "moe_set_routing", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
     "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward", "moe_gradient_workspace_bytes",
-    "moe_gradient_norm", "moe_clip_gradients",
+    "moe_gradient_norm", "moe_clip_gradients", "moe_adapter_workspace_bytes", "moe_adapter_forward",
+    "moe_adapter_backward",
 )
 MOE_ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 MOE_NUM_STAGES = 7
@@ -100,6 +101,22 @@ class moe_balance_io(ctypes.Structure):
 class moe_gradient(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
                 ("dtype", ctypes.c_int64)]
+
+
+class moe_adapter_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("in_features", "out_features", "rank", "num_adapters", "dtype")]
+
+
+class moe_adapter_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "base", "down", "up", "ids", "scales", "out", "hidden",
+                                                "workspace")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "base_stride", "out_stride")])
+
+
+class moe_adapter_grad_io(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dout", "x", "base", "down", "up", "ids", "scales", "hidden", "dx",
+                                                "ddown", "dup", "workspace")]
+                + [(n, ctypes.c_int64) for n in ("dout_stride", "x_stride", "base_stride", "dx_stride")])
 
 
 class MoEError(RuntimeError):
@@ -170,6 +187,9 @@ def load_library() -> ctypes.CDLL:
         "moe_gradient_workspace_bytes": (S, []),
         "moe_gradient_norm": (I, [P, L, P, P, P]),
         "moe_clip_gradients": (I, [P, L, F, F, P, P, P]),
+        "moe_adapter_workspace_bytes": (S, [ctypes.POINTER(moe_adapter_config), L, I]),
+        "moe_adapter_forward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_io), L, P]),
+        "moe_adapter_backward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_grad_io), L, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

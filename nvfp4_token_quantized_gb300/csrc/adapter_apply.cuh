@@ -1,0 +1,324 @@
+// adapter_apply.cuh - rows through their adapters: hidden = scale x down^T, out =
+// base + hidden up.  Also the gradient by x, with the factors exchanged.
+//
+// Bound by bytes (x, base and out once each) up to a rank of some 64, so one
+// kernel does both products and the hidden rows never leave the SMs.  A cluster
+// takes a tile of up to 128 rows of one adapter: its CTAs split the first
+// product's long axis, add their parts through distributed shared memory, and
+// split the second product's columns.  Few rows (a decode step) thus still
+// spread over the GPU.  Within a CTA a warp has 16 rows; fewer rows leave more
+// warps for the split.
+//
+// hidden is FP32; the second product takes it as two 16-bit parts (split2), as a
+// single rounding would show beside the output's own.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "adapter_common.cuh"
+
+namespace moe {
+namespace cg = cooperative_groups;
+
+// Row pitch of FP32 tiles in shared memory: the eight rows and four pairs of a
+// fragment fall into different banks.
+__host__ __device__ constexpr int hidden_pitch(int R) { return R + (40 - R % 32) % 32; }
+
+template <int NT>
+struct ApplyShared {
+  static constexpr int R = 8 * NT, RP = hidden_pitch(R), KS = (NT + 1) / 2;
+  static constexpr int PART = ADAPTER_TILE * RP * 4;                        // sums, then fragments
+  static constexpr int FRAGS = (ADAPTER_TILE / 16) * KS * 2 * 512;
+  static constexpr int FIRST = PART > FRAGS ? PART : FRAGS;
+  static constexpr int BYTES = FIRST + PART;
+};
+
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_apply_kernel(const AdapterArgs a) {
+  using S = ApplyShared<NT>;
+  constexpr int R = S::R, RP = S::RP, KS = S::KS;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float* part = reinterpret_cast<float*>(smem);
+  uint4* frags = reinterpret_cast<uint4*>(smem);
+  float* hid = reinterpret_cast<float*>(smem + S::FIRST);
+  __shared__ int row_of[ADAPTER_TILE];
+  __shared__ Piece found;
+  __shared__ int counts[4];  // of a direct call's warps
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
+
+  // ---- the tile's rows ----
+  int group, count;
+  if (a.direct) {
+    // every group is one tile: its rows are found in ids themselves
+    group = number;
+    const bool mine = tid < a.rows && adapter_key(a.ids[tid], a.L) == group;
+    const unsigned m = __ballot_sync(0xffffffffu, mine);
+    if (warp < 4 && lane == 0) counts[warp] = __popc(m);
+    __syncthreads();
+    int before = 0;
+    count = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      before += w < warp ? counts[w] : 0;
+      count += counts[w];
+    }
+    if (mine) row_of[before + __popc(m & ((1u << lane) - 1))] = tid;
+    pdl_wait();
+  } else {
+    pdl_wait();
+    const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
+    group = p.group;
+    count = group < 0 ? 0 : p.count;
+    if (tid < count) row_of[tid] = a.row_list[p.start + tid];
+  }
+  pdl_trigger();
+  if (count == 0) return;  // (the whole cluster)
+  __syncthreads();
+
+  const T* x = static_cast<const T*>(a.x);
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.out);
+  const int K = a.in, N = a.n_out;
+
+  if (group == a.L) {  // no adapter: base alone
+    for (int r = crank * ADAPTER_WARPS + warp; r < count; r += C * ADAPTER_WARPS) {
+      const int64_t row = row_of[r];
+      if (a.hidden)
+        for (int i = lane; i < a.rank; i += 32) a.hidden[row * a.rank + i] = 0.0f;
+      if (out == base && base) continue;
+      for (int c = lane * 8; c < N; c += 256)
+        store8<T, VEC>(out + row * a.out_stride, c, N,
+                       base ? load8<T, VEC>(base + row * a.base_stride, c, N, true) : make_uint4(0, 0, 0, 0));
+    }
+    return;
+  }
+
+  // warps: wm groups of 16 rows, the rest splits the long axes
+  const int wm = count <= 16 ? 1 : count <= 32 ? 2 : count <= 64 ? 4 : 8;
+  const int ways = ADAPTER_WARPS / wm, rg = warp & (wm - 1), way = warp / wm;
+  const int r0 = rg * 16 + g, r1 = r0 + 8;
+  const bool on0 = r0 < count, on1 = r1 < count;
+  const int64_t row0 = on0 ? row_of[r0] : 0, row1 = on1 ? row_of[r1] : 0;
+
+  // ---- hidden: this warp's 16 rows, its share of the long axis ----
+  {
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    const int units = (K + 31) / 32, slices = C * ways;
+    const int per = (units + slices - 1) / slices;
+    const int u0 = (crank * ways + way) * per, u1 = min(units, u0 + per);
+    if (rg * 16 < count) {
+      const T* x0 = x + row0 * a.x_stride;
+      const T* x1 = x + row1 * a.x_stride;
+      const T* w = static_cast<const T*>(a.first) + (int64_t)group * a.rank * K;
+      constexpr int U = NT <= 2 ? 4 : NT <= 8 ? 2 : 1;  // units in flight
+      for (int u = u0; u < u1; u += U) {
+        uint4 q0[U], q1[U], b[U][NT];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int col = (u + i) * 32 + t * 8;
+          const bool in = u + i < u1;
+          q0[i] = load8<T, VEC>(x0, col, K, in && on0);
+          q1[i] = load8<T, VEC>(x1, col, K, in && on1);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            b[i][j] = load8<T, VEC>(w + (int64_t)(8 * j + g) * K, col, K, in && 8 * j + g < a.rank);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint4 first = make_uint4(q0[i].x, q1[i].x, q0[i].y, q1[i].y);
+          const uint4 second = make_uint4(q0[i].z, q1[i].z, q0[i].w, q1[i].w);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma16816(acc[j], first, b[i][j].x, b[i][j].y, T());
+            mma16816(acc[j], second, b[i][j].z, b[i][j].w, T());
+          }
+        }
+      }
+    }
+    // part[way][row][rank]
+    float* p0 = part + ((way * wm + rg) * 16 + g) * RP + 2 * t;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      *reinterpret_cast<float2*>(p0 + 8 * j) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2*>(p0 + 8 * RP + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+    }
+  }
+  __syncthreads();
+  // ---- its parts added: the CTA's ways, then the cluster's CTAs ----
+  const float scale = a.scales ? a.scales[group] : 1.0f;
+  cg::cluster_group cluster = cg::this_cluster();
+  if (C > 1) {
+    if (ways > 1) {
+      for (int i = tid; i < count * R; i += ADAPTER_THREADS) {
+        float* p = part + (i / R) * RP + i % R;
+        float s = *p;
+        for (int w = 1; w < ways; ++w) s += p[w * wm * 16 * RP];
+        *p = s;
+      }
+    }
+    cluster.sync();
+  }
+  for (int i = crank * ADAPTER_THREADS + tid; i < count * R; i += C * ADAPTER_THREADS) {
+    const int r = i / R, c = i % R, at = r * RP + c;
+    float s = 0.0f;
+    if (C > 1) {
+      for (int p = 0; p < C; ++p) s += cluster.map_shared_rank(part, p)[at];
+    } else {
+      for (int w = 0; w < ways; ++w) s += part[w * wm * 16 * RP + at];
+    }
+    s *= scale;
+    if (a.hidden && c < a.rank) a.hidden[(int64_t)row_of[r] * a.rank + c] = s;
+    if (C > 1) {
+      for (int p = 0; p < C; ++p) cluster.map_shared_rank(hid, p)[at] = s;
+    } else {
+      hid[at] = s;
+    }
+  }
+  if (C > 1)
+    cluster.sync();  // (the last access to another CTA's shared memory lies before)
+  else
+    __syncthreads();
+
+  // ---- hidden as fragments, two parts each ----
+  float back0 = 1.0f, back1 = 1.0f;
+  {
+    const float* h0 = hid + r0 * RP + 2 * t;
+    const float* h1 = h0 + 8 * RP;
+    float s0 = 1.0f, s1 = 1.0f;
+    if constexpr (sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value) {
+      float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (on0) m0 = fmaxf(m0, fmaxf(fabsf(h0[8 * j]), fabsf(h0[8 * j + 1])));
+        if (on1) m1 = fmaxf(m1, fmaxf(fabsf(h1[8 * j]), fabsf(h1[8 * j + 1])));
+      }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+      }
+      s0 = exponent_scale(m0, back0);
+      s1 = exponent_scale(m1, back1);
+    }
+    for (int ks = way; ks < KS; ks += ways) {
+      float v[4][2];  // row 0 and 1 at the first eight ranks, then at the second
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 16 * ks + 8 * (q >> 1);
+        const bool have = c < R && (q & 1 ? on1 : on0);
+        const float2 f = have ? *reinterpret_cast<const float2*>((q & 1 ? h1 : h0) + c) : make_float2(0.0f, 0.0f);
+        const float s = q & 1 ? s1 : s0;
+        v[q][0] = f.x * s;
+        v[q][1] = f.y * s;
+      }
+      uint4 hi, lo;
+      split2<T>(v[0][0], v[0][1], hi.x, lo.x);
+      split2<T>(v[1][0], v[1][1], hi.y, lo.y);
+      split2<T>(v[2][0], v[2][1], hi.z, lo.z);
+      split2<T>(v[3][0], v[3][1], hi.w, lo.w);
+      frags[((rg * KS + ks) * 2) * 32 + lane] = hi;
+      frags[((rg * KS + ks) * 2 + 1) * 32 + lane] = lo;
+    }
+  }
+  __syncthreads();
+  if (rg * 16 >= count) return;
+
+  // ---- out: 64 columns at a time ----
+  const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
+  for (int n0 = (crank * ways + way) * 64; n0 < N; n0 += C * ways * 64) {
+    const int oc = n0 + 16 * t;
+    uint4 y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      y[q] = base ? load8<T, VEC>(base + (q & 1 ? row1 : row0) * a.base_stride, oc + 8 * (q >> 1), N, q & 1 ? on1 : on0)
+                  : make_uint4(0, 0, 0, 0);
+    float d[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint4 b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = 16 * ks + 2 * t + (q & 1) + 8 * (q >> 1);
+        b[q] = load8<T, VEC>(up + (int64_t)k * N, n0 + 8 * g, N, k < a.rank);
+      }
+      const uint4 hi = frags[((rg * KS + ks) * 2) * 32 + lane], lo = frags[((rg * KS + ks) * 2 + 1) * 32 + lane];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b0 = pair_of(b[0], b[1], j), b1 = pair_of(b[2], b[3], j);
+        mma16816(d[j], hi, b0, b1, T());
+        mma16816(d[j], lo, b0, b1, T());
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // columns oc + 8 * (q >> 1) + 0..7 of row q & 1: d[0..7][i]
+      const int i = (q & 1) * 2 + (q >> 1);
+      const float back = q & 1 ? back1 : back0;
+      const uint32_t w[4] = {y[q].x, y[q].y, y[q].z, y[q].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 f = unpack2(w[p], T());
+        o[p] = pack2(fmaf(d[2 * p][i], back, f.x), fmaf(d[2 * p + 1][i], back, f.y), T());
+      }
+      if (q & 1 ? on1 : on0)
+        store8<T, VEC>(out + (q & 1 ? row1 : row0) * a.out_stride, oc + 8 * (q >> 1), N,
+                       make_uint4(o[0], o[1], o[2], o[3]));
+    }
+  }
+}
+
+template <typename T, int NT, bool VEC>
+cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s, bool pdl) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = adapter_apply_kernel<T, NT, VEC>;
+  constexpr int bytes = ApplyShared<NT>::BYTES;
+  if (bytes > 46 * 1024) {
+    const cudaError_t e = raise_shared(kernel, bytes, done);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.cluster));
+  cfg.blockDim = dim3(ADAPTER_THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)a.cluster, 1, 1};
+  cfg.numAttrs = 1;
+  if (pdl) {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T>
+cudaError_t launch_apply(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s) {
+  switch ((a.rank + 7) / 8) {
+#define MOE_APPLY(NT) return vec ? launch_apply_one<T, NT, true>(a, s, pdl) : launch_apply_one<T, NT, false>(a, s, pdl)
+    case 1: MOE_APPLY(1);
+    case 2: MOE_APPLY(2);
+    case 3: MOE_APPLY(3);
+    case 4: MOE_APPLY(4);
+    case 5:
+    case 6: MOE_APPLY(6);
+    case 7:
+    case 8: MOE_APPLY(8);
+  }
+  MOE_APPLY(16);
+#undef MOE_APPLY
+}
+
+}  // namespace moe

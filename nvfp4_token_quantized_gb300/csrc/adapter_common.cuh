@@ -1,0 +1,133 @@
+// adapter_common.cuh - what the kernels of the low-rank adapters share: the
+// tensor cores' 16 x 8 x 16 product on register fragments, loads of eight
+// neighbouring elements, and the rows grouped by adapter.
+//
+// Fragments without shared memory.  A product may number its contraction and
+// its columns as it likes, as long as both operands agree, so each lane loads
+// 16 bytes of a row and hands them out to the fragments in the order it has:
+//  - contraction along the rows' long axis (hidden = x down^T): of 32 elements a
+//    lane (quad position t) holds 8t .. 8t+7; elements 0..3 are its four of the
+//    first product, 4..7 those of the second, in both operands;
+//  - contraction across rows (out = hidden up, gradients): a lane loads columns
+//    8g .. 8g+7 (g = lane / 4) of rows 2t, 2t+1, 2t+8, 2t+9; product j of eight
+//    takes column 8g + j from it, so the eight accumulators of a lane hold 16
+//    neighbouring columns, which are moved by two 16-byte accesses a row.
+#pragma once
+
+#include "common.cuh"
+#include "elem_types.cuh"
+#include "kernels_ops.h"
+
+namespace moe {
+
+constexpr int ADAPTER_THREADS = 256;
+constexpr int ADAPTER_WARPS = ADAPTER_THREADS / 32;
+constexpr int ADAPTER_TILE = 128;  // rows of a tile: 16 a warp
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Elements col .. col+7 of a row, zeros from `width` on and where !on.  VEC:
+// rows start on 16 bytes and width is a multiple of 8.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load8(const T* row, int col, int width, bool on) {
+  uint4 q = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (on && col < width) q = *reinterpret_cast<const uint4*>(row + col);
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + col;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = on && col + i < width ? p[i] : 0u;
+    q = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+  return q;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* row, int col, int width, const uint4& q) {
+  if constexpr (VEC) {
+    if (col < width) *reinterpret_cast<uint4*>(row + col) = q;
+  } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < width) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// Element j of two rows' eight, packed (the first row's in the low half).
+__device__ __forceinline__ uint32_t pair_of(const uint4& a, const uint4& b, int j) {
+  const uint32_t wa = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
+  const uint32_t wb = j < 2 ? b.x : j < 4 ? b.y : j < 6 ? b.z : b.w;
+  return __byte_perm(wa, wb, j & 1 ? 0x7632 : 0x5410);
+}
+
+// Two FP32 values as T plus what T leaves of them, as T: hi + lo keeps 16 bits
+// and more (22 for FP16 near 1), so a product with both loses nothing that the
+// output's own rounding would show.
+template <typename T>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(a, b, T());
+  const float2 h = unpack2(hi, T());
+  lo = pack2(isinf(h.x) ? 0.0f : a - h.x, isinf(h.y) ? 0.0f : b - h.y, T());
+}
+
+// 2^-e and 2^e for values up to m in size, e the exponent of m: FP16 fragments
+// of scaled values neither overflow nor lose small ones.  1 for 0, infinity and
+// NaN.
+__device__ __forceinline__ float exponent_scale(float m, float& back) {
+  const int e = (int)(__float_as_uint(m) >> 23);  // m >= 0
+  const bool plain = e == 0 || e == 255;
+  // (2^-e of a biased exponent e is 254 - e: kept a normal number)
+  const int b = plain ? 127 : min(max(e, 1), 253);
+  back = __uint_as_float((uint32_t)b << 23);
+  return __uint_as_float((uint32_t)(254 - b) << 23);
+}
+
+// ---- rows by adapter ----
+
+// Adapter a's rows are rows[starts[a]] .. rows[starts[a + 1] - 1], in ascending
+// order; group L holds the rows without an adapter, starts[L + 1] = T.
+__device__ __forceinline__ int adapter_key(int id, int L) { return (unsigned)id < (unsigned)L ? id : L; }
+
+// Pieces of `unit` rows of the groups: group a's pieces have the numbers
+// starts[a] / unit + a and up; numbers between two groups' may be unused.
+struct Piece {
+  int group;
+  int start, count;  // in rows[]
+  int number;        // of the group's pieces
+};
+
+__host__ __device__ __forceinline__ int64_t pieces_of(int64_t rows, int64_t groups, int unit) {
+  return rows / unit + groups;
+}
+
+// The piece of a number, by all threads of the CTA; group -1 for an unused
+// number.  `found` is shared.
+__device__ __forceinline__ Piece find_piece(const int32_t* starts, int groups, int unit, int number, Piece* found) {
+  if (threadIdx.x == 0) found->group = -1;
+  __syncthreads();
+  for (int a = threadIdx.x; a < groups; a += blockDim.x) {
+    const int lo = starts[a], hi = starts[a + 1];
+    const int i = number - (lo / unit + a);
+    if (i >= 0 && lo + (int64_t)i * unit < hi) {
+      const int at = lo + i * unit;
+      *found = {a, at, min(unit, hi - at), i};
+    }
+  }
+  __syncthreads();
+  return *found;
+}
+
+}  // namespace moe

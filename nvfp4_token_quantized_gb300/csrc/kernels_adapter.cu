@@ -1,0 +1,148 @@
+// kernels_adapter.cu - low-rank adapters of many requests: rows grouped by their
+// adapter, and the launches of a forward and of the gradients.
+#include <algorithm>
+
+#include "adapter_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int PLAN_THREADS = 1024;
+constexpr unsigned ALL = 0xffffffffu;
+
+// Group blockIdx.x (an adapter, or L for rows without one): its first place,
+// the number of rows of the groups before it, and its rows in ascending order.
+// Every CTA goes through all ids, 16 a thread and round: no CTA waits for
+// another.
+__global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_t* ids, int rows, int L,
+                                                                    int32_t* starts, int32_t* row_list) {
+  constexpr int PER = 16, ROUND = PLAN_THREADS * PER;
+  __shared__ int warp_sum[32], below;
+  pdl_trigger();
+  const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) below = 0;
+  __syncthreads();
+  int less = 0;
+  for (int64_t i = tid; i < rows; i += PLAN_THREADS) less += adapter_key(ids[i], L) < group;
+  less = __reduce_add_sync(ALL, less);
+  if (lane == 0 && less) atomicAdd(&below, less);
+  __syncthreads();
+  int at = below;
+  if (tid == 0) {
+    starts[group] = at;
+    if (group == L) starts[L + 1] = rows;
+  }
+  for (int64_t base = 0; base < rows; base += ROUND) {
+    unsigned mine = 0;
+    const int64_t first = base + tid * PER;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (first + i < rows && adapter_key(ids[first + i], L) == group) mine |= 1u << i;
+    const int n = __popc(mine);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(ALL, upto, o);
+      if (lane >= o) upto += v;
+    }
+    __syncthreads();  // (the round before has read the warps' sums)
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    const int w = warp_sum[lane];
+    const int before = __reduce_add_sync(ALL, lane < warp ? w : 0), all = __reduce_add_sync(ALL, w);
+    int put = at + before + upto - n;
+    while (mine) {
+      row_list[put++] = (int32_t)(first + __ffs(mine) - 1);
+      mine &= mine - 1;
+    }
+    at += all;
+  }
+}
+
+int64_t words16(int64_t n) { return (n + 3) / 4 * 4; }
+
+// Where the parts of a workspace lie, in 4-byte words, 16-byte aligned.
+struct Layout {
+  int64_t starts, row_list, hidden, sums[2], end;
+};
+
+int outer_unit(int64_t rows) {
+  // about sixteen pieces of a large batch: with eight column blocks a side that
+  // fills the SMs, and the pieces' FP32 sums stay small beside the rows
+  const int64_t unit = (rows + 15) / 16;
+  return (int)std::min<int64_t>(std::max<int64_t>((unit + 63) / 64 * 64, 64), 1024);
+}
+
+Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
+  Layout l{};
+  l.starts = 0;
+  l.row_list = words16(c.num_adapters + 2);
+  l.hidden = l.row_list + words16(rows);
+  l.sums[0] = l.hidden + (backward ? words16(rows * c.rank) : 0);
+  const int64_t pieces = backward ? pieces_of(rows, c.num_adapters, outer_unit(rows)) : 0;
+  l.sums[1] = l.sums[0] + words16(pieces * c.rank * c.in_features);
+  l.end = l.sums[1] + words16(pieces * c.rank * c.out_features);
+  return l;
+}
+
+cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
+  return launch_k(adapter_plan_kernel, dim3((unsigned)a.L + 1), dim3(PLAN_THREADS), 0, s, false, a.ids, (int)a.rows,
+                  a.L, const_cast<int32_t*>(a.starts), const_cast<int32_t*>(a.row_list));
+}
+
+// CTAs of a cluster: enough for some two CTAs an SM.
+int cluster_of(int64_t tiles, int64_t rows, int L) {
+  const int64_t full = std::min<int64_t>(rows, (rows + ADAPTER_TILE - 1) / ADAPTER_TILE + std::min<int64_t>(L, rows) / 2);
+  const int64_t t = std::min(tiles, full);
+  return t >= 304 ? 1 : t >= 152 ? 2 : t >= 60 ? 4 : 8;
+}
+
+cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
+  a.direct = !planned;
+  a.tiles = planned ? pieces_of(a.rows, a.L + 1, ADAPTER_TILE) : a.L + 1;
+  a.cluster = cluster_of(a.tiles, a.rows, a.L);
+  return f16 ? launch_apply_f16(a, vec, planned, s) : launch_apply_bf16(a, vec, planned, s);
+}
+
+}  // namespace
+
+size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward) {
+  return (size_t)layout(c, rows, backward).end * 4;
+}
+
+cudaError_t launch_adapter(AdapterArgs a, const moe_adapter_config& c, bool vec, void* workspace, cudaStream_t s) {
+  const Layout l = layout(c, a.rows, false);
+  int32_t* w = static_cast<int32_t*>(workspace);
+  a.starts = w + l.starts;
+  a.row_list = w + l.row_list;
+  const bool planned = a.rows > ADAPTER_TILE;
+  if (planned) {
+    const cudaError_t e = launch_plan(a, s);
+    if (e != cudaSuccess) return e;
+  }
+  return apply(a, c.dtype == MOE_DTYPE_F16, vec, planned, s);
+}
+
+cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapter_config& c, bool vec, void* workspace,
+                                    cudaStream_t s) {
+  const Layout l = layout(c, a.rows, true);
+  int32_t* w = static_cast<int32_t*>(workspace);
+  a.starts = o.starts = w + l.starts;
+  a.row_list = o.row_list = w + l.row_list;
+  a.hidden = reinterpret_cast<float*>(w + l.hidden);
+  const bool f16 = c.dtype == MOE_DTYPE_F16;
+  cudaError_t e = launch_plan(a, s);
+  if (e == cudaSuccess) e = apply(a, f16, vec, true, s);
+  if (e != cudaSuccess) return e;
+  o.hidden[0] = a.hidden;  // down's gradient goes by dout up^T, up's by the forward's hidden
+  o.sums[0] = reinterpret_cast<float*>(w + l.sums[0]);
+  o.sums[1] = reinterpret_cast<float*>(w + l.sums[1]);
+  o.rows = a.rows;
+  o.L = a.L;
+  o.rank = a.rank;
+  o.unit = outer_unit(a.rows);
+  for (int i = 0; i < 2; ++i) o.blocks[i] = (o.width[i] + 511) / 512;
+  return f16 ? launch_outer_f16(o, vec, s) : launch_outer_bf16(o, vec, s);
+}
+
+}  // namespace moe

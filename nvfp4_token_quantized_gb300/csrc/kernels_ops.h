@@ -5,9 +5,25 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_nvfp4.h"
 
 namespace moe {
+
+// Raises a kernel's dynamic shared memory to `bytes` once for each device;
+// `done` holds a bit a device between calls.
+template <typename K>
+cudaError_t raise_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 constexpr int SELECT_MAX_EXPERTS = 512;
 constexpr int SELECT_MAX_TOPK = 32;    // a slot per lane
@@ -109,5 +125,52 @@ struct ClipArgs {
 };
 
 cudaError_t launch_clip(const moe_gradient* tensors, int64_t num, const ClipArgs& a, cudaStream_t s);
+
+// ---- low-rank adapters (kernels_adapter.cu) ----
+
+constexpr int ADAPTER_MAX_RANK = 128;
+
+// out = base + (scale x first^T) second, a row's factors by its adapter.
+struct AdapterArgs {
+  const void *x, *base;
+  void* out;
+  int64_t x_stride, base_stride, out_stride;
+  const int32_t* ids;
+  const void *first, *second;  // [L, rank, in], [L, rank, n_out]
+  const float* scales;
+  float* hidden;  // [rows, rank] or NULL
+  int64_t rows;
+  int in, n_out, rank, L;
+  // set by the launch
+  const int32_t *starts, *row_list;
+  int64_t tiles;
+  int cluster;
+  bool direct;  // up to 128 rows: each CTA finds its own
+};
+
+// Gradients of both factors: sums over an adapter's rows of hidden^T x.
+struct OuterArgs {
+  const void* x[2];
+  int64_t stride[2];
+  const float* hidden[2];
+  void* grad[2];
+  int width[2];
+  // set by the launch
+  const int32_t *starts, *row_list;
+  float* sums[2];
+  int64_t rows;
+  int L, rank, unit, blocks[2];
+};
+
+size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward);
+// vec: every row starts on 16 bytes and both widths are multiples of 8.
+cudaError_t launch_adapter(AdapterArgs a, const moe_adapter_config& c, bool vec, void* workspace, cudaStream_t s);
+// a: the gradient by x (its first factor is up); hidden[0] is set by the launch.
+cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapter_config& c, bool vec, void* workspace,
+                                    cudaStream_t s);
+cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
+cudaError_t launch_apply_f16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
+cudaError_t launch_outer_bf16(const OuterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_outer_f16(const OuterArgs& a, bool vec, cudaStream_t s);
 
 }  // namespace moe

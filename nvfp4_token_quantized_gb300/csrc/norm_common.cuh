@@ -63,20 +63,6 @@ constexpr int NORM_SMALL_CTA = 128;  // threads of a CTA whose rows take a warp 
 inline int row_cta_threads(int lanes) { return lanes > 32 ? lanes : NORM_SMALL_CTA; }
 inline int rows_per_cta(int lanes) { return row_cta_threads(lanes) / lanes; }
 
-// Raises a kernel's dynamic shared memory to `bytes` once for each device;
-// `done` holds a bit a device between calls.
-template <typename K>
-cudaError_t raise_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 // Sums over a row's threads of N values at a time; every thread gets the same
 // bits.  Inside a warp several values are summed together: each step of the
 // tree hands half of them to the other half of the lanes, so four values take

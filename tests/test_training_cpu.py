@@ -134,3 +134,68 @@ def test_aligned_calls_reach_the_device_check(lib):
     assert _clip(lib, b, a) == UNSUPPORTED and _clip(lib) == UNSUPPORTED
     assert _clip(lib, (MB, 3 * MB, 100, F32), (MB, 4 * MB, 100, F32)) == UNSUPPORTED  # (one source, read twice)
     assert _loss(lib) == UNSUPPORTED and _loss(lib, T=0, logits=None, topk_ids=None) == UNSUPPORTED
+
+
+def _adapter_cfg(K=64, N=96, r=8, L=4, dtype=BF16):
+    from nvfp4_token_quantized_gb300.binding import moe_adapter_config
+
+    return ctypes.byref(moe_adapter_config(K, N, r, L, dtype))
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({}, OK), (dict(r=128, dtype=F16), OK), (dict(K=1, N=1, r=1, L=1), OK), (dict(K=0), INVALID), (dict(N=-1), INVALID),
+    (dict(r=0), INVALID), (dict(L=0), INVALID), (dict(dtype=F32), INVALID), (dict(dtype=0), INVALID),
+    (dict(r=129), UNSUPPORTED), (dict(K=(1 << 20) + 1), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED),
+    (dict(L=65536), UNSUPPORTED),
+])
+def test_adapter_configurations(lib, kw, status):
+    from nvfp4_token_quantized_gb300.binding import moe_adapter_grad_io, moe_adapter_io
+
+    cfg = _adapter_cfg(**kw)
+    assert lib.moe_adapter_forward(cfg, ctypes.byref(moe_adapter_io()), 0, None) == status
+    assert (lib.moe_adapter_workspace_bytes(cfg, 10, 0) > 0) == (status == OK)
+    assert lib.moe_adapter_workspace_bytes(cfg, 10, 1) >= lib.moe_adapter_workspace_bytes(cfg, 10, 0)
+    assert lib.moe_adapter_workspace_bytes(cfg, -1, 0) == 0
+    if status != OK:
+        assert lib.moe_adapter_backward(cfg, ctypes.byref(moe_adapter_grad_io()), 4, None) == status
+
+
+def test_adapter_operands(lib):
+    from nvfp4_token_quantized_gb300.binding import moe_adapter_io
+
+    def call(rows=200, **kw):
+        d = dict(x=MB, base=2 * MB, down=3 * MB, up=4 * MB, ids=5 * MB, scales=6 * MB, out=7 * MB, hidden=8 * MB,
+                 workspace=9 * MB, x_stride=64, base_stride=96, out_stride=96)
+        d.update(kw)
+        return lib.moe_adapter_forward(_adapter_cfg(), ctypes.byref(moe_adapter_io(**d)), rows, None)
+
+    assert lib.moe_adapter_forward(None, None, 0, None) == INVALID
+    assert lib.moe_adapter_forward(_adapter_cfg(), None, 0, None) == INVALID
+    for bad in (dict(rows=-1), dict(rows=1 << 31), dict(x=None), dict(down=None), dict(up=None), dict(ids=None),
+                dict(out=None), dict(workspace=None), dict(workspace=9 * MB + 8), dict(x=MB + 1), dict(base=2 * MB + 1),
+                dict(down=3 * MB + 1), dict(ids=5 * MB + 2), dict(scales=6 * MB + 2), dict(hidden=8 * MB + 2),
+                dict(x_stride=63), dict(out_stride=95), dict(base_stride=0), dict(x_stride=1 << 60)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(out=MB), dict(out=3 * MB), dict(out=4 * MB), dict(out=5 * MB), dict(out=6 * MB), dict(out=8 * MB),
+                dict(out=9 * MB), dict(hidden=MB), dict(workspace=7 * MB), dict(out=2 * MB + 192),
+                dict(out=2 * MB, out_stride=104)):
+        assert call(**bad) == ALIAS, bad
+
+
+def test_adapter_gradient_operands(lib):
+    from nvfp4_token_quantized_gb300.binding import moe_adapter_grad_io
+
+    def call(rows=200, **kw):
+        d = dict(dout=MB, x=2 * MB, base=None, down=3 * MB, up=4 * MB, ids=5 * MB, scales=None, hidden=6 * MB, dx=7 * MB,
+                 ddown=8 * MB, dup=9 * MB, workspace=10 * MB, dout_stride=96, x_stride=64, base_stride=64, dx_stride=64)
+        d.update(kw)
+        return lib.moe_adapter_backward(_adapter_cfg(), ctypes.byref(moe_adapter_grad_io(**d)), rows, None)
+
+    assert lib.moe_adapter_backward(_adapter_cfg(), None, 0, None) == INVALID
+    for bad in (dict(dout=None), dict(x=None), dict(down=None), dict(up=None), dict(ids=None), dict(hidden=None),
+                dict(dx=None), dict(ddown=None), dict(dup=None), dict(workspace=None), dict(workspace=10 * MB + 4),
+                dict(dx_stride=63), dict(rows=-1), dict(rows=0, ddown=None), dict(base=11 * MB, base_stride=60)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(dx=2 * MB), dict(dx=MB), dict(ddown=3 * MB), dict(dup=4 * MB), dict(dup=8 * MB), dict(dx=6 * MB),
+                dict(workspace=7 * MB), dict(base=7 * MB + 128), dict(base=7 * MB, base_stride=72)):
+        assert call(**bad) == ALIAS, bad
