@@ -584,7 +584,8 @@ typedef struct {
   int dtype; /* moe_dtype of the logits */
 } moe_balance_io;
 
-/* Device bytes moe_balance_loss needs; 0 for a refused cfg or sizes. */
+/* Device bytes moe_balance_loss needs: 0 for one sequence of few tokens (then
+ * workspace may be NULL), and for a refused cfg or sizes. */
 MOE_API size_t moe_balance_workspace_bytes(const moe_route_config* cfg, int64_t num_tokens, int64_t num_sequences);
 
 /* loss: FP32 scalar; counts: int32 [num_sequences, num_experts]; slope: FP32 of

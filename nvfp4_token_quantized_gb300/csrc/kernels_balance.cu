@@ -28,6 +28,8 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_AT_ONCE = 2 * WARPS;  // sixteen lanes a row
 constexpr int JOIN = 8;                  // CTAs of a cluster that joins the runs' sums
+constexpr int JOIN_THREADS = 1024;       // of a CTA that joins all runs of a batch
+constexpr int OFFSETS = 1024;            // that a CTA keeps in shared memory
 constexpr unsigned ALL = 0xffffffffu;
 
 // Four neighbouring elements of a row, as loaded.
@@ -184,42 +186,61 @@ __device__ __forceinline__ int64_t bound_of(const BalanceArgs& a, int64_t i) {
   return v < 0 ? 0 : v > a.rows ? a.rows : v;
 }
 
-// The sequence that row `row` lies in or before (block-wide: a count of the
-// ends at or before it).
-__device__ __forceinline__ int64_t first_sequence(const BalanceArgs& a, int64_t row, int* count) {
-  if (!a.offsets) return 0;
-  if (threadIdx.x == 0) *count = 0;
-  __syncthreads();
-  int n = 0;
-  for (int64_t i = threadIdx.x; i < a.sequences; i += THREADS) n += bound_of(a, i + 1) <= row;
-  n = __reduce_add_sync(ALL, n);
-  if ((threadIdx.x & 31) == 0 && n) atomicAdd(count, n);
-  __syncthreads();
-  return *count;
-}
-
-// The run that starts at row `at` < end; seq moves on to its sequence.  It
-// ends behind `at` whatever the offsets hold.
-__device__ __forceinline__ Run next_run(const BalanceArgs& a, int64_t at, int64_t end, int64_t& seq) {
-  if (!a.offsets) return {at, end, 0};
-  while (seq < a.sequences && bound_of(a, seq + 1) <= at) ++seq;
-  if (seq >= a.sequences) return {at, end, -1};
-  const int64_t lo = bound_of(a, seq), hi = bound_of(a, seq + 1);
-  if (at < lo) return {at, lo < end ? lo : end, -1};
-  return {at, hi < end ? hi : end, seq};
-}
+// A CTA's walk through the sequences; the first offsets are kept in shared
+// memory, which spares every step one latency of L2.
+struct Walk {
+  int bounds[OFFSETS];
+  int count;
+  // The sequence that row `row` lies in or before: the number of ends at or
+  // before it, counted by all threads.
+  __device__ __forceinline__ int64_t first(const BalanceArgs& a, int64_t row) {
+    if (!a.offsets) return 0;
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    int n = 0;
+    for (int64_t i = threadIdx.x; i <= a.sequences; i += THREADS) {
+      const int64_t v = bound_of(a, i);
+      if (i < OFFSETS) bounds[i] = (int)v;
+      n += i > 0 && v <= row;
+    }
+    n = __reduce_add_sync(ALL, n);
+    if ((threadIdx.x & 31) == 0 && n) atomicAdd(&count, n);
+    __syncthreads();
+    return count;
+  }
+  __device__ __forceinline__ int64_t at(const BalanceArgs& a, int64_t i) const {
+    return i < OFFSETS ? bounds[i] : bound_of(a, i);
+  }
+  // The run that starts at row `from` < end; seq moves on to its sequence.  It
+  // ends behind `from` whatever the offsets hold.
+  __device__ __forceinline__ Run next(const BalanceArgs& a, int64_t from, int64_t end, int64_t& seq) const {
+    if (!a.offsets) return {from, end, 0};
+    while (seq < a.sequences && at(a, seq + 1) <= from) ++seq;
+    if (seq >= a.sequences) return {from, end, -1};
+    const int64_t lo = at(a, seq), hi = at(a, seq + 1);
+    if (from < lo) return {from, lo < end ? lo : end, -1};
+    return {from, hi < end ? hi : end, seq};
+  }
+};
 
 // Words of a run's sums: E sums of shares, E counts, the tokens.
 __host__ __device__ __forceinline__ int part_words(int E) { return 2 * E + 1; }
 
+template <int THREADS>
+struct JoinShared {
+  float sums[THREADS];
+  int counts[THREADS];
+  int tokens;
+  float loss;
+};
 struct SumShared {
   float sums[WARPS][SELECT_MAX_EXPERTS];
   int counts[SELECT_MAX_EXPERTS];
-  int tokens, sequence;
-  uint32_t part[2 * SELECT_MAX_EXPERTS + 1];  // (of a cluster that joins its own)
-  float join_sum[THREADS];
-  int join_count[THREADS];
-  float loss;
+  int tokens;
+};
+struct SmallShared {  // of a cluster that joins its own sums
+  uint32_t part[2 * SELECT_MAX_EXPERTS + 1];
+  JoinShared<THREADS> join;
 };
 
 // Sums and counts of rows [lo, hi) into dst (global or shared).
@@ -233,9 +254,13 @@ __device__ __forceinline__ void sum_run(const BalanceArgs& a, int64_t lo, int64_
   __syncthreads();
 
   const T* logits = static_cast<const T*>(a.logits);
-  const auto fetch = [&](int64_t row, Part& p) {
-    const bool on = row < hi && (!a.mask || a.mask[row]);
-    p.load(logits + row * a.stride, a.E, sub, on, minus_infinity<T>());
+  // (a lane also brings slots sub and sub + 16 of its row's chosen experts)
+  const auto fetch = [&](int64_t row, Part& p, int (&id)[2]) {
+    const bool in = row < hi;
+    const bool on = in && (!a.mask || a.mask[row]);  // (a load beside the others, not before them)
+    p.load(logits + row * a.stride, a.E, sub, in, minus_infinity<T>());
+    id[0] = in && sub < a.K ? a.ids[row * a.K + sub] : -1;
+    id[1] = in && sub + 16 < a.K ? a.ids[row * a.K + sub + 16] : -1;
     return on;
   };
   float acc[N];
@@ -243,21 +268,20 @@ __device__ __forceinline__ void sum_run(const BalanceArgs& a, int64_t lo, int64_
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
   int mine = 0;
   Part cur;
-  bool on = fetch(lo + warp * 2 + half, cur);
-
-  // (the chosen experts while the first rows are on their way)
-  const uint32_t slots = (uint32_t)((hi - lo) * a.K);
-  const int32_t* ids = a.ids + lo * a.K;
-  for (uint32_t i = threadIdx.x; i < slots; i += THREADS) {
-    const int id = ids[i];
-    if ((unsigned)id < (unsigned)a.E && (!a.mask || a.mask[lo + i / (uint32_t)a.K])) atomicAdd(&sh.counts[id], 1);
-  }
-
+  int id[2];
+  bool on = fetch(lo + warp * 2 + half, cur, id);
   for (int64_t base = lo + warp * 2; base < hi; base += ROWS_AT_ONCE) {
     Part nxt;
-    const bool nxt_on = fetch(base + ROWS_AT_ONCE + half, nxt);
+    int nxt_id[2];
+    const bool nxt_on = fetch(base + ROWS_AT_ONCE + half, nxt, nxt_id);
+    if (on && (unsigned)id[0] < (unsigned)a.E) atomicAdd(&sh.counts[id[0]], 1);
+    if (on && (unsigned)id[1] < (unsigned)a.E) atomicAdd(&sh.counts[id[1]], 1);
     float x[N];
     cur.values(x);
+    if (a.mask && !on) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+    }
     float none[1], inv;
     if (a.sigmoid)
       inv = sigmoid_scores<N, false>(x, none);
@@ -268,6 +292,8 @@ __device__ __forceinline__ void sum_run(const BalanceArgs& a, int64_t lo, int64_
     mine += on;
     cur = nxt;
     on = nxt_on;
+    id[0] = nxt_id[0];
+    id[1] = nxt_id[1];
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -290,8 +316,9 @@ __device__ __forceinline__ void sum_run(const BalanceArgs& a, int64_t lo, int64_
 
 // Joins `parts` runs' sums of sequence s: the cluster's CTAs take an eighth of
 // the experts each, and in a CTA groups of threads every so many runs.
-template <typename PartAt>
-__device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int parts, PartAt part_at, SumShared& sh) {
+template <int THREADS, typename PartAt>
+__device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int parts, PartAt part_at,
+                                           JoinShared<THREADS>& sh) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int width = (a.E + JOIN - 1) / JOIN, groups = THREADS / width;
@@ -301,26 +328,36 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
   float sum = 0.0f;
   int count = 0, tokens = 0;
   if (group < groups && e < a.E) {
-#pragma unroll 4
-    for (int p = group; p < parts; p += groups) {
-      const uint32_t* w = part_at(p);
-      sum += __uint_as_float(w[e]);
-      count += (int)w[a.E + e];
+    constexpr int U = 8;  // runs whose loads are in flight together
+    for (int p = group; p < parts; p += groups * U) {
+      uint32_t s[U], c[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool on = p + u * groups < parts;
+        const uint32_t* w = part_at(on ? p + u * groups : p);
+        s[u] = on ? w[e] : 0u;
+        c[u] = on ? w[a.E + e] : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        sum += __uint_as_float(s[u]);
+        count += (int)c[u];
+      }
     }
   }
   for (int p = threadIdx.x; p < parts; p += THREADS) tokens += (int)part_at(p)[2 * a.E];
   tokens = __reduce_add_sync(ALL, tokens);
   if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(&sh.tokens, tokens);
-  sh.join_sum[threadIdx.x] = sum;
-  sh.join_count[threadIdx.x] = count;
+  sh.sums[threadIdx.x] = sum;
+  sh.counts[threadIdx.x] = count;
   __syncthreads();
   const float n = (float)max(sh.tokens, 1);
   const float unit = a.coefficient * ((float)a.E / (float)a.K) / n;
   float term = 0.0f;
   if (group == 0 && e < a.E) {
     for (int g = 1; g < groups; ++g) {
-      sum += sh.join_sum[g * width + local];
-      count += sh.join_count[g * width + local];
+      sum += sh.sums[g * width + local];
+      count += sh.counts[g * width + local];
     }
     a.counts[s * a.E + e] = count;
     const float slope = unit * (float)count / n;
@@ -329,10 +366,10 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
   }
   // (experts of a CTA: at most 64, so two warps hold terms)
   __syncthreads();
-  sh.join_sum[threadIdx.x] = term;
+  sh.sums[threadIdx.x] = term;
   __syncthreads();
   if (threadIdx.x < 32) {
-    float v = sh.join_sum[threadIdx.x] + sh.join_sum[threadIdx.x + 32];
+    float v = sh.sums[threadIdx.x] + sh.sums[threadIdx.x + 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
     if (threadIdx.x == 0) sh.loss = v;
@@ -351,41 +388,55 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
   cluster.sync();  // (shared memory stays until every CTA has read it)
 }
 
-// A CTA sums its block of rows, run by run.  One cluster alone joins its own
-// sums through distributed shared memory.
+// Few rows of one sequence: one cluster, joined through distributed shared
+// memory.
 template <typename T, bool VEC, int C>
-__global__ void __launch_bounds__(THREADS) balance_sum_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(THREADS) balance_small_kernel(BalanceArgs a) {
   __shared__ SumShared sh;
+  __shared__ SmallShared own;
+  int64_t lo = 0, hi = a.rows;
+  if (a.offsets) lo = bound_of(a, 0), hi = bound_of(a, 1);
+  const int64_t share = (hi - lo + JOIN - 1) / JOIN;
+  const int64_t begin = min(lo + blockIdx.x * share, hi), end = min(begin + share, hi);
+  sum_run<T, VEC, C>(a, begin, max(begin, end), sh, own.part);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  join_parts<THREADS>(a, 0, JOIN, [&](int p) { return (const uint32_t*)cluster.map_shared_rank(&own.part[0], p); },
+                      own.join);
+}
+
+// A CTA sums its block of rows, run by run.
+template <typename T, bool VEC, int C>
+__global__ void __launch_bounds__(THREADS, C <= 2 ? 5 : C <= 4 ? 3 : 2) balance_sum_kernel(BalanceArgs a) {
+  __shared__ SumShared sh;
+  __shared__ Walk walk;
   pdl_trigger();
-  const int64_t begin = (int64_t)blockIdx.x * a.block_rows;
-  const int64_t end = begin + a.block_rows < a.rows ? begin + a.block_rows : a.rows;
-  if (a.small) {
-    sum_run<T, VEC, C>(a, begin, end > begin ? end : begin, sh, sh.part);
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    join_parts(a, 0, JOIN, [&](int p) { return (const uint32_t*)cluster.map_shared_rank(&sh.part[0], p); }, sh);
-    return;
-  }
-  int64_t seq = first_sequence(a, begin, &sh.sequence);
+  const int64_t begin = min((int64_t)blockIdx.x * a.block_rows, a.rows);
+  const int64_t end = min(begin + a.block_rows, a.rows);
+  int64_t seq = walk.first(a, begin);
   for (int64_t at = begin; at < end;) {
-    const Run r = next_run(a, at, end, seq);
+    const Run r = walk.next(a, at, end, seq);
     // (a block and a sequence meet once: block + sequence numbers their runs)
     if (r.seq >= 0) sum_run<T, VEC, C>(a, r.lo, r.hi, sh, a.parts + (blockIdx.x + r.seq) * part_words(a.E));
     at = r.hi;
   }
 }
 
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) balance_join_kernel(BalanceArgs a) {
-  __shared__ SumShared sh;
+  __shared__ JoinShared<THREADS> sh;
   pdl_wait();
   pdl_trigger();
   const int64_t s = blockIdx.x / JOIN;
-  int64_t lo = 0, hi = a.rows;
-  if (a.offsets) lo = bound_of(a, s), hi = bound_of(a, s + 1);
-  const int64_t first = hi > lo ? lo / a.block_rows : 0;
-  const int parts = hi > lo ? (int)((hi - 1) / a.block_rows - first + 1) : 0;
+  int64_t first = 0;
+  int parts = a.blocks;
+  if (a.offsets) {
+    const int64_t lo = bound_of(a, s), hi = bound_of(a, s + 1);
+    first = hi > lo ? lo / a.block_rows : 0;
+    parts = hi > lo ? (int)((hi - 1) / a.block_rows - first + 1) : 0;
+  }
   const uint32_t* base = a.parts + (first + s) * part_words(a.E);
-  join_parts(a, s, parts, [&](int p) { return base + (int64_t)p * part_words(a.E); }, sh);
+  join_parts<THREADS>(a, s, parts, [&](int p) { return base + (int64_t)p * part_words(a.E); }, sh);
 }
 
 // Several sequences: the mean over those with tokens.
@@ -423,10 +474,10 @@ __global__ void __launch_bounds__(THREADS) balance_mean_kernel(BalanceArgs a) {
 // scores; plus `add`.  A row is read by the lanes that write it, before they
 // write, so dlogits may be logits or add.
 template <typename T, bool VEC, int C>
-__global__ void __launch_bounds__(THREADS) balance_grad_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(THREADS, C <= 2 ? 3 : C <= 4 ? 2 : 1) balance_grad_kernel(BalanceArgs a) {
   using Part = RowPart<T, VEC, C>;
   constexpr int N = Part::N;
-  __shared__ int sequence;
+  __shared__ Walk walk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 15, half = lane >> 4;
   const int64_t begin = (int64_t)blockIdx.x * a.block_rows;
   const int64_t end = begin + a.block_rows < a.rows ? begin + a.block_rows : a.rows;
@@ -434,9 +485,9 @@ __global__ void __launch_bounds__(THREADS) balance_grad_kernel(BalanceArgs a) {
   const T* add = static_cast<const T*>(a.add);
   T* dlogits = static_cast<T*>(a.dlogits);
   const float dloss = a.dloss ? *a.dloss : 1.0f;
-  int64_t seq = first_sequence(a, begin, &sequence);
+  int64_t seq = walk.first(a, begin);
   for (int64_t at = begin; at < end;) {
-    const Run run = next_run(a, at, end, seq);
+    const Run run = walk.next(a, at, end, seq);
     at = run.hi;
     float g[N];
 #pragma unroll
@@ -444,17 +495,20 @@ __global__ void __launch_bounds__(THREADS) balance_grad_kernel(BalanceArgs a) {
       const int e = Part::expert(i, sub);
       g[i] = run.seq >= 0 && e < a.E ? a.slope[run.seq * a.E + e] * dloss : 0.0f;
     }
-    const auto fetch = [&](int64_t row, Part& p, Part& more) {
-      const bool in = row < run.hi, on = in && run.seq >= 0 && (!a.mask || a.mask[row]);
-      p.load(logits + row * a.stride, a.E, sub, on, minus_infinity<T>());
-      if (add) more.load(add + row * a.add_stride, a.E, sub, in, 0u);
+    const auto fetch = [&](int64_t row, Part& p) {
+      const bool in = row < run.hi && run.seq >= 0;
+      const bool on = in && (!a.mask || a.mask[row]);
+      p.load(logits + row * a.stride, a.E, sub, in, minus_infinity<T>());
       return on;
     };
-    Part cur, cur_add;
-    bool on = fetch(run.lo + warp * 2 + half, cur, cur_add);
+    Part cur;
+    bool on = fetch(run.lo + warp * 2 + half, cur);
     for (int64_t base = run.lo + warp * 2; base < run.hi; base += ROWS_AT_ONCE) {
-      Part nxt, nxt_add;
-      const bool nxt_on = fetch(base + ROWS_AT_ONCE + half, nxt, nxt_add);
+      const int64_t row = base + half;
+      // (add's own row as late as its registers allow: both prefetched spill)
+      Part more, nxt;
+      if (add) more.load(add + row * a.add_stride, a.E, sub, row < run.hi, 0u);
+      const bool nxt_on = fetch(row + ROWS_AT_ONCE, nxt);
       float x[N];
       cur.values(x);
       float mean = 0.0f;
@@ -480,14 +534,12 @@ __global__ void __launch_bounds__(THREADS) balance_grad_kernel(BalanceArgs a) {
       }
       if (add) {
         float y[N];
-        cur_add.values(y);
+        more.values(y);
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] += y[i];
       }
-      const int64_t row = base + half;
       if (row < run.hi) Part::store(dlogits + row * a.dstride, a.E, sub, x);
       cur = nxt;
-      cur_add = nxt_add;
       on = nxt_on;
     }
   }
@@ -495,11 +547,11 @@ __global__ void __launch_bounds__(THREADS) balance_grad_kernel(BalanceArgs a) {
 
 // ---- launches ----
 
-cudaError_t launch(void (*kernel)(BalanceArgs), int64_t grid, int cluster, bool pdl, cudaStream_t s,
+cudaError_t launch(void (*kernel)(BalanceArgs), int64_t grid, int threads, int cluster, bool pdl, cudaStream_t s,
                    const BalanceArgs& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   if (cluster > 1) {
@@ -517,27 +569,33 @@ cudaError_t launch(void (*kernel)(BalanceArgs), int64_t grid, int cluster, bool 
 }
 
 using Kernel = void (*)(BalanceArgs);
+enum Which { SUM, SMALL, GRAD };
+
+template <typename T, bool VEC, int C>
+Kernel pick(Which w) {
+  return w == SUM ? balance_sum_kernel<T, VEC, C> : w == SMALL ? balance_small_kernel<T, VEC, C> : balance_grad_kernel<T, VEC, C>;
+}
 
 template <typename T, bool VEC>
-Kernel kernel_for(int E, bool grad) {
+Kernel kernel_for(int E, Which w) {
   switch ((E + 63) / 64) {
-    case 1: return grad ? balance_grad_kernel<T, VEC, 1> : balance_sum_kernel<T, VEC, 1>;
-    case 2: return grad ? balance_grad_kernel<T, VEC, 2> : balance_sum_kernel<T, VEC, 2>;
-    case 3: return grad ? balance_grad_kernel<T, VEC, 3> : balance_sum_kernel<T, VEC, 3>;
-    case 4: return grad ? balance_grad_kernel<T, VEC, 4> : balance_sum_kernel<T, VEC, 4>;
+    case 1: return pick<T, VEC, 1>(w);
+    case 2: return pick<T, VEC, 2>(w);
+    case 3: return pick<T, VEC, 3>(w);
+    case 4: return pick<T, VEC, 4>(w);
   }
-  return grad ? balance_grad_kernel<T, VEC, 8> : balance_sum_kernel<T, VEC, 8>;
+  return pick<T, VEC, 8>(w);
 }
 
-Kernel kernel_for(const BalanceArgs& a, bool vec, bool grad) {
-  if (a.dtype == MOE_DTYPE_F32) return vec ? kernel_for<float, true>(a.E, grad) : kernel_for<float, false>(a.E, grad);
-  if (a.dtype == MOE_DTYPE_F16)
-    return vec ? kernel_for<__half, true>(a.E, grad) : kernel_for<__half, false>(a.E, grad);
-  return vec ? kernel_for<__nv_bfloat16, true>(a.E, grad) : kernel_for<__nv_bfloat16, false>(a.E, grad);
+Kernel kernel_for(const BalanceArgs& a, bool vec, Which w) {
+  if (a.dtype == MOE_DTYPE_F32) return vec ? kernel_for<float, true>(a.E, w) : kernel_for<float, false>(a.E, w);
+  if (a.dtype == MOE_DTYPE_F16) return vec ? kernel_for<__half, true>(a.E, w) : kernel_for<__half, false>(a.E, w);
+  return vec ? kernel_for<__nv_bfloat16, true>(a.E, w) : kernel_for<__nv_bfloat16, false>(a.E, w);
 }
 
-constexpr int64_t SUM_CTAS = 152 * 2;     // one wave of two CTAs an SM
-constexpr int64_t GRAD_CTAS = 152 * 2;
+// CTAs of one wave: as many an SM as the kernels' registers allow.
+int64_t sum_ctas(int E) { return 152 * (E <= 128 ? 5 : E <= 256 ? 3 : 2); }
+int64_t grad_ctas(int E) { return 152 * (E <= 128 ? 3 : E <= 256 ? 2 : 1); }
 constexpr int64_t SMALL_ELEMENTS = 1 << 17;  // logits that one cluster takes
 
 int64_t rows_of_a_block(int64_t rows, int64_t ctas) {
@@ -545,44 +603,43 @@ int64_t rows_of_a_block(int64_t rows, int64_t ctas) {
   return std::max<int64_t>((r + ROWS_AT_ONCE - 1) / ROWS_AT_ONCE * ROWS_AT_ONCE, ROWS_AT_ONCE);
 }
 
-int64_t sum_blocks(int64_t rows) {
-  const int64_t r = rows_of_a_block(rows, SUM_CTAS);
+int64_t sum_blocks(int E, int64_t rows) {
+  const int64_t r = rows_of_a_block(rows, sum_ctas(E));
   return (rows + r - 1) / r;
 }
 
-bool small_call(int E, int64_t rows, bool offsets) { return !offsets && rows * E <= SMALL_ELEMENTS; }
+bool small_call(int E, int64_t rows, int64_t sequences) { return sequences == 1 && rows * E <= SMALL_ELEMENTS; }
 
 }  // namespace
 
 size_t balance_workspace(int E, int64_t rows, int64_t sequences) {
+  if (small_call(E, rows, sequences)) return 0;
   // (the runs' sums, then a loss and the tokens of each sequence)
-  return ((size_t)(sum_blocks(rows) + sequences) * part_words(E) + 2 * (size_t)sequences) * 4;
+  return ((size_t)(sum_blocks(E, rows) + sequences) * part_words(E) + 2 * (size_t)sequences) * 4;
 }
 
 cudaError_t launch_balance(BalanceArgs a, bool vec, void* workspace, cudaStream_t s) {
-  const Kernel sum = kernel_for(a, vec, false);
-  if (small_call(a.E, a.rows, a.offsets != nullptr)) {
-    a.small = true;
-    a.block_rows = std::max<int64_t>((a.rows + JOIN - 1) / JOIN, 1);
-    return launch(sum, JOIN, JOIN, false, s, a);
-  }
-  a.block_rows = rows_of_a_block(a.rows, SUM_CTAS);
-  const int64_t blocks = sum_blocks(a.rows);
+  if (small_call(a.E, a.rows, a.sequences)) return launch(kernel_for(a, vec, SMALL), JOIN, THREADS, JOIN, false, s, a);
+  a.block_rows = rows_of_a_block(a.rows, sum_ctas(a.E));
+  const int64_t blocks = sum_blocks(a.E, a.rows);
   a.parts = static_cast<uint32_t*>(workspace);
   a.seq_loss = reinterpret_cast<float*>(a.parts + (blocks + a.sequences) * part_words(a.E));
   a.seq_tokens = reinterpret_cast<int32_t*>(a.seq_loss + a.sequences);
   cudaError_t e = cudaSuccess;
-  if (blocks) e = launch(sum, blocks, 1, false, s, a);
+  a.blocks = (int)blocks;
+  if (blocks) e = launch(kernel_for(a, vec, SUM), blocks, THREADS, 1, false, s, a);
   if (e != cudaSuccess) return e;
-  e = launch(balance_join_kernel, a.sequences * JOIN, JOIN, blocks > 0, s, a);
+  const bool one = a.sequences == 1;
+  e = launch(one ? balance_join_kernel<JOIN_THREADS> : balance_join_kernel<THREADS>, a.sequences * JOIN,
+             one ? JOIN_THREADS : THREADS, JOIN, blocks > 0, s, a);
   if (e != cudaSuccess || a.sequences == 1) return e;
   const int64_t want = (a.sequences * a.E + THREADS * 4 - 1) / (THREADS * 4);
-  return launch(balance_mean_kernel, std::min<int64_t>(want, 304), 1, true, s, a);
+  return launch(balance_mean_kernel, std::min<int64_t>(want, 304), THREADS, 1, true, s, a);
 }
 
 cudaError_t launch_balance_backward(BalanceArgs a, bool vec, cudaStream_t s) {
-  a.block_rows = rows_of_a_block(a.rows, GRAD_CTAS);
-  return launch(kernel_for(a, vec, true), (a.rows + a.block_rows - 1) / a.block_rows, 1, false, s, a);
+  a.block_rows = rows_of_a_block(a.rows, grad_ctas(a.E));
+  return launch(kernel_for(a, vec, GRAD), (a.rows + a.block_rows - 1) / a.block_rows, THREADS, 1, false, s, a);
 }
 
 }  // namespace moe

@@ -44,6 +44,7 @@ struct List {
   float* norm;
   float limit, eps;
   bool scale;         // (of a small set: more than the norm)
+  bool in_place;      // every tensor
 };
 
 // Chunk `id` of a list: the tensor's data from the 16-byte granule it starts
@@ -180,7 +181,6 @@ struct Squares {
       wide += Granules<T>::squares_wide(q);
     }
   }
-  __device__ __forceinline__ double total() const { return (double)sum + wide; }
 };
 
 template <int CAP>
@@ -219,17 +219,33 @@ __device__ __forceinline__ void scale_chunk(const List<CAP>& l, uint32_t id, flo
     scale_typed<__nv_bfloat16>(l, c, f);
 }
 
-// Over the CTA, the same in every thread.
-__device__ __forceinline__ double block_sum(double v, double* red) {
+// Over the CTA, the same in every thread (red: of THREADS / 32 values).
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, double* red) {
+  V* r = reinterpret_cast<V*>(red);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
   __syncthreads();
-  double t = 0.0;
+  V t = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) t += red[w];
+  for (int w = 0; w < THREADS / 32; ++w) t += r[w];
   __syncthreads();
   return t;
+}
+
+// The threads' sums: in FP32, which is four times as quick as FP64's shuffles
+// and slow adds, and FP64 only where a thread has some.
+__device__ __forceinline__ double block_squares(const Squares& s, double* red) {
+  double t = block_sum(s.sum, red);
+  if (__syncthreads_or(s.wide != 0.0)) t += block_sum(s.wide, red);
+  return t;
+}
+
+// Rounded once more than the FP64 root where the sum is an FP32 normal number.
+__device__ __forceinline__ float root(double sum) {
+  const float s = (float)sum;
+  return s > 0x1p-120f && s < 0x1p126f ? sqrtf(s) : (float)sqrt(sum);
 }
 
 // min(1, limit / (norm + eps)); NaN where the norm is.
@@ -245,14 +261,14 @@ __global__ void __launch_bounds__(THREADS) gradient_squares_kernel(const __grid_
   Squares s;
   const uint32_t chunks = l.first[l.n];
   for (uint32_t id = blockIdx.x; id < chunks; id += gridDim.x) add_chunk(l, id, s);
-  const double t = block_sum(s.total(), red);
+  const double t = block_squares(s, red);
   if (threadIdx.x == 0) l.sums[blockIdx.x] = l.add ? l.sums[blockIdx.x] + t : t;
 }
 
 __device__ __forceinline__ float norm_of(const double* sums, int parts, double* red) {
   double v = 0.0;
   for (int i = threadIdx.x; i < parts; i += THREADS) v += sums[i];
-  return (float)sqrt(block_sum(v, red));
+  return root(block_sum(v, red));
 }
 
 template <int CAP>
@@ -262,6 +278,7 @@ __global__ void __launch_bounds__(THREADS) gradient_scale_kernel(const __grid_co
   const float norm = norm_of(l.sums, l.parts, red);
   if (blockIdx.x == 0 && threadIdx.x == 0) *l.norm = norm;
   const float f = factor(norm, l.limit, l.eps);
+  if (f == 1.0f && l.in_place) return;
   const uint32_t chunks = l.first[l.n];
   for (uint32_t id = blockIdx.x; id < chunks; id += gridDim.x) scale_chunk(l, chunks - 1 - id, f);
 }
@@ -282,12 +299,12 @@ __global__ void __launch_bounds__(THREADS) gradient_small_kernel(const __grid_co
   Squares s;
   const uint32_t chunks = l.first[l.n];
   for (uint32_t id = blockIdx.x; id < chunks; id += SMALL_CTAS) add_chunk(l, id, s);
-  const double t = block_sum(s.total(), red);
+  const double t = block_squares(s, red);
   if (threadIdx.x == 0) mine = t;
   cluster.sync();
   double all = 0.0;
   for (int r = 0; r < SMALL_CTAS; ++r) all += *cluster.map_shared_rank(&mine, r);
-  const float norm = (float)sqrt(all);
+  const float norm = root(all);
   if (blockIdx.x == 0 && threadIdx.x == 0) *l.norm = norm;
   if (l.scale) {
     const float f = factor(norm, l.limit, l.eps);
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(THREADS) gradient_small_kernel(const __grid_co
   cluster.sync();  // (shared memory stays until every CTA has read it)
 }
 
-constexpr int FEW = 64, MANY = 1024;  // tensors of a launch: 2 KB of parameters, or 30 KB
+constexpr int FEW = 64, SOME = 256, MANY = 1024;  // tensors of a launch: 2, 8 or 30 KB of parameters
 static_assert(sizeof(List<MANY>) <= 32764, "kernel parameters");
 
 uint32_t chunks_of(const moe_gradient& t) {
@@ -309,7 +326,9 @@ uint32_t chunks_of(const moe_gradient& t) {
 template <int CAP>
 void fill(List<CAP>& l, const moe_gradient* t, int n) {
   uint32_t at = 0;
+  l.in_place = true;
   for (int i = 0; i < n; ++i) {
+    l.in_place = l.in_place && t[i].data == t[i].out;
     l.src[i] = t[i].data;
     l.dst[i] = t[i].out;
     l.count[i] = t[i].count;
@@ -374,7 +393,7 @@ cudaError_t run(const moe_gradient* t, int64_t n, const ClipArgs& a, cudaStream_
 }  // namespace
 
 cudaError_t launch_clip(const moe_gradient* t, int64_t n, const ClipArgs& a, cudaStream_t s) {
-  return n <= FEW ? run<FEW>(t, n, a, s) : run<MANY>(t, n, a, s);
+  return n <= FEW ? run<FEW>(t, n, a, s) : n <= SOME ? run<SOME>(t, n, a, s) : run<MANY>(t, n, a, s);
 }
 
 }  // namespace moe

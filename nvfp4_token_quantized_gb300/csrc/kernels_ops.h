@@ -102,7 +102,7 @@ struct BalanceArgs {
   int64_t add_stride, dstride;
   // set by the launch
   int64_t block_rows;
-  bool small;
+  int blocks;
   uint32_t* parts;
   float* seq_loss;
   int32_t* seq_tokens;

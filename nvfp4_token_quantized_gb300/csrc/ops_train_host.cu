@@ -73,7 +73,8 @@ moe_status moe_balance_loss(const moe_route_config* cfg, const moe_balance_io* i
   if (st != MOE_OK) return st;
   if (!std::isfinite(coefficient)) return MOE_ERR_INVALID_ARG;
   if (num_tokens > 0 && (!io->topk_ids || !aligned(io->topk_ids, 4))) return MOE_ERR_INVALID_ARG;
-  if (!loss || !counts || !slope || !workspace || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(slope, 4) ||
+  const size_t need = balance_workspace(a.E, a.rows, a.sequences);
+  if (!loss || !counts || !slope || (need && !workspace) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(slope, 4) ||
       !aligned(workspace, 16))
     return MOE_ERR_INVALID_ARG;
   a.ids = io->topk_ids;
@@ -85,7 +86,7 @@ moe_status moe_balance_loss(const moe_route_config* cfg, const moe_balance_io* i
   const Rows in[4] = {logit_rows(a.logits, a.rows, a.stride, a), flat(a.rows ? a.ids : nullptr, a.rows * a.K * 4),
                       flat(a.offsets, (a.sequences + 1) * 4), flat(a.rows ? a.mask : nullptr, a.rows)};
   const Rows out[4] = {flat(loss, 4), flat(counts, table), flat(slope, table),
-                       flat(workspace, (int64_t)balance_workspace(a.E, a.rows, a.sequences))};
+                       flat(need ? workspace : nullptr, (int64_t)need)};
   for (int o = 0; o < 4; ++o) {
     for (const Rows& i : in)
       if (overlap(out[o], i)) return MOE_ERR_ALIAS;

@@ -81,21 +81,49 @@ class GradientClip:
 
     @staticmethod
     def _table(grads, out, dev):
-        """moe_gradient of each tensor, as one array of integers."""
-        rows = []
-        for i, (t, o) in enumerate(zip(grads, out)):
-            if not isinstance(t, torch.Tensor) or not isinstance(o, torch.Tensor):
-                raise TypeError(f"gradient {i} must be a torch tensor")
-            dt = _DTYPES.get(t.dtype)
-            if dt is None:
-                raise ValueError(f"gradient {i} must be bfloat16, float16 or float32, not {t.dtype}")
-            if t.get_device() != dev:
-                raise ValueError(f"gradient {i} must be on cuda:{dev}, the current device")
-            if not t.is_contiguous() and not _dense(t):
-                raise ValueError(f"gradient {i}: the elements must lie next to each other")
-            if o is not t and (o.dtype is not t.dtype or o.get_device() != dev or o.shape != t.shape
-                               or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous()))):
-                raise ValueError(f"out {i} must be laid out as gradient {i}: {tuple(t.shape)} of {t.dtype}, "
-                                 f"strides {t.stride()}, on cuda:{dev}")
-            rows += (t.data_ptr(), o.data_ptr(), t.numel(), dt)
-        return array.array("q", rows)
+        """moe_gradient of each tensor, as one array of integers (columns by
+        torch's own calls, so that long lists cost little)."""
+        n = len(grads)
+        table = array.array("q", bytes(32 * n))
+        try:
+            types = [_DTYPES.get(t.dtype) for t in grads]
+            if None in types or (n and set(map(_get_device, grads)) != {dev}) or not all(map(_is_contiguous, grads)):
+                _refuse(grads, dev)
+            where = array.array("q", list(map(_data_ptr, grads)))
+            table[0::4] = table[1::4] = where
+            table[2::4] = array.array("q", list(map(_numel, grads)))
+            table[3::4] = array.array("q", types)
+            if out is not grads:
+                if (n and set(map(_get_device, out)) != {dev}) or types != [_DTYPES.get(o.dtype) for o in out] or (
+                        list(map(_size, grads)) != list(map(_size, out))) or (
+                        list(map(_stride, grads)) != list(map(_stride, out))):
+                    for i, (t, o) in enumerate(zip(grads, out)):
+                        _refuse_out(i, t, o, dev)
+                table[1::4] = array.array("q", list(map(_data_ptr, out)))
+        except (AttributeError, TypeError):
+            raise TypeError("gradients must be torch tensors") from None
+        return table
+
+
+_base = torch._C.TensorBase
+_data_ptr, _numel, _get_device, _is_contiguous = _base.data_ptr, _base.numel, _base.get_device, _base.is_contiguous
+_size, _stride = _base.size, _base.stride
+
+
+def _refuse(grads, dev):
+    """Raises for the first gradient that cannot be taken (a dense one in
+    another order of its dimensions can)."""
+    for i, t in enumerate(grads):
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"gradient {i} must be bfloat16, float16 or float32, not {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"gradient {i} must be on cuda:{dev}, the current device")
+        if not _dense(t):
+            raise ValueError(f"gradient {i}: the elements must lie next to each other")
+
+
+def _refuse_out(i, t, o, dev):
+    if (o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != dev
+            or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous()))):
+        raise ValueError(f"out {i} must be laid out as gradient {i}: {tuple(t.shape)} of {t.dtype}, strides "
+                         f"{t.stride()}, on cuda:{dev}")

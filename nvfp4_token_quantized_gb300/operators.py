@@ -252,9 +252,9 @@ class ExpertRouter:
         io = moe_balance_io(logits.data_ptr(), _vector(ids, torch.int32, T * self.K, "ids", dev), po, pm, ld, S, dt)
         loss, counts, slope = _new_scalar(), _new_rows(S, self.E, torch.int32), _new_rows(S, self.E, torch.float32)
         need = int(self._lib.moe_balance_workspace_bytes(self._cfg, T, S))
-        ws = _new_vector(max(need, 16), torch.uint8)
+        ws = _new_vector(need, torch.uint8) if need else None
         st = self._lib.moe_balance_loss(self._cfg, ctypes.byref(io), float(coefficient), T, loss.data_ptr(),
-                                        counts.data_ptr(), slope.data_ptr(), ws.data_ptr(),
+                                        counts.data_ptr(), slope.data_ptr(), None if ws is None else ws.data_ptr(),
                                         _current(dev) if stream is None else stream)
         if st != MOE_OK:
             raise MoEError(st, f"moe_balance_loss(T={T}, E={self.E}, K={self.K}, sequences={S}, "

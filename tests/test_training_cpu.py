@@ -35,12 +35,12 @@ def _loss(lib, T=100, S=1, coefficient=1.0, loss=4 * MB, counts=5 * MB, slope=6 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), INVALID), (dict(topk_ids=None), INVALID), (dict(loss=None), INVALID),
-    (dict(counts=None), INVALID), (dict(slope=None), INVALID), (dict(ws=None), INVALID), (dict(ws=7 * MB + 8), INVALID),
+    (dict(counts=None), INVALID), (dict(slope=None), INVALID), (dict(T=9999, ws=None), INVALID), (dict(ws=7 * MB + 8), INVALID),
     (dict(logits=MB + 2), INVALID), (dict(topk_ids=2 * MB + 2), INVALID), (dict(offsets=2), INVALID),
     (dict(logits_stride=63), INVALID), (dict(dtype=0), INVALID), (dict(dtype=4), INVALID), (dict(S=0), INVALID),
     (dict(S=2), INVALID), (dict(S=1 << 31, offsets=3 * MB), INVALID), (dict(T=-1), INVALID), (dict(T=1 << 30), INVALID),
     (dict(coefficient=float("inf")), INVALID), (dict(logits_stride=1 << 62), INVALID),
-    (dict(loss=MB), ALIAS), (dict(counts=2 * MB), ALIAS), (dict(slope=5 * MB + 8), ALIAS), (dict(ws=6 * MB + 16), ALIAS),
+    (dict(loss=MB), ALIAS), (dict(counts=2 * MB), ALIAS), (dict(slope=5 * MB + 8), ALIAS), (dict(T=9999, ws=6 * MB + 16), ALIAS),
     (dict(loss=5 * MB + 4), ALIAS), (dict(mask=6 * MB + 10), ALIAS), (dict(offsets=4 * MB, S=3), ALIAS),
 ])
 def test_balance_loss(lib, kw, status):
