@@ -20,10 +20,6 @@
 namespace moe {
 namespace cg = cooperative_groups;
 
-// Row pitch of FP32 tiles in shared memory: the eight rows and four pairs of a
-// fragment fall into different banks.
-__host__ __device__ constexpr int hidden_pitch(int R) { return R + (40 - R % 32) % 32; }
-
 template <int NT>
 struct ApplyShared {
   static constexpr int R = 8 * NT, RP = hidden_pitch(R), KS = (NT + 1) / 2;
@@ -81,16 +77,8 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   T* out = static_cast<T*>(a.out);
   const int K = a.in, N = a.n_out;
 
-  if (group == a.L) {  // no adapter: base alone
-    for (int r = crank * ADAPTER_WARPS + warp; r < count; r += C * ADAPTER_WARPS) {
-      const int64_t row = row_of[r];
-      if (a.hidden)
-        for (int i = lane; i < a.rank; i += 32) a.hidden[row * a.rank + i] = 0.0f;
-      if (out == base && base) continue;
-      for (int c = lane * 8; c < N; c += 256)
-        store8<T, VEC>(out + row * a.out_stride, c, N,
-                       base ? load8<T, VEC>(base + row * a.base_stride, c, N, true) : make_uint4(0, 0, 0, 0));
-    }
+  if (group == a.L) {
+    rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
     return;
   }
 
@@ -286,22 +274,7 @@ cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s, bool pdl) {
     const cudaError_t e = raise_shared(kernel, bytes, done);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.cluster));
-  cfg.blockDim = dim3(ADAPTER_THREADS);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)a.cluster, 1, 1};
-  cfg.numAttrs = 1;
-  if (pdl) {
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
-  }
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_clustered(kernel, a, bytes, pdl, s);
 }
 
 template <typename T>

@@ -18,6 +18,8 @@
 #include "elem_types.cuh"
 #include "kernels_ops.h"
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int ADAPTER_THREADS = 256;
@@ -100,6 +102,49 @@ __device__ __forceinline__ float exponent_scale(float m, float& back) {
 // Adapter a's rows are rows[starts[a]] .. rows[starts[a + 1] - 1], in ascending
 // order; group L holds the rows without an adapter, starts[L + 1] = T.
 __device__ __forceinline__ int adapter_key(int id, int L) { return (unsigned)id < (unsigned)L ? id : L; }
+
+// Row pitch of FP32 tiles in shared memory: the eight rows and four pairs of a
+// fragment fall into different banks.
+__host__ __device__ constexpr int hidden_pitch(int R) { return R + (40 - R % 32) % 32; }
+
+// A tile of rows without an adapter: base alone, by the C CTAs of a cluster.
+template <typename T, bool VEC>
+__device__ __forceinline__ void rows_without_adapter(const AdapterArgs& a, const int* row_of, int count, int crank,
+                                                     int C) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.out);
+  for (int r = crank * ADAPTER_WARPS + warp; r < count; r += C * ADAPTER_WARPS) {
+    const int64_t row = row_of[r];
+    if (a.hidden)
+      for (int i = lane; i < a.rank; i += 32) a.hidden[row * a.rank + i] = 0.0f;
+    if (out == base) continue;
+    for (int c = lane * 8; c < a.n_out; c += 256)
+      store8<T, VEC>(out + row * a.out_stride, c, a.n_out,
+                     base ? load8<T, VEC>(base + row * a.base_stride, c, a.n_out, true) : make_uint4(0, 0, 0, 0));
+  }
+}
+
+// tiles x cluster CTAs; pdl: may start while its predecessor finishes.
+template <typename K>
+cudaError_t launch_clustered(K kernel, const AdapterArgs& a, int bytes, bool pdl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.tiles * a.cluster));
+  cfg.blockDim = dim3(ADAPTER_THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)a.cluster, 1, 1};
+  cfg.numAttrs = 1;
+  if (pdl) {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 
 // Pieces of `unit` rows of the groups: group a's pieces have the numbers
 // starts[a] / unit + a and up; numbers between two groups' may be unused.

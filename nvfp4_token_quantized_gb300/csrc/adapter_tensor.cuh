@@ -1,0 +1,404 @@
+// adapter_tensor.cuh - rows through their adapters (as adapter_apply.cuh) for
+// batches of many rows: both products on the tensor cores' tcgen05 path, operands
+// in 128-byte swizzled shared memory, sums in tensor memory.
+//
+// A tile is 128 rows of one adapter.  Its x is streamed in stages of 64 columns
+// beside the same columns of down (D1 += x down^T, 128 x rank), then base and up in
+// stages of 64 output columns (D2 = hidden up, 128 x 64).  The rows are those that
+// the plan lists, in any order, so they come by 16-byte asynchronous copies, each
+// to the place that the swizzle gives it; up is read as it lies, rank rows of
+// neighbouring columns, which is the layout of an operand whose columns are
+// contiguous.  hidden enters the second product as two 16-bit parts side by side
+// (split2), which doubles a contraction of 16 to 128 and costs nothing visible.
+//
+// Stages follow one another without roles: every thread copies, waits for its own
+// copies, meets the others, and one thread issues the stage's products; the slot is
+// filled again when their commit has arrived.  Two CTAs share an SM, so that one's
+// barriers and the join between the products hide behind the other's copies.  The
+// CTAs of a cluster split a tile as in adapter_apply.cuh.
+//
+// Waits are bounded: one that runs out raises a flag, further waits return at once,
+// and the tile's rows become NaN.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "adapter_common.cuh"
+
+namespace moe {
+namespace cg = cooperative_groups;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Writes of this thread so far, before later accesses of the tensor cores.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// D[tmem] (+)= A B, both operands 16-bit in shared memory.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// M 128, FP32 sums; b_rows: B's contraction runs across its rows.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc_f16(int N, bool b_rows) {
+  const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)b_rows << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+// Descriptor of an operand whose contraction runs across rows of 128 bytes, with
+// the 128-byte swizzle: eight rows are 1024 bytes, as are the next eight.  (One
+// panel of 64 columns: the stride between panels is not used.)
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(1024u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16-byte chunk c of a row of 128 bytes lies at chunk c ^ (row % 8).
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
+  return (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
+}
+
+template <int R>
+struct TensorShared {
+  static constexpr int ROWS = ADAPTER_TILE * 128;          // of x, or of base and out
+  static constexpr int STAGE = ROWS + R * 128;
+  static constexpr int STAGES = R == 64 ? 3 : 4;
+  static constexpr int PANELS = R <= 32 ? 1 : 2 * R / 64;  // of hidden's parts, 64 wide
+  static constexpr int RP = hidden_pitch(R);
+  static constexpr int HIDDEN = PANELS * ROWS;
+  static constexpr int BYTES = HIDDEN + STAGES * STAGE + 1024;  // (aligned inside)
+  static_assert(ADAPTER_TILE * RP * 4 <= STAGES * STAGE, "the first product's sums lie in the stages");
+};
+
+template <typename T, int R>
+__global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tensor_kernel(const AdapterArgs a) {
+  using S = TensorShared<R>;
+  constexpr int ST = S::STAGES, RP = S::RP;
+  constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  unsigned char* panels = smem;                 // hidden's parts
+  unsigned char* ring = smem + S::HIDDEN;
+  float* part = reinterpret_cast<float*>(ring);  // (between the products)
+  __shared__ int row_of[ADAPTER_TILE];
+  __shared__ float back[ADAPTER_TILE];
+  __shared__ Piece found;
+  __shared__ uint64_t filled[ST], done[2];       // commits: of the first product's slots, of D2
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile int gave_up;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
+
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&filled[i], 1);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
+    gave_up = 0;
+    fence_mbarrier_init();
+  }
+  pdl_wait();
+  const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
+  pdl_trigger();
+  if (p.group < 0) return;  // (the whole cluster)
+  const int count = p.count, group = p.group;
+  if (tid < ADAPTER_TILE) {
+    row_of[tid] = tid < count ? a.row_list[p.start + tid] : 0;
+    back[tid] = 1.0f;
+  }
+  const T* x = static_cast<const T*>(a.x);
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.out);
+  const int K = a.in, N = a.n_out;
+  if (group == a.L) {
+    __syncthreads();
+    rows_without_adapter<T, true>(a, row_of, count, crank, C);
+    return;
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_at, 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at, ring_at = smem_u32(ring), panels_at = smem_u32(panels);
+  const auto wait = [&](uint64_t* bar, int parity) {
+    if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
+    __syncwarp();
+  };
+
+  // ---- D1 = x down^T over this CTA's columns ----
+  const int chunks = (K + 63) / 64, each = (chunks + C - 1) / C;
+  const int c0 = min(crank * each, chunks), nk = min(each, chunks - c0);
+  {
+    const int sub = tid & 7, r0 = tid >> 3;  // 16-byte chunk of a row, first of the rows 32 apart
+    const T* px[4];
+    bool on[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      on[i] = r0 + 32 * i < count;
+      px[i] = x + (int64_t)row_of[r0 + 32 * i] * a.x_stride;
+    }
+    const T* down = static_cast<const T*>(a.first) + (int64_t)group * a.rank * K;
+    const auto issue = [&](int i) {
+      const int col = (c0 + i) * 64 + sub * 8;
+      const uint32_t at = ring_at + (i % ST) * S::STAGE;
+      const bool in = col < K;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) copy16(at + swizzled(r0 + 32 * q, sub), in ? px[q] + col : x, in && on[q]);
+#pragma unroll
+      for (int r = r0; r < R; r += 32) {
+        const bool have = in && r < a.rank;
+        copy16(at + S::ROWS + swizzled(r, sub), have ? down + (int64_t)r * K + col : down, have);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < nk) issue(i);
+      copy_commit();
+    }
+    for (int i = 0; i < nk; ++i) {
+      copy_wait<ST - 2>();
+      fence_async_proxy();
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t at = ring_at + (i % ST) * S::STAGE;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_f16(tmem, smem_desc_sw128(at + k * 32), smem_desc_sw128(at + S::ROWS + k * 32), idesc_f16<T>(R, false),
+                     i > 0 || k > 0);
+        tc_commit(&filled[i % ST]);
+      }
+      if (i + ST - 1 < nk) {
+        if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
+        issue(i + ST - 1);
+      }
+      copy_commit();
+    }
+    copy_wait<0>();
+    if (nk > 0) wait(&filled[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
+    __syncthreads();
+    tc_fence_after();
+  }
+
+  // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
+  const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+  {
+    float* to = part + mine * RP + half * (R / 2);
+#pragma unroll
+    for (int c = 0; c < R / 2; c += 8) {
+      float v[8];
+      if (nk > 0) {
+        tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + half * (R / 2) + c, v);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      }
+      reinterpret_cast<float4*>(to + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(to + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    tc_fence_before();
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  if (C > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  {
+    constexpr int G = R / 8;  // lanes of a row, eight ranks each
+    const float scale = a.scales ? a.scales[group] : 1.0f;
+    const int share = ADAPTER_TILE / C, lane8 = tid % G;
+    for (int r = crank * share + tid / G; r < (crank + 1) * share; r += ADAPTER_THREADS / G) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      for (int q = 0; q < C; ++q) {
+        const float4* f =
+            reinterpret_cast<const float4*>((C > 1 ? cluster.map_shared_rank(part, q) : part) + r * RP + lane8 * 8);
+        const float4 lo = f[0], hi = f[1];
+        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+      }
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] *= scale;
+        m = fmaxf(m, fabsf(v[i]));
+      }
+      if (a.hidden && r < count) {
+        float* h = a.hidden + (int64_t)row_of[r] * a.rank + lane8 * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (lane8 * 8 + i < a.rank) h[i] = v[i];
+      }
+      float s = 1.0f, b = 1.0f;
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int o = 1; o < G; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = exponent_scale(m, b);
+      }
+      uint4 hi, lo;
+      split2<T>(v[0] * s, v[1] * s, hi.x, lo.x);
+      split2<T>(v[2] * s, v[3] * s, hi.y, lo.y);
+      split2<T>(v[4] * s, v[5] * s, hi.z, lo.z);
+      split2<T>(v[6] * s, v[7] * s, hi.w, lo.w);
+      // columns [0, R) of the panels hold the first parts, [R, 2R) the second
+      const int ch = lane8, cl = G + lane8;
+      const uint32_t at_hi = (ch >> 3) * S::ROWS + swizzled(r, ch & 7), at_lo = (cl >> 3) * S::ROWS + swizzled(r, cl & 7);
+      for (int q = 0; q < C; ++q) {
+        unsigned char* to = C > 1 ? cluster.map_shared_rank(panels, q) : panels;
+        *reinterpret_cast<uint4*>(to + at_hi) = hi;
+        *reinterpret_cast<uint4*>(to + at_lo) = lo;
+        if (SCALED && lane8 == 0) *(C > 1 ? cluster.map_shared_rank(&back[r], q) : &back[r]) = b;
+      }
+    }
+    fence_async_proxy();
+  }
+  if (C > 1)
+    cluster.sync();  // (the last access to another CTA's shared memory lies before)
+  else
+    __syncthreads();
+  fence_async_proxy();
+
+  // ---- out = base + hidden up, 64 columns a stage ----
+  {
+    const int blocks = (N + 63) / 64, nb = crank < blocks ? (blocks - crank + C - 1) / C : 0;
+    const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
+    // A warp copies the rows and the half of their columns that it adds to, and
+    // stores: eight rows by four chunks at a time.
+    const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2);
+    int64_t at_row[4];
+    bool on[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      at_row[q] = row_of[first + 8 * q];
+      on[q] = first + 8 * q < count;
+    }
+    const auto issue = [&](int i) {
+      const int col = (crank + i * C) * 64;
+      const uint32_t at = ring_at + (i % ST) * S::STAGE;
+      const bool in = col + sub * 8 < N;
+      if (base) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          copy16(at + swizzled(first + 8 * q, sub), in ? base + at_row[q] * a.base_stride + col + sub * 8 : base,
+                 in && on[q]);
+      }
+      const int chunk = tid & 7;
+      const bool up_in = col + chunk * 8 < N;
+#pragma unroll
+      for (int r = tid >> 3; r < R; r += 32) {
+        const bool have = up_in && r < a.rank;
+        copy16(at + S::ROWS + swizzled(r, chunk), have ? up + (int64_t)r * N + col + chunk * 8 : up, have);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      if (i < nb) issue(i);
+      copy_commit();
+    }
+    const float bk = back[mine];
+    for (int i = 0; i <= nb; ++i) {
+      if (i < nb) {
+        copy_wait<ST - 2>();
+        fence_async_proxy();
+        __syncthreads();
+        if (tid == 0) {
+          tc_fence_after();
+          const uint32_t b = ring_at + (i % ST) * S::STAGE + S::ROWS;
+#pragma unroll
+          for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
+            tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
+                       smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, true), k > 0);
+          tc_commit(&done[i & 1]);
+        }
+      }
+      if (i == 0) continue;
+      // the stage before, while the tensor cores work on this one
+      const int j = i - 1, col = (crank + j * C) * 64;
+      wait(&done[j & 1], (j >> 1) & 1);
+      tc_fence_after();
+      float v[32];
+      tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (j & 1) * 64 + half * 32, v);
+      unsigned char* tile = ring + (j % ST) * S::STAGE;
+      uint4 y[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        y[c] = base ? *reinterpret_cast<const uint4*>(tile + swizzled(mine, half * 4 + c)) : make_uint4(0, 0, 0, 0);
+      tmem_ld_wait();
+      tc_fence_before();
+      const float lost = gave_up ? NAN : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2(w[e], T());
+          o[e] = pack2(fmaf(v[c * 8 + 2 * e], bk, f.x) + lost, fmaf(v[c * 8 + 2 * e + 1], bk, f.y) + lost, T());
+        }
+        *reinterpret_cast<uint4*>(tile + swizzled(mine, half * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      __syncwarp();
+      uint4 o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const uint4*>(tile + swizzled(first + 8 * q, sub));
+      __syncwarp();  // (the warp's part of the slot is filled again below)
+      if (col + sub * 8 < N) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (on[q]) *reinterpret_cast<uint4*>(out + at_row[q] * a.out_stride + col + sub * 8) = o[q];
+      }
+      if (j + ST < nb) issue(j + ST);
+      copy_commit();
+    }
+    copy_wait<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+template <typename T, int R>
+cudaError_t launch_tensor_one(const AdapterArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = adapter_tensor_kernel<T, R>;
+  const cudaError_t e = raise_shared(kernel, TensorShared<R>::BYTES, done);
+  if (e != cudaSuccess) return e;
+  return launch_clustered(kernel, a, TensorShared<R>::BYTES, true, s);
+}
+
+template <typename T>
+cudaError_t launch_tensor(const AdapterArgs& a, cudaStream_t s) {
+  if (a.rank <= 16) return launch_tensor_one<T, 16>(a, s);
+  if (a.rank <= 32) return launch_tensor_one<T, 32>(a, s);
+  if (a.rank <= 64) return launch_tensor_one<T, 64>(a, s);
+  return launch_tensor_one<T, 128>(a, s);
+}
+
+}  // namespace moe

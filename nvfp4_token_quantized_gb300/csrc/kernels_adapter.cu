@@ -90,17 +90,20 @@ cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
                   a.L, const_cast<int32_t*>(a.starts), const_cast<int32_t*>(a.row_list));
 }
 
-// CTAs of a cluster: enough for some two CTAs an SM.
+// CTAs of a cluster: as many as keep the likely tiles within one wave of two
+// CTAs an SM (half of the adapters' last tiles count: which are used is known
+// on the device only).
 int cluster_of(int64_t tiles, int64_t rows, int L) {
   const int64_t full = std::min<int64_t>(rows, (rows + ADAPTER_TILE - 1) / ADAPTER_TILE + std::min<int64_t>(L, rows) / 2);
-  const int64_t t = std::min(tiles, full);
-  return t >= 304 ? 1 : t >= 152 ? 2 : t >= 60 ? 4 : 8;
+  const int64_t t = std::max<int64_t>(std::min(tiles, full), 1);
+  return t * 8 <= 304 ? 8 : t * 4 <= 304 ? 4 : t * 2 <= 304 ? 2 : 1;
 }
 
 cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
   a.direct = !planned;
   a.tiles = planned ? pieces_of(a.rows, a.L + 1, ADAPTER_TILE) : a.L + 1;
   a.cluster = cluster_of(a.tiles, a.rows, a.L);
+  if (planned && vec) return f16 ? launch_tensor_f16(a, s) : launch_tensor_bf16(a, s);
   return f16 ? launch_apply_f16(a, vec, planned, s) : launch_apply_bf16(a, vec, planned, s);
 }
 

@@ -170,6 +170,8 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
                                     cudaStream_t s);
 cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
 cudaError_t launch_apply_f16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
+cudaError_t launch_tensor_bf16(const AdapterArgs& a, cudaStream_t s);
+cudaError_t launch_tensor_f16(const AdapterArgs& a, cudaStream_t s);
 cudaError_t launch_outer_bf16(const OuterArgs& a, bool vec, cudaStream_t s);
 cudaError_t launch_outer_f16(const OuterArgs& a, bool vec, cudaStream_t s);
 
