@@ -1,0 +1,240 @@
+// adapter_gradient.cuh - the gradients of an adapter's factors (as
+// adapter_outer.cuh) on the tensor cores' tcgen05 path: D = x^T hidden, 128 columns
+// of x by the ranks, contraction over the rows.
+//
+// Both operands lie as they are stored, rows of neighbouring columns, which is the
+// layout of operands whose contraction runs across rows.  x's rows come by
+// asynchronous copies of 512 bytes a row.  hidden is first split into its two
+// 16-bit parts, by a kernel that writes them in the order and swizzle in which the
+// tensor cores read them, once for all columns.  With FP16 the parts of a piece
+// share a power of two.
+//
+// A CTA takes a piece (up to `unit` rows of one adapter) and 256 columns.  Bound by
+// the bytes of x and dout, once each.
+#pragma once
+
+#include "adapter_mma.cuh"
+
+namespace moe {
+
+constexpr int GRADIENT_COLUMNS = 256, GRADIENT_ROWS = 32;  // of a CTA, of a stage
+
+template <int R>
+struct GradientShared {
+  static constexpr int PANEL = GRADIENT_ROWS * 128;           // 64 columns of a stage's rows
+  static constexpr int PARTS = 2 * R <= 64 ? 1 : 2 * R / 64;  // panels of hidden's two parts
+  static constexpr int N = 2 * R < 64 ? 2 * R : 64;           // columns of one product
+  static constexpr int X = GRADIENT_COLUMNS / 64 * PANEL, HIDDEN = PARTS * PANEL, STAGE = X + HIDDEN;
+  static constexpr int STAGES = 4;
+  static constexpr int D = R <= 64 ? 64 : 128;                // tensor memory columns of 128 columns of x
+  static constexpr int BYTES = STAGES * STAGE + 1024;         // (aligned inside)
+};
+
+// hidden's parts of one piece: [stage][panel][row] of 128 bytes, swizzled; ranks
+// [0, R) of the panels' columns hold the first parts, [R, 2R) the second.
+template <typename T, int R>
+__global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
+  using S = GradientShared<R>;
+  constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
+  __shared__ Piece found;
+  __shared__ float warp_max[8];
+  const int tid = threadIdx.x, side = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  const Piece p = find_piece(a.starts, a.L, a.unit, blockIdx.x, &found);
+  if (p.group < 0) return;
+  const float* hidden = a.hidden[side];
+  const int32_t* rows = a.row_list + p.start;
+  constexpr int G = R / 8;  // threads of a row, eight ranks each
+  const int lane8 = tid % G;
+  const auto load = [&](int r, float (&v)[8]) {
+    const float* h = hidden + (r < p.count ? (int64_t)rows[r] * a.rank : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r < p.count && lane8 * 8 + i < a.rank ? h[lane8 * 8 + i] : 0.0f;
+  };
+  float s = 1.0f;
+  if constexpr (SCALED) {
+    float m = 0.0f, back;
+    for (int r = tid / G; r < p.count; r += 256 / G) {
+      float v[8];
+      load(r, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
+    s = exponent_scale(m, back);
+    if (tid == 0) a.back[side][blockIdx.x] = back;
+  }
+  const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
+  unsigned char* to = a.parts[side] + (int64_t)blockIdx.x * (a.unit / GRADIENT_ROWS) * S::HIDDEN;
+  for (int r = tid / G; r < stages * GRADIENT_ROWS; r += 256 / G) {
+    float v[8];
+    load(r, v);
+    uint4 hi, lo;
+    split2<T>(v[0] * s, v[1] * s, hi.x, lo.x);
+    split2<T>(v[2] * s, v[3] * s, hi.y, lo.y);
+    split2<T>(v[4] * s, v[5] * s, hi.z, lo.z);
+    split2<T>(v[6] * s, v[7] * s, hi.w, lo.w);
+    unsigned char* stage = to + (int64_t)(r / GRADIENT_ROWS) * S::HIDDEN;
+    const int row = r % GRADIENT_ROWS, ch = lane8, cl = G + lane8;
+    *reinterpret_cast<uint4*>(stage + (ch >> 3) * S::PANEL + swizzled(row, ch & 7)) = hi;
+    *reinterpret_cast<uint4*>(stage + (cl >> 3) * S::PANEL + swizzled(row, cl & 7)) = lo;
+  }
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(const OuterArgs a) {
+  using S = GradientShared<R>;
+  constexpr int ST = S::STAGES;
+  extern __shared__ unsigned char raw[];
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  __shared__ Piece found;
+  __shared__ uint64_t filled[ST];
+  __shared__ uint32_t tmem_at;
+  __shared__ volatile int gave_up;
+  __shared__ int row_of[1024];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (set up while the kernels before run)
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(&filled[i], 1);
+    gave_up = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_at, 2 * S::D);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_wait();
+  pdl_trigger();
+  const Piece p = find_piece(a.starts, a.L, a.unit, blockIdx.x, &found);
+  const int side = blockIdx.y < a.blocks[0] ? 0 : 1;  // down's gradient, then up's
+  if (p.group < 0) {
+    if (warp == 0) tmem_dealloc(tmem, 2 * S::D);
+    return;
+  }
+  const int n0 = (blockIdx.y - (side ? a.blocks[0] : 0)) * GRADIENT_COLUMNS, N = a.width[side];
+  const T* x = static_cast<const T*>(a.x[side]);
+  const int64_t stride = a.stride[side];
+  for (int r = tid; r < p.count; r += ADAPTER_THREADS) row_of[r] = a.row_list[p.start + r];
+  __syncthreads();
+  const auto wait = [&](uint64_t* bar, int parity) {
+    if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
+    __syncwarp();
+  };
+
+  const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
+  const unsigned char* parts = a.parts[side] + (int64_t)blockIdx.x * (a.unit / GRADIENT_ROWS) * S::HIDDEN;
+  // a warp copies whole rows: 32 chunks of 16 bytes, four rows a warp
+  const int col = n0 + lane * 8;
+  const bool in = col < N;
+  const auto issue = [&](int i) {
+    const uint32_t at = ring + (i % ST) * S::STAGE;
+#pragma unroll
+    for (int q = 0; q < GRADIENT_ROWS / ADAPTER_WARPS; ++q) {
+      const int row = warp + q * ADAPTER_WARPS, r = i * GRADIENT_ROWS + row;
+      const bool on = in && r < p.count;
+      copy16(at + (lane >> 3) * S::PANEL + swizzled(row, lane & 7), on ? x + row_of[r] * stride + col : x, on);
+    }
+#pragma unroll
+    for (int c = tid; c < S::HIDDEN / 16; c += ADAPTER_THREADS)
+      copy16(at + S::X + c * 16, parts + (int64_t)i * S::HIDDEN + c * 16, true);
+  };
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    if (i < stages) issue(i);
+    copy_commit();
+  }
+  for (int i = 0; i < stages; ++i) {
+    copy_wait<ST - 2>();
+    fence_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t at = ring + (i % ST) * S::STAGE;
+#pragma unroll
+      for (int k = 0; k < GRADIENT_ROWS / 16; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int q = 0; q < S::PARTS; ++q) {
+            // (128 ranks: two panels of first parts, two of second ones)
+            const int to = R > 64 ? q & 1 : 0, first = R > 64 ? q < 2 : q == 0;
+            tc_mma_f16(tmem + m * S::D + to * 64, smem_desc_rows(at + 2 * m * S::PANEL + k * 2048, S::PANEL),
+                       smem_desc_rows(at + S::X + q * S::PANEL + k * 2048), idesc_f16<T>(S::N, true, true),
+                       i > 0 || k > 0 || !first);
+          }
+      tc_commit(&filled[i % ST]);
+    }
+    if (i + ST - 1 < stages) {
+      if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
+      issue(i + ST - 1);
+    }
+    copy_commit();
+  }
+  copy_wait<0>();
+  wait(&filled[(stages - 1) % ST], ((stages - 1) / ST) & 1);  // (the last commit covers all before)
+  tc_fence_after();
+
+  // A lane has a column of x, its ranks side by side in tensor memory.
+  const int quarter = warp & 3, m = warp >> 2, c = n0 + m * 128 + quarter * 32 + lane;
+  const float back = std::is_same<T, __nv_bfloat16>::value ? 1.0f : a.back[side][blockIdx.x];
+  const float lost = gave_up ? NAN : 0.0f;
+  const int64_t n = (int64_t)a.rank * N;
+  const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // the adapter's only piece
+  float* sums = a.sums[side] + (int64_t)blockIdx.x * n + c;
+  T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
+#pragma unroll
+  for (int r0 = 0; r0 < R; r0 += 8) {
+    float v[8], w[8];
+    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + m * S::D + r0;
+    tmem_ld8(at, v);
+    if (R <= 32) tmem_ld8(at + R, w);  // (the parts have columns of their own)
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= a.rank || c >= N) continue;
+      const float f = (R <= 32 ? v[i] + w[i] : v[i]) * back + lost;
+      if (alone)
+        grad[(int64_t)(r0 + i) * N] = from_f32<T>(f);
+      else
+        sums[(int64_t)(r0 + i) * N] = f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * S::D);
+  }
+}
+
+template <typename T, int R>
+cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = adapter_gradient_kernel<T, R>;
+  cudaError_t e = raise_shared(kernel, GradientShared<R>::BYTES, done);
+  if (e != cudaSuccess) return e;
+  const unsigned pieces = (unsigned)pieces_of(a.rows, a.L, a.unit);
+  e = launch_k(adapter_split_kernel<T, R>, dim3(pieces, 2), dim3(256), 0, s, true, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3(pieces, (unsigned)(a.blocks[0] + a.blocks[1])), dim3(ADAPTER_THREADS),
+                  GradientShared<R>::BYTES, s, true, a);
+}
+
+template <typename T>
+cudaError_t launch_gradient(const OuterArgs& a, cudaStream_t s) {
+  if (a.rank <= 16) return launch_gradient_one<T, 16>(a, s);
+  if (a.rank <= 32) return launch_gradient_one<T, 32>(a, s);
+  if (a.rank <= 64) return launch_gradient_one<T, 64>(a, s);
+  return launch_gradient_one<T, 128>(a, s);
+}
+
+}  // namespace moe

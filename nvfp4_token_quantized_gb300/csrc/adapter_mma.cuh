@@ -1,0 +1,63 @@
+// adapter_mma.cuh - what the adapters' tcgen05 kernels share: asynchronous copies to
+// swizzled places, descriptors and products of 16-bit operands.
+#pragma once
+
+#include "adapter_common.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// This thread's writes to shared memory so far, before later accesses of the
+// tensor cores: its own CTA's memory, or any in the cluster.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// D[tmem] (+)= A B, both operands 16-bit in shared memory.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// M 128, FP32 sums; a_rows, b_rows: the operand's contraction runs across its
+// rows.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc_f16(int N, bool a_rows, bool b_rows) {
+  const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_rows << 15) | ((uint32_t)b_rows << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Descriptor of an operand whose contraction runs across rows of 128 bytes, with
+// the 128-byte swizzle: panels of 64 columns `panel` bytes apart, in a panel
+// eight rows every 1024 bytes.
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr, uint32_t panel = 1024) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16-byte chunk c of a row of 128 bytes lies at chunk c ^ (row % 8).
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
+  return (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
+}
+
+}  // namespace moe

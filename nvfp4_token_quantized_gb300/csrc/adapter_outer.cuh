@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(const OuterArgs a) {
   const int64_t n = (int64_t)a.rank * a.width[side];
   const int lo = a.starts[group], hi = a.starts[group + 1];
   const int parts = (hi - lo + a.unit - 1) / a.unit;
+  if (a.alone && parts == 1) return;  // (written already)
   const float* sums = a.sums[side] + (lo / a.unit + group) * n;
   T* out = static_cast<T*>(a.grad[side]) + group * n;
   for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
@@ -160,6 +161,13 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(const OuterArgs a) {
     for (int p = 0; p < parts; ++p) s += sums[p * n + i];
     out[i] = from_f32<T>(s);
   }
+}
+
+template <typename T>
+cudaError_t launch_join(const OuterArgs& a, cudaStream_t s) {
+  const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);
+  const dim3 grid((unsigned)std::min<int64_t>((n + 255) / 256, 1024), (unsigned)a.L, 2);
+  return launch_k(adapter_join_kernel<T>, grid, dim3(256), 0, s, true, a);
 }
 
 template <typename T, int MT>
@@ -182,10 +190,7 @@ cudaError_t launch_outer(const OuterArgs& a, bool vec, cudaStream_t s) {
     e = launch_outer_mt<T, 3>(a, vec, s);
   else
     e = launch_outer_mt<T, 4>(a, vec, s);
-  if (e != cudaSuccess) return e;
-  const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);
-  const dim3 grid((unsigned)std::min<int64_t>((n + 255) / 256, 1024), (unsigned)a.L, 2);
-  return launch_k(adapter_join_kernel<T>, grid, dim3(256), 0, s, true, a);
+  return e == cudaSuccess ? launch_join<T>(a, s) : e;
 }
 
 }  // namespace moe

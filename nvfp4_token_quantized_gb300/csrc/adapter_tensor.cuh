@@ -24,60 +24,10 @@
 #include <cooperative_groups.h>
 
 #include "adapter_common.cuh"
+#include "adapter_mma.cuh"
 
 namespace moe {
 namespace cg = cooperative_groups;
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// Writes of this thread so far, before later accesses of the tensor cores.
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// D[tmem] (+)= A B, both operands 16-bit in shared memory.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      "}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// M 128, FP32 sums; b_rows: B's contraction runs across its rows.
-template <typename T>
-__device__ __forceinline__ constexpr uint32_t idesc_f16(int N, bool b_rows) {
-  const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)b_rows << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((128u >> 4) << 24);
-}
-// Descriptor of an operand whose contraction runs across rows of 128 bytes, with
-// the 128-byte swizzle: eight rows are 1024 bytes, as are the next eight.  (One
-// panel of 64 columns: the stride between panels is not used.)
-__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(1024u >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16-byte chunk c of a row of 128 bytes lies at chunk c ^ (row % 8).
-__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
-  return (uint32_t)row * 128 + (uint32_t)((chunk ^ (row & 7)) << 4);
-}
 
 template <int R>
 struct TensorShared {
@@ -110,30 +60,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
 
+  // (set up while the plan is made)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) mbar_init(&filled[i], 1);
     mbar_init(&done[0], 1);
     mbar_init(&done[1], 1);
     gave_up = 0;
     fence_mbarrier_init();
-  }
-  pdl_wait();
-  const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
-  pdl_trigger();
-  if (p.group < 0) return;  // (the whole cluster)
-  const int count = p.count, group = p.group;
-  if (tid < ADAPTER_TILE) {
-    row_of[tid] = tid < count ? a.row_list[p.start + tid] : 0;
-    back[tid] = 1.0f;
-  }
-  const T* x = static_cast<const T*>(a.x);
-  const T* base = static_cast<const T*>(a.base);
-  T* out = static_cast<T*>(a.out);
-  const int K = a.in, N = a.n_out;
-  if (group == a.L) {
-    __syncthreads();
-    rows_without_adapter<T, true>(a, row_of, count, crank, C);
-    return;
   }
   if (warp == 0) {
     tmem_alloc(&tmem_at, 128);
@@ -143,6 +76,28 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at, ring_at = smem_u32(ring), panels_at = smem_u32(panels);
+  pdl_wait();
+  const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
+  pdl_trigger();
+  const int count = p.count, group = p.group;
+  if (group < 0) {  // (the whole cluster)
+    if (warp == 0) tmem_dealloc(tmem, 128);
+    return;
+  }
+  if (tid < ADAPTER_TILE) {
+    row_of[tid] = tid < count ? a.row_list[p.start + tid] : 0;
+    back[tid] = 1.0f;
+  }
+  const T* x = static_cast<const T*>(a.x);
+  const T* base = static_cast<const T*>(a.base);
+  T* out = static_cast<T*>(a.out);
+  const int K = a.in, N = a.n_out;
+  __syncthreads();
+  if (group == a.L) {
+    if (warp == 0) tmem_dealloc(tmem, 128);
+    rows_without_adapter<T, true>(a, row_of, count, crank, C);
+    return;
+  }
   const auto wait = [&](uint64_t* bar, int parity) {
     if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
     __syncwarp();
@@ -151,6 +106,8 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   // ---- D1 = x down^T over this CTA's columns ----
   const int chunks = (K + 63) / 64, each = (chunks + C - 1) / C;
   const int c0 = min(crank * each, chunks), nk = min(each, chunks - c0);
+  const int blocks = (N + 63) / 64, blocks_each = (blocks + C - 1) / C;  // (of the second product)
+  const int b0 = min(crank * blocks_each, blocks), nb = min(blocks_each, blocks - b0);
   {
     const int sub = tid & 7, r0 = tid >> 3;  // 16-byte chunk of a row, first of the rows 32 apart
     const T* px[4];
@@ -180,13 +137,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
     }
     for (int i = 0; i < nk; ++i) {
       copy_wait<ST - 2>();
-      fence_async_proxy();
+      fence_async_shared();
       __syncthreads();
       if (tid == 0) {
         const uint32_t at = ring_at + (i % ST) * S::STAGE;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma_f16(tmem, smem_desc_sw128(at + k * 32), smem_desc_sw128(at + S::ROWS + k * 32), idesc_f16<T>(R, false),
+          tc_mma_f16(tmem, smem_desc_sw128(at + k * 32), smem_desc_sw128(at + S::ROWS + k * 32), idesc_f16<T>(R, false, false),
                      i > 0 || k > 0);
         tc_commit(&filled[i % ST]);
       }
@@ -284,7 +241,6 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
 
   // ---- out = base + hidden up, 64 columns a stage ----
   {
-    const int blocks = (N + 63) / 64, nb = crank < blocks ? (blocks - crank + C - 1) / C : 0;
     const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
     // A warp copies the rows and the half of their columns that it adds to, and
     // stores: eight rows by four chunks at a time.
@@ -297,7 +253,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
       on[q] = first + 8 * q < count;
     }
     const auto issue = [&](int i) {
-      const int col = (crank + i * C) * 64;
+      const int col = (b0 + i) * 64;
       const uint32_t at = ring_at + (i % ST) * S::STAGE;
       const bool in = col + sub * 8 < N;
       if (base) {
@@ -323,7 +279,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
     for (int i = 0; i <= nb; ++i) {
       if (i < nb) {
         copy_wait<ST - 2>();
-        fence_async_proxy();
+        fence_async_shared();
         __syncthreads();
         if (tid == 0) {
           tc_fence_after();
@@ -331,13 +287,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
 #pragma unroll
           for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
             tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
-                       smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, true), k > 0);
+                       smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, false, true), k > 0);
           tc_commit(&done[i & 1]);
         }
       }
       if (i == 0) continue;
       // the stage before, while the tensor cores work on this one
-      const int j = i - 1, col = (crank + j * C) * 64;
+      const int j = i - 1, col = (b0 + j) * 64;
       wait(&done[j & 1], (j >> 1) & 1);
       tc_fence_after();
       float v[32];

@@ -10,34 +10,46 @@ namespace {
 constexpr int PLAN_THREADS = 1024;
 constexpr unsigned ALL = 0xffffffffu;
 
+// Sixteen neighbouring ids, as groups (-1 from `rows` on).
+__device__ __forceinline__ void load_groups(const int32_t* ids, int64_t first, int rows, int L, int (&g)[16]) {
+  if (first + 16 <= rows && ((uintptr_t)(ids + first) & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int4 v = reinterpret_cast<const int4*>(ids + first)[i];
+      g[4 * i] = v.x, g[4 * i + 1] = v.y, g[4 * i + 2] = v.z, g[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = adapter_key(g[i], L);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = first + i < rows ? adapter_key(ids[first + i], L) : -1;
+  }
+}
+
 // Group blockIdx.x (an adapter, or L for rows without one): its first place,
 // the number of rows of the groups before it, and its rows in ascending order.
-// Every CTA goes through all ids, 16 a thread and round: no CTA waits for
-// another.
+// Every CTA goes through all ids, 16 a thread and round (up to 16384 rows, once):
+// no CTA waits for another.
 __global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_t* ids, int rows, int L,
                                                                     int32_t* starts, int32_t* row_list) {
   constexpr int PER = 16, ROUND = PLAN_THREADS * PER;
-  __shared__ int warp_sum[32], below;
+  __shared__ int less_sum[32], warp_sum[32];
   pdl_trigger();
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) below = 0;
-  __syncthreads();
-  int less = 0;
-  for (int64_t i = tid; i < rows; i += PLAN_THREADS) less += adapter_key(ids[i], L) < group;
-  less = __reduce_add_sync(ALL, less);
-  if (lane == 0 && less) atomicAdd(&below, less);
-  __syncthreads();
-  int at = below;
-  if (tid == 0) {
-    starts[group] = at;
-    if (group == L) starts[L + 1] = rows;
-  }
+  int g[PER], less = 0;
   for (int64_t base = 0; base < rows; base += ROUND) {
-    unsigned mine = 0;
-    const int64_t first = base + tid * PER;
+    load_groups(ids, base + tid * PER, rows, L, g);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (first + i < rows && adapter_key(ids[first + i], L) == group) mine |= 1u << i;
+    for (int i = 0; i < PER; ++i) less += (unsigned)g[i] < (unsigned)group;
+  }
+  less = __reduce_add_sync(ALL, less);
+  if (lane == 0) less_sum[warp] = less;
+  int at = 0;
+  for (int64_t base = 0; base < rows; base += ROUND) {
+    if (rows > ROUND) load_groups(ids, base + tid * PER, rows, L, g);  // (else they are still here)
+    unsigned mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine |= (unsigned)(g[i] == group) << i;
     const int n = __popc(mine);
     int upto = n;
 #pragma unroll
@@ -45,17 +57,24 @@ __global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_
       const int v = __shfl_up_sync(ALL, upto, o);
       if (lane >= o) upto += v;
     }
-    __syncthreads();  // (the round before has read the warps' sums)
     if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
+    if (base == 0) at = __reduce_add_sync(ALL, less_sum[lane]);
+    if (base == 0 && tid == 0) starts[group] = at;
     const int w = warp_sum[lane];
     const int before = __reduce_add_sync(ALL, lane < warp ? w : 0), all = __reduce_add_sync(ALL, w);
     int put = at + before + upto - n;
+    const int32_t first = (int32_t)(base + tid * PER);
     while (mine) {
-      row_list[put++] = (int32_t)(first + __ffs(mine) - 1);
+      row_list[put++] = first + __ffs(mine) - 1;
       mine &= mine - 1;
     }
     at += all;
+    __syncthreads();  // (the next round overwrites the warps' sums)
+  }
+  if (tid == 0) {
+    if (rows == 0) starts[group] = 0;
+    if (group == L) starts[L + 1] = rows;
   }
 }
 
@@ -63,7 +82,7 @@ int64_t words16(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Where the parts of a workspace lie, in 4-byte words, 16-byte aligned.
 struct Layout {
-  int64_t starts, row_list, hidden, sums[2], end;
+  int64_t starts, row_list, hidden, back, parts[2], sums[2], end;
 };
 
 int outer_unit(int64_t rows) {
@@ -78,8 +97,14 @@ Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
   l.starts = 0;
   l.row_list = words16(c.num_adapters + 2);
   l.hidden = l.row_list + words16(rows);
-  l.sums[0] = l.hidden + (backward ? words16(rows * c.rank) : 0);
-  const int64_t pieces = backward ? pieces_of(rows, c.num_adapters, outer_unit(rows)) : 0;
+  const int unit = outer_unit(rows);
+  const int64_t pieces = backward ? pieces_of(rows, c.num_adapters, unit) : 0;
+  // (two 16-bit parts of up to 16, 32, 64 or 128 ranks in rows of 128 bytes)
+  const int64_t part = pieces * unit * (c.rank <= 32 ? 1 : c.rank <= 64 ? 2 : 4) * 32;
+  l.back = l.hidden + (backward ? words16(rows * c.rank) : 0);
+  l.parts[0] = l.back + words16(2 * pieces);
+  l.parts[1] = l.parts[0] + part;
+  l.sums[0] = l.parts[1] + part;
   l.sums[1] = l.sums[0] + words16(pieces * c.rank * c.in_features);
   l.end = l.sums[1] + words16(pieces * c.rank * c.out_features);
   return l;
@@ -144,7 +169,13 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
   o.L = a.L;
   o.rank = a.rank;
   o.unit = outer_unit(a.rows);
-  for (int i = 0; i < 2; ++i) o.blocks[i] = (o.width[i] + 511) / 512;
+  for (int i = 0; i < 2; ++i) {
+    o.blocks[i] = (o.width[i] + (vec ? 255 : 511)) / (vec ? 256 : 512);
+    o.parts[i] = reinterpret_cast<unsigned char*>(w + l.parts[i]);
+    o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, a.L, o.unit);
+  }
+  o.alone = vec;
+  if (vec) return f16 ? launch_gradient_f16(o, s) : launch_gradient_bf16(o, s);
   return f16 ? launch_outer_f16(o, vec, s) : launch_outer_bf16(o, vec, s);
 }
 

@@ -158,8 +158,11 @@ struct OuterArgs {
   // set by the launch
   const int32_t *starts, *row_list;
   float* sums[2];
+  unsigned char* parts[2];  // hidden split in two (tensor cores)
+  float* back[2];           // and its scale, a piece each (FP16)
   int64_t rows;
   int L, rank, unit, blocks[2];
+  bool alone;               // an adapter's only piece writes its gradient itself
 };
 
 size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward);
@@ -174,5 +177,7 @@ cudaError_t launch_tensor_bf16(const AdapterArgs& a, cudaStream_t s);
 cudaError_t launch_tensor_f16(const AdapterArgs& a, cudaStream_t s);
 cudaError_t launch_outer_bf16(const OuterArgs& a, bool vec, cudaStream_t s);
 cudaError_t launch_outer_f16(const OuterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_gradient_bf16(const OuterArgs& a, cudaStream_t s);
+cudaError_t launch_gradient_f16(const OuterArgs& a, cudaStream_t s);
 
 }  // namespace moe
