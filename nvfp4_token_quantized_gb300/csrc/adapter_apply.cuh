@@ -1,13 +1,13 @@
-// adapter_apply.cuh - rows through their adapters: hidden = scale x down^T, out =
-// base + hidden up.  Also the gradient by x, with the factors exchanged.
+// adapter_apply.cuh - rows through their adapters, up to 128 of them (a decode step):
+// hidden = scale x down^T, out = base + hidden up, in one launch.
 //
-// Bound by bytes (x, base and out once each) up to a rank of some 64, so one
-// kernel does both products and the hidden rows never leave the SMs.  A cluster
-// takes a tile of up to 128 rows of one adapter: its CTAs split the first
+// Bound by the adapters' bytes and by latency.  A cluster takes the rows of one
+// adapter, which its CTAs find in ids themselves; the CTAs split the first
 // product's long axis, add their parts through distributed shared memory, and
-// split the second product's columns.  Few rows (a decode step) thus still
-// spread over the GPU.  Within a CTA a warp has 16 rows; fewer rows leave more
-// warps for the split.
+// split the second product's columns, so that few rows still spread over the GPU.
+// Within a CTA a warp has 16 rows; fewer rows leave more warps for the split.  The
+// operands go from memory into the fragments of mma.sync (adapter_common.cuh): with
+// one to some rows an adapter a tile of 128 would be empty for the most part.
 //
 // hidden is FP32; the second product takes it as two 16-bit parts (split2), as a
 // single rounding would show beside the output's own.
@@ -38,37 +38,22 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   uint4* frags = reinterpret_cast<uint4*>(smem);
   float* hid = reinterpret_cast<float*>(smem + S::FIRST);
   __shared__ int row_of[ADAPTER_TILE];
-  __shared__ Piece found;
-  __shared__ int counts[4];  // of a direct call's warps
+  __shared__ int counts[4];  // of the warps that hold a row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
+  const int C = a.cluster, crank = blockIdx.x % C, group = blockIdx.x / C;
 
-  // ---- the tile's rows ----
-  int group, count;
-  if (a.direct) {
-    // every group is one tile: its rows are found in ids themselves
-    group = number;
-    const bool mine = tid < a.rows && adapter_key(a.ids[tid], a.L) == group;
-    const unsigned m = __ballot_sync(0xffffffffu, mine);
-    if (warp < 4 && lane == 0) counts[warp] = __popc(m);
-    __syncthreads();
-    int before = 0;
-    count = 0;
+  // ---- the group's rows, found in ids ----
+  const bool mine = tid < a.rows && adapter_key(a.ids[tid], a.L) == group;
+  const unsigned m = __ballot_sync(0xffffffffu, mine);
+  if (warp < 4 && lane == 0) counts[warp] = __popc(m);
+  __syncthreads();
+  int before = 0, count = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      before += w < warp ? counts[w] : 0;
-      count += counts[w];
-    }
-    if (mine) row_of[before + __popc(m & ((1u << lane) - 1))] = tid;
-    pdl_wait();
-  } else {
-    pdl_wait();
-    const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
-    group = p.group;
-    count = group < 0 ? 0 : p.count;
-    if (tid < count) row_of[tid] = a.row_list[p.start + tid];
+  for (int w = 0; w < 4; ++w) {
+    before += w < warp ? counts[w] : 0;
+    count += counts[w];
   }
-  pdl_trigger();
+  if (mine) row_of[before + __popc(m & ((1u << lane) - 1))] = tid;
   if (count == 0) return;  // (the whole cluster)
   __syncthreads();
 
@@ -266,7 +251,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
 }
 
 template <typename T, int NT, bool VEC>
-cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s, bool pdl) {
+cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = adapter_apply_kernel<T, NT, VEC>;
   constexpr int bytes = ApplyShared<NT>::BYTES;
@@ -274,13 +259,13 @@ cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s, bool pdl) {
     const cudaError_t e = raise_shared(kernel, bytes, done);
     if (e != cudaSuccess) return e;
   }
-  return launch_clustered(kernel, a, bytes, pdl, s);
+  return launch_clustered(kernel, a, bytes, false, s);
 }
 
 template <typename T>
-cudaError_t launch_apply(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s) {
+cudaError_t launch_apply(const AdapterArgs& a, bool vec, cudaStream_t s) {
   switch ((a.rank + 7) / 8) {
-#define MOE_APPLY(NT) return vec ? launch_apply_one<T, NT, true>(a, s, pdl) : launch_apply_one<T, NT, false>(a, s, pdl)
+#define MOE_APPLY(NT) return vec ? launch_apply_one<T, NT, true>(a, s) : launch_apply_one<T, NT, false>(a, s)
     case 1: MOE_APPLY(1);
     case 2: MOE_APPLY(2);
     case 3: MOE_APPLY(3);

@@ -1,17 +1,12 @@
 // The low-rank adapters' kernels for bf16 rows and factors.
 #include "adapter_apply.cuh"
 #include "adapter_gradient.cuh"
-#include "adapter_outer.cuh"
 #include "adapter_tensor.cuh"
 
 namespace moe {
-cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s) {
-  return launch_apply<__nv_bfloat16>(a, vec, pdl, s);
-}
-cudaError_t launch_tensor_bf16(const AdapterArgs& a, cudaStream_t s) { return launch_tensor<__nv_bfloat16>(a, s); }
-cudaError_t launch_outer_bf16(const OuterArgs& a, bool vec, cudaStream_t s) { return launch_outer<__nv_bfloat16>(a, vec, s); }
-cudaError_t launch_gradient_bf16(const OuterArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_gradient<__nv_bfloat16>(a, s);
-  return e == cudaSuccess ? launch_join<__nv_bfloat16>(a, s) : e;
+cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, cudaStream_t s) { return launch_apply<__nv_bfloat16>(a, vec, s); }
+cudaError_t launch_tensor_bf16(const AdapterArgs& a, bool vec, cudaStream_t s) { return launch_tensor<__nv_bfloat16>(a, vec, s); }
+cudaError_t launch_gradient_bf16(const OuterArgs& a, bool vec, cudaStream_t s) {
+  return launch_gradient<__nv_bfloat16>(a, vec, s);
 }
 }  // namespace moe

@@ -1,6 +1,6 @@
-// adapter_gradient.cuh - the gradients of an adapter's factors (as
-// adapter_outer.cuh) on the tensor cores' tcgen05 path: D = x^T hidden, 128 columns
-// of x by the ranks, contraction over the rows.
+// adapter_gradient.cuh - the gradients of an adapter's factors, sums over its rows
+// of hidden[row] (as a column) times x[row] (as a row), on the tensor cores' tcgen05
+// path: D = x^T hidden, 128 columns of x by the ranks, contraction over the rows.
 //
 // Both operands lie as they are stored, rows of neighbouring columns, which is the
 // layout of operands whose contraction runs across rows.  x's rows come by
@@ -9,15 +9,21 @@
 // tensor cores read them, once for all columns.  With FP16 the parts of a piece
 // share a power of two.
 //
+// Rows that do not start on 16 bytes come as in adapter_tensor.cuh.  The CTAs' FP32
+// sums are joined by a last kernel in the order of the rows.
+//
 // A CTA takes a piece (up to `unit` rows of one adapter) and 256 columns.  Bound by
 // the bytes of x and dout, once each.
 #pragma once
+
+#include <algorithm>
 
 #include "adapter_mma.cuh"
 
 namespace moe {
 
 constexpr int GRADIENT_COLUMNS = 256, GRADIENT_ROWS = 32;  // of a CTA, of a stage
+constexpr int SPLIT_ROWS = 64;                             // of a CTA that splits
 
 template <int R>
 struct GradientShared {
@@ -41,6 +47,7 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
   const int tid = threadIdx.x, side = blockIdx.y;
   pdl_wait();
   pdl_trigger();
+  // (blockIdx.z: SPLIT_ROWS of the piece's rows)
   const Piece p = find_piece(a.starts, a.L, a.unit, blockIdx.x, &found);
   if (p.group < 0) return;
   const float* hidden = a.hidden[side];
@@ -68,11 +75,12 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
     s = exponent_scale(m, back);
-    if (tid == 0) a.back[side][blockIdx.x] = back;
+    if (tid == 0 && blockIdx.z == 0) a.back[side][blockIdx.x] = back;
   }
   const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
   unsigned char* to = a.parts[side] + (int64_t)blockIdx.x * (a.unit / GRADIENT_ROWS) * S::HIDDEN;
-  for (int r = tid / G; r < stages * GRADIENT_ROWS; r += 256 / G) {
+  const int stop = min(stages * GRADIENT_ROWS, (int)(blockIdx.z + 1) * SPLIT_ROWS);
+  for (int r = blockIdx.z * SPLIT_ROWS + tid / G; r < stop; r += 256 / G) {
     float v[8];
     load(r, v);
     uint4 hi, lo;
@@ -87,7 +95,7 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
   }
 }
 
-template <typename T, int R>
+template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(const OuterArgs a) {
   using S = GradientShared<R>;
   constexpr int ST = S::STAGES;
@@ -136,24 +144,51 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(co
   // a warp copies whole rows: 32 chunks of 16 bytes, four rows a warp
   const int col = n0 + lane * 8;
   const bool in = col < N;
+  constexpr int Q = GRADIENT_ROWS / ADAPTER_WARPS;
   const auto issue = [&](int i) {
     const uint32_t at = ring + (i % ST) * S::STAGE;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int q = 0; q < GRADIENT_ROWS / ADAPTER_WARPS; ++q) {
-      const int row = warp + q * ADAPTER_WARPS, r = i * GRADIENT_ROWS + row;
-      const bool on = in && r < p.count;
-      copy16(at + (lane >> 3) * S::PANEL + swizzled(row, lane & 7), on ? x + row_of[r] * stride + col : x, on);
+      for (int q = 0; q < Q; ++q) {
+        const int row = warp + q * ADAPTER_WARPS, r = i * GRADIENT_ROWS + row;
+        const bool on = in && r < p.count;
+        copy16(at + (lane >> 3) * S::PANEL + swizzled(row, lane & 7), on ? x + row_of[r] * stride + col : x, on);
+      }
     }
 #pragma unroll
     for (int c = tid; c < S::HIDDEN / 16; c += ADAPTER_THREADS)
       copy16(at + S::X + c * 16, parts + (int64_t)i * S::HIDDEN + c * 16, true);
+  };
+  Loose lx[VEC ? 1 : Q];
+  bool odd[VEC ? 1 : Q];
+  const auto fetch = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int r = i * GRADIENT_ROWS + warp + q * ADAPTER_WARPS;
+      const bool on = in && r < p.count;
+      const T* at = on ? x + row_of[r] * stride + col : x;
+      lx[q].load(at, N - col, on);
+      odd[q] = Loose::odd(at);
+    }
+  };
+  const auto put = [&](int i) {
+    const uint32_t at = ring + (i % ST) * S::STAGE;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      put16(at + (lane >> 3) * S::PANEL + swizzled(warp + q * ADAPTER_WARPS, lane & 7), lx[q].chunk(odd[q], N - col));
   };
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) {
     if (i < stages) issue(i);
     copy_commit();
   }
+  if constexpr (!VEC) fetch(0);
   for (int i = 0; i < stages; ++i) {
+    if constexpr (!VEC) {
+      if (i >= ST) wait(&filled[i % ST], ((i - ST) / ST) & 1);
+      put(i);
+      if (i + 1 < stages) fetch(i + 1);
+    }
     copy_wait<ST - 2>();
     fence_async_shared();
     __syncthreads();
@@ -188,7 +223,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(co
   const float back = std::is_same<T, __nv_bfloat16>::value ? 1.0f : a.back[side][blockIdx.x];
   const float lost = gave_up ? NAN : 0.0f;
   const int64_t n = (int64_t)a.rank * N;
-  const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // the adapter's only piece
+  const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
   float* sums = a.sums[side] + (int64_t)blockIdx.x * n + c;
   T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
 #pragma unroll
@@ -216,25 +251,61 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(co
   }
 }
 
-template <typename T, int R>
+// A factor's gradient: its pieces' sums in order, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) adapter_join_kernel(const OuterArgs a) {
+  pdl_wait();
+  const int side = blockIdx.z, group = blockIdx.y;
+  const int64_t n = (int64_t)a.rank * a.width[side];
+  const int lo = a.starts[group], hi = a.starts[group + 1];
+  const int parts = (hi - lo + a.unit - 1) / a.unit;
+  if (parts == 1) return;  // (written already)
+  const float* sums = a.sums[side] + (lo / a.unit + group) * n;
+  T* out = static_cast<T*>(a.grad[side]) + group * n;
+  constexpr int U = 4;  // elements and pieces whose loads are in flight together
+  for (int64_t i = (int64_t)blockIdx.x * 256 * U + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256 * U) {
+    float s[U] = {};
+    for (int p = 0; p < parts; p += U) {
+      float v[U][U];
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+#pragma unroll
+        for (int e = 0; e < U; ++e) v[q][e] = p + q < parts && i + e * 256 < n ? sums[(p + q) * n + i + e * 256] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+#pragma unroll
+        for (int e = 0; e < U; ++e) s[e] += v[q][e];
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e)
+      if (i + e * 256 < n) out[i + e * 256] = from_f32<T>(s[e]);
+  }
+}
+
+template <typename T, int R, bool VEC>
 cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  const auto kernel = adapter_gradient_kernel<T, R>;
+  const auto kernel = adapter_gradient_kernel<T, R, VEC>;
   cudaError_t e = raise_shared(kernel, GradientShared<R>::BYTES, done);
   if (e != cudaSuccess) return e;
   const unsigned pieces = (unsigned)pieces_of(a.rows, a.L, a.unit);
-  e = launch_k(adapter_split_kernel<T, R>, dim3(pieces, 2), dim3(256), 0, s, true, a);
+  e = launch_k(adapter_split_kernel<T, R>, dim3(pieces, 2, (unsigned)(a.unit / SPLIT_ROWS)), dim3(256), 0, s, true,
+               a);
   if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(pieces, (unsigned)(a.blocks[0] + a.blocks[1])), dim3(ADAPTER_THREADS),
-                  GradientShared<R>::BYTES, s, true, a);
+  e = launch_k(kernel, dim3(pieces, (unsigned)(a.blocks[0] + a.blocks[1])), dim3(ADAPTER_THREADS),
+               GradientShared<R>::BYTES, s, true, a);
+  if (e != cudaSuccess) return e;
+  const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);
+  const dim3 grid((unsigned)std::min<int64_t>((n + 1023) / 1024, 1024), (unsigned)a.L, 2);
+  return launch_k(adapter_join_kernel<T>, grid, dim3(256), 0, s, true, a);
 }
 
 template <typename T>
-cudaError_t launch_gradient(const OuterArgs& a, cudaStream_t s) {
-  if (a.rank <= 16) return launch_gradient_one<T, 16>(a, s);
-  if (a.rank <= 32) return launch_gradient_one<T, 32>(a, s);
-  if (a.rank <= 64) return launch_gradient_one<T, 64>(a, s);
-  return launch_gradient_one<T, 128>(a, s);
+cudaError_t launch_gradient(const OuterArgs& a, bool vec, cudaStream_t s) {
+  if (a.rank <= 16) return vec ? launch_gradient_one<T, 16, true>(a, s) : launch_gradient_one<T, 16, false>(a, s);
+  if (a.rank <= 32) return vec ? launch_gradient_one<T, 32, true>(a, s) : launch_gradient_one<T, 32, false>(a, s);
+  if (a.rank <= 64) return vec ? launch_gradient_one<T, 64, true>(a, s) : launch_gradient_one<T, 64, false>(a, s);
+  return vec ? launch_gradient_one<T, 128, true>(a, s) : launch_gradient_one<T, 128, false>(a, s);
 }
 
 }  // namespace moe

@@ -14,6 +14,34 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Sixteen bytes of a row that starts anywhere: the aligned words around them, to be
+// put in order once they have arrived.  (Words that hold an element of the row are
+// read, others not.)
+struct Loose {
+  uint32_t w[5];
+  __device__ __forceinline__ static bool odd(const void* at) { return ((uintptr_t)at & 2) != 0; }
+  // `left` elements of the row from `at` on
+  __device__ __forceinline__ void load(const void* at, int left, bool on) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>((uintptr_t)at & ~(uintptr_t)3);
+    const int o = odd(at);
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = on && 2 * j - o < min(left, 8) ? p[j] : 0u;
+  }
+  __device__ __forceinline__ uint4 chunk(bool odd, int left) const {
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+      if (2 * j + 1 >= left) r[j] = 2 * j < left ? r[j] & 0xffffu : 0u;
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+__device__ __forceinline__ void put16(uint32_t dst, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // This thread's writes to shared memory so far, before later accesses of the
 // tensor cores: its own CTA's memory, or any in the cluster.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -11,6 +11,10 @@
 // contiguous.  hidden enters the second product as two 16-bit parts side by side
 // (split2), which doubles a contraction of 16 to 128 and costs nothing visible.
 //
+// Rows that do not start on 16 bytes (or widths that are no multiple of 8) are read
+// as aligned words one stage ahead, put in order in registers and stored to the
+// same places; their output leaves element by element.
+//
 // Stages follow one another without roles: every thread copies, waits for its own
 // copies, meets the others, and one thread issues the stage's products; the slot is
 // filled again when their commit has arrived.  Two CTAs share an SM, so that one's
@@ -41,10 +45,10 @@ struct TensorShared {
   static_assert(ADAPTER_TILE * RP * 4 <= STAGES * STAGE, "the first product's sums lie in the stages");
 };
 
-template <typename T, int R>
+template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tensor_kernel(const AdapterArgs a) {
   using S = TensorShared<R>;
-  constexpr int ST = S::STAGES, RP = S::RP;
+  constexpr int ST = S::STAGES, RP = S::RP, W = (R + 31) / 32;  // (a thread's chunks of a factor)
   constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   __syncthreads();
   if (group == a.L) {
     if (warp == 0) tmem_dealloc(tmem, 128);
-    rows_without_adapter<T, true>(a, row_of, count, crank, C);
+    rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
     return;
   }
   const auto wait = [&](uint64_t* bar, int parity) {
@@ -130,13 +134,45 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         copy16(at + S::ROWS + swizzled(r, sub), have ? down + (int64_t)r * K + col : down, have);
       }
     };
+    Loose lx[VEC ? 1 : 4], lw[VEC ? 1 : W];
+    const auto fetch = [&](int i) {  // (rows that start anywhere)
+      const int col = (c0 + i) * 64 + sub * 8;
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) {
-      if (i < nk) issue(i);
-      copy_commit();
+      for (int q = 0; q < 4; ++q) lx[q].load(px[q] + col, K - col, on[q]);
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        const int r = r0 + 32 * q;
+        lw[q].load(down + (int64_t)r * K + col, K - col, r < a.rank);
+      }
+    };
+    const auto put = [&](int i) {
+      const int col = (c0 + i) * 64 + sub * 8;
+      const uint32_t at = ring_at + (i % ST) * S::STAGE;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) put16(at + swizzled(r0 + 32 * q, sub), lx[q].chunk(Loose::odd(px[q] + col), K - col));
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        const int r = r0 + 32 * q;
+        if (r < R) put16(at + S::ROWS + swizzled(r, sub), lw[q].chunk(Loose::odd(down + (int64_t)r * K + col), K - col));
+      }
+    };
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < ST - 1; ++i) {
+        if (i < nk) issue(i);
+        copy_commit();
+      }
+    } else {
+      if (nk > 0) fetch(0);
     }
     for (int i = 0; i < nk; ++i) {
-      copy_wait<ST - 2>();
+      if constexpr (VEC) {
+        copy_wait<ST - 2>();
+      } else {
+        if (i >= ST) wait(&filled[i % ST], ((i - ST) / ST) & 1);
+        put(i);
+        if (i + 1 < nk) fetch(i + 1);
+      }
       fence_async_shared();
       __syncthreads();
       if (tid == 0) {
@@ -147,11 +183,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
                      i > 0 || k > 0);
         tc_commit(&filled[i % ST]);
       }
-      if (i + ST - 1 < nk) {
-        if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
-        issue(i + ST - 1);
+      if constexpr (VEC) {
+        if (i + ST - 1 < nk) {
+          if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
+          issue(i + ST - 1);
+        }
+        copy_commit();
       }
-      copy_commit();
     }
     copy_wait<0>();
     if (nk > 0) wait(&filled[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
@@ -159,8 +197,74 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
     tc_fence_after();
   }
 
-  // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
   const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+
+  // ---- the second product's copies ----
+  const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
+  // A warp copies the rows and the half of their columns that it adds to, and
+  // stores: eight rows by four chunks at a time.
+  const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2), up_row = tid >> 3, up_chunk = tid & 7;
+  int64_t at_row[4];
+  bool on[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    at_row[q] = row_of[first + 8 * q];
+    on[q] = first + 8 * q < count;
+  }
+  // Stage i lies in slot (i + FREE) % ST: the first FREE slots hold the sums until
+  // they are joined, the others can be filled at once.
+  constexpr int FREE = (ADAPTER_TILE * RP * 4 + S::STAGE - 1) / S::STAGE;
+  static_assert(FREE < ST, "a slot beside the sums");
+  const auto issue = [&](int i) {
+    const int col = (b0 + i) * 64;
+    const uint32_t at = ring_at + ((i + FREE) % ST) * S::STAGE;
+    const bool in = col + sub * 8 < N;
+    if (base) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        copy16(at + swizzled(first + 8 * q, sub), in ? base + at_row[q] * a.base_stride + col + sub * 8 : base,
+               in && on[q]);
+    }
+    const bool up_in = col + up_chunk * 8 < N;
+#pragma unroll
+    for (int r = up_row; r < R; r += 32) {
+      const bool have = up_in && r < a.rank;
+      copy16(at + S::ROWS + swizzled(r, up_chunk), have ? up + (int64_t)r * N + col + up_chunk * 8 : up, have);
+    }
+  };
+  Loose lb[VEC ? 1 : 4], lu[VEC ? 1 : W];
+  const auto fetch = [&](int i) {
+    const int cb = (b0 + i) * 64 + sub * 8, cu = (b0 + i) * 64 + up_chunk * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) lb[q].load(base + at_row[q] * a.base_stride + cb, N - cb, base && on[q]);
+#pragma unroll
+    for (int q = 0; q < W; ++q) lu[q].load(up + (int64_t)(up_row + 32 * q) * N + cu, N - cu, up_row + 32 * q < a.rank);
+  };
+  const auto put = [&](int i) {
+    const uint32_t at = ring_at + ((i + FREE) % ST) * S::STAGE;
+    const int cb = (b0 + i) * 64 + sub * 8, cu = (b0 + i) * 64 + up_chunk * 8;
+    if (base) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        put16(at + swizzled(first + 8 * q, sub), lb[q].chunk(Loose::odd(base + at_row[q] * a.base_stride + cb), N - cb));
+    }
+#pragma unroll
+    for (int q = 0; q < W; ++q)
+      if (up_row + 32 * q < R)
+        put16(at + S::ROWS + swizzled(up_row + 32 * q, up_chunk),
+              lu[q].chunk(Loose::odd(up + (int64_t)(up_row + 32 * q) * N + cu), N - cu));
+  };
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < ST - FREE; ++i) {
+      if (i < nb) issue(i);
+      copy_commit();
+    }
+  } else {
+    if (nb > 0) fetch(0);
+  }
+
+  // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
   {
     float* to = part + mine * RP + half * (R / 2);
 #pragma unroll
@@ -241,49 +345,27 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
 
   // ---- out = base + hidden up, 64 columns a stage ----
   {
-    const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
-    // A warp copies the rows and the half of their columns that it adds to, and
-    // stores: eight rows by four chunks at a time.
-    const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2);
-    int64_t at_row[4];
-    bool on[4];
+    if constexpr (VEC) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      at_row[q] = row_of[first + 8 * q];
-      on[q] = first + 8 * q < count;
-    }
-    const auto issue = [&](int i) {
-      const int col = (b0 + i) * 64;
-      const uint32_t at = ring_at + (i % ST) * S::STAGE;
-      const bool in = col + sub * 8 < N;
-      if (base) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          copy16(at + swizzled(first + 8 * q, sub), in ? base + at_row[q] * a.base_stride + col + sub * 8 : base,
-                 in && on[q]);
+      for (int i = ST - FREE; i < ST; ++i) {
+        if (i < nb) issue(i);
+        copy_commit();
       }
-      const int chunk = tid & 7;
-      const bool up_in = col + chunk * 8 < N;
-#pragma unroll
-      for (int r = tid >> 3; r < R; r += 32) {
-        const bool have = up_in && r < a.rank;
-        copy16(at + S::ROWS + swizzled(r, chunk), have ? up + (int64_t)r * N + col + chunk * 8 : up, have);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < ST; ++i) {
-      if (i < nb) issue(i);
-      copy_commit();
     }
     const float bk = back[mine];
     for (int i = 0; i <= nb; ++i) {
       if (i < nb) {
-        copy_wait<ST - 2>();
+        if constexpr (VEC) {
+          copy_wait<ST - 2>();
+        } else {
+          put(i);  // (the slot's last stage has been read: its products and rows, above)
+          if (i + 1 < nb) fetch(i + 1);
+        }
         fence_async_shared();
         __syncthreads();
         if (tid == 0) {
           tc_fence_after();
-          const uint32_t b = ring_at + (i % ST) * S::STAGE + S::ROWS;
+          const uint32_t b = ring_at + ((i + FREE) % ST) * S::STAGE + S::ROWS;
 #pragma unroll
           for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
             tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
@@ -298,7 +380,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
       tc_fence_after();
       float v[32];
       tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (j & 1) * 64 + half * 32, v);
-      unsigned char* tile = ring + (j % ST) * S::STAGE;
+      unsigned char* tile = ring + ((j + FREE) % ST) * S::STAGE;
       uint4 y[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -318,17 +400,29 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         *reinterpret_cast<uint4*>(tile + swizzled(mine, half * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       __syncwarp();
-      uint4 o[4];
+      if constexpr (VEC) {
+        uint4 o[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const uint4*>(tile + swizzled(first + 8 * q, sub));
-      __syncwarp();  // (the warp's part of the slot is filled again below)
-      if (col + sub * 8 < N) {
+        for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const uint4*>(tile + swizzled(first + 8 * q, sub));
+        __syncwarp();  // (the warp's part of the slot is filled again below)
+        if (col + sub * 8 < N) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (on[q]) *reinterpret_cast<uint4*>(out + at_row[q] * a.out_stride + col + sub * 8) = o[q];
+          for (int q = 0; q < 4; ++q)
+            if (on[q]) *reinterpret_cast<uint4*>(out + at_row[q] * a.out_stride + col + sub * 8) = o[q];
+        }
+        if (j + ST < nb) issue(j + ST);
+        copy_commit();
+      } else {
+        // a row's 32 columns, an element a lane
+        const int c = col + half * 32 + lane;
+        const unsigned char* from = tile + (lane & 7) * 2;
+#pragma unroll 4
+        for (int r = quarter * 32; r < min(quarter * 32 + 32, count); ++r) {
+          const uint16_t v = *reinterpret_cast<const uint16_t*>(from + swizzled(r, half * 4 + (lane >> 3)));
+          if (c < N) reinterpret_cast<uint16_t*>(out)[row_of[r] * a.out_stride + c] = v;
+        }
+        __syncwarp();
       }
-      if (j + ST < nb) issue(j + ST);
-      copy_commit();
     }
     copy_wait<0>();
   }
@@ -340,21 +434,21 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   }
 }
 
-template <typename T, int R>
+template <typename T, int R, bool VEC>
 cudaError_t launch_tensor_one(const AdapterArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  const auto kernel = adapter_tensor_kernel<T, R>;
+  const auto kernel = adapter_tensor_kernel<T, R, VEC>;
   const cudaError_t e = raise_shared(kernel, TensorShared<R>::BYTES, done);
   if (e != cudaSuccess) return e;
   return launch_clustered(kernel, a, TensorShared<R>::BYTES, true, s);
 }
 
 template <typename T>
-cudaError_t launch_tensor(const AdapterArgs& a, cudaStream_t s) {
-  if (a.rank <= 16) return launch_tensor_one<T, 16>(a, s);
-  if (a.rank <= 32) return launch_tensor_one<T, 32>(a, s);
-  if (a.rank <= 64) return launch_tensor_one<T, 64>(a, s);
-  return launch_tensor_one<T, 128>(a, s);
+cudaError_t launch_tensor(const AdapterArgs& a, bool vec, cudaStream_t s) {
+  if (a.rank <= 16) return vec ? launch_tensor_one<T, 16, true>(a, s) : launch_tensor_one<T, 16, false>(a, s);
+  if (a.rank <= 32) return vec ? launch_tensor_one<T, 32, true>(a, s) : launch_tensor_one<T, 32, false>(a, s);
+  if (a.rank <= 64) return vec ? launch_tensor_one<T, 64, true>(a, s) : launch_tensor_one<T, 64, false>(a, s);
+  return vec ? launch_tensor_one<T, 128, true>(a, s) : launch_tensor_one<T, 128, false>(a, s);
 }
 
 }  // namespace moe

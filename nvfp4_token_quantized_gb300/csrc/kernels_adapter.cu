@@ -86,8 +86,8 @@ struct Layout {
 };
 
 int outer_unit(int64_t rows) {
-  // about sixteen pieces of a large batch: with eight column blocks a side that
-  // fills the SMs, and the pieces' FP32 sums stay small beside the rows
+  // about sixteen pieces of a large batch: with a side's column blocks that fills
+  // the SMs, and the pieces' FP32 sums stay small beside the rows
   const int64_t unit = (rows + 15) / 16;
   return (int)std::min<int64_t>(std::max<int64_t>((unit + 63) / 64 * 64, 64), 1024);
 }
@@ -125,11 +125,10 @@ int cluster_of(int64_t tiles, int64_t rows, int L) {
 }
 
 cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
-  a.direct = !planned;
   a.tiles = planned ? pieces_of(a.rows, a.L + 1, ADAPTER_TILE) : a.L + 1;
   a.cluster = cluster_of(a.tiles, a.rows, a.L);
-  if (planned && vec) return f16 ? launch_tensor_f16(a, s) : launch_tensor_bf16(a, s);
-  return f16 ? launch_apply_f16(a, vec, planned, s) : launch_apply_bf16(a, vec, planned, s);
+  if (planned) return f16 ? launch_tensor_f16(a, vec, s) : launch_tensor_bf16(a, vec, s);
+  return f16 ? launch_apply_f16(a, vec, s) : launch_apply_bf16(a, vec, s);
 }
 
 }  // namespace
@@ -170,13 +169,11 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
   o.rank = a.rank;
   o.unit = outer_unit(a.rows);
   for (int i = 0; i < 2; ++i) {
-    o.blocks[i] = (o.width[i] + (vec ? 255 : 511)) / (vec ? 256 : 512);
+    o.blocks[i] = (o.width[i] + 255) / 256;
     o.parts[i] = reinterpret_cast<unsigned char*>(w + l.parts[i]);
     o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, a.L, o.unit);
   }
-  o.alone = vec;
-  if (vec) return f16 ? launch_gradient_f16(o, s) : launch_gradient_bf16(o, s);
-  return f16 ? launch_outer_f16(o, vec, s) : launch_outer_bf16(o, vec, s);
+  return f16 ? launch_gradient_f16(o, vec, s) : launch_gradient_bf16(o, vec, s);
 }
 
 }  // namespace moe

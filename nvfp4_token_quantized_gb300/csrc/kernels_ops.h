@@ -145,7 +145,6 @@ struct AdapterArgs {
   const int32_t *starts, *row_list;
   int64_t tiles;
   int cluster;
-  bool direct;  // up to 128 rows: each CTA finds its own
 };
 
 // Gradients of both factors: sums over an adapter's rows of hidden^T x.
@@ -158,11 +157,10 @@ struct OuterArgs {
   // set by the launch
   const int32_t *starts, *row_list;
   float* sums[2];
-  unsigned char* parts[2];  // hidden split in two (tensor cores)
+  unsigned char* parts[2];  // hidden split in two
   float* back[2];           // and its scale, a piece each (FP16)
   int64_t rows;
   int L, rank, unit, blocks[2];
-  bool alone;               // an adapter's only piece writes its gradient itself
 };
 
 size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward);
@@ -171,13 +169,11 @@ cudaError_t launch_adapter(AdapterArgs a, const moe_adapter_config& c, bool vec,
 // a: the gradient by x (its first factor is up); hidden[0] is set by the launch.
 cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapter_config& c, bool vec, void* workspace,
                                     cudaStream_t s);
-cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
-cudaError_t launch_apply_f16(const AdapterArgs& a, bool vec, bool pdl, cudaStream_t s);
-cudaError_t launch_tensor_bf16(const AdapterArgs& a, cudaStream_t s);
-cudaError_t launch_tensor_f16(const AdapterArgs& a, cudaStream_t s);
-cudaError_t launch_outer_bf16(const OuterArgs& a, bool vec, cudaStream_t s);
-cudaError_t launch_outer_f16(const OuterArgs& a, bool vec, cudaStream_t s);
-cudaError_t launch_gradient_bf16(const OuterArgs& a, cudaStream_t s);
-cudaError_t launch_gradient_f16(const OuterArgs& a, cudaStream_t s);
+cudaError_t launch_apply_bf16(const AdapterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_apply_f16(const AdapterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_tensor_bf16(const AdapterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_tensor_f16(const AdapterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_gradient_bf16(const OuterArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_gradient_f16(const OuterArgs& a, bool vec, cudaStream_t s);
 
 }  // namespace moe
