@@ -259,7 +259,7 @@ cudaError_t launch_apply_one(const AdapterArgs& a, cudaStream_t s) {
     const cudaError_t e = raise_shared(kernel, bytes, done);
     if (e != cudaSuccess) return e;
   }
-  return launch_clustered(kernel, a, bytes, false, s);
+  return launch_clustered(kernel, a, ADAPTER_THREADS, bytes, false, s);
 }
 
 template <typename T>

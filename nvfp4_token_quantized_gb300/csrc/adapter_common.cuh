@@ -127,10 +127,10 @@ __device__ __forceinline__ void rows_without_adapter(const AdapterArgs& a, const
 
 // tiles x cluster CTAs; pdl: may start while its predecessor finishes.
 template <typename K>
-cudaError_t launch_clustered(K kernel, const AdapterArgs& a, int bytes, bool pdl, cudaStream_t s) {
+cudaError_t launch_clustered(K kernel, const AdapterArgs& a, int threads, int bytes, bool pdl, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.tiles * a.cluster));
-  cfg.blockDim = dim3(ADAPTER_THREADS);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

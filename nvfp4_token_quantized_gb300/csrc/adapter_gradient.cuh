@@ -96,20 +96,23 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
 }
 
 template <typename T, int R, bool VEC>
-__global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(const OuterArgs a) {
+__global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(const OuterArgs a) {
   using S = GradientShared<R>;
   constexpr int ST = S::STAGES;
   extern __shared__ unsigned char raw[];
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   __shared__ Piece found;
-  __shared__ uint64_t filled[ST];
+  __shared__ uint64_t arrived[ST], freed[ST];  // copies in, products done
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   __shared__ int row_of[1024];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // (set up while the kernels before run)
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(&filled[i], 1);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&arrived[i], VEC ? ADAPTER_THREADS : 2 * ADAPTER_THREADS);
+      mbar_init(&freed[i], 1);
+    }
     gave_up = 0;
     fence_mbarrier_init();
   }
@@ -132,10 +135,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(co
   const int n0 = (blockIdx.y - (side ? a.blocks[0] : 0)) * GRADIENT_COLUMNS, N = a.width[side];
   const T* x = static_cast<const T*>(a.x[side]);
   const int64_t stride = a.stride[side];
-  for (int r = tid; r < p.count; r += ADAPTER_THREADS) row_of[r] = a.row_list[p.start + r];
+  for (int r = tid; r < p.count; r += TENSOR_THREADS) row_of[r] = a.row_list[p.start + r];
   __syncthreads();
-  const auto wait = [&](uint64_t* bar, int parity) {
+  const auto wait_alone = [&](uint64_t* bar, int parity) {  // (one lane)
     if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
+  };
+  const auto wait = [&](uint64_t* bar, int parity) {  // (whole warps)
+    wait_alone(bar, parity);
     __syncwarp();
   };
 
@@ -177,70 +183,69 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, 2) adapter_gradient_kernel(co
     for (int q = 0; q < Q; ++q)
       put16(at + (lane >> 3) * S::PANEL + swizzled(warp + q * ADAPTER_WARPS, lane & 7), lx[q].chunk(odd[q], N - col));
   };
+  if (warp == ADAPTER_WARPS) {
+    if (lane == 0)
+      for (int i = 0; i < stages; ++i) {
+        wait_alone(&arrived[i % ST], (i / ST) & 1);
+        fence_async_shared();
+        const uint32_t at = ring + (i % ST) * S::STAGE;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) {
-    if (i < stages) issue(i);
-    copy_commit();
+        for (int k = 0; k < GRADIENT_ROWS / 16; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < S::PARTS; ++q) {
+              // (128 ranks: two panels of first parts, two of second ones)
+              const int to = R > 64 ? q & 1 : 0, first = R > 64 ? q < 2 : q == 0;
+              tc_mma_f16(tmem + m * S::D + to * 64, smem_desc_rows(at + 2 * m * S::PANEL + k * 2048, S::PANEL),
+                         smem_desc_rows(at + S::X + q * S::PANEL + k * 2048), idesc_f16<T>(S::N, true, true),
+                         i > 0 || k > 0 || !first);
+            }
+        tc_commit(&freed[i % ST]);
+      }
+    __syncwarp();
+  } else {
+    if constexpr (!VEC) fetch(0);
+    for (int i = 0; i < stages; ++i) {
+      if (i >= ST) wait(&freed[i % ST], ((i - ST) / ST) & 1);
+      issue(i);
+      if constexpr (!VEC) {
+        put(i);
+        if (i + 1 < stages) fetch(i + 1);
+        mbar_arrive(&arrived[i % ST]);  // (for what it has stored itself)
+      }
+      copy_arrive(&arrived[i % ST]);
+    }
   }
-  if constexpr (!VEC) fetch(0);
-  for (int i = 0; i < stages; ++i) {
-    if constexpr (!VEC) {
-      if (i >= ST) wait(&filled[i % ST], ((i - ST) / ST) & 1);
-      put(i);
-      if (i + 1 < stages) fetch(i + 1);
-    }
-    copy_wait<ST - 2>();
-    fence_async_shared();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t at = ring + (i % ST) * S::STAGE;
-#pragma unroll
-      for (int k = 0; k < GRADIENT_ROWS / 16; ++k)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int q = 0; q < S::PARTS; ++q) {
-            // (128 ranks: two panels of first parts, two of second ones)
-            const int to = R > 64 ? q & 1 : 0, first = R > 64 ? q < 2 : q == 0;
-            tc_mma_f16(tmem + m * S::D + to * 64, smem_desc_rows(at + 2 * m * S::PANEL + k * 2048, S::PANEL),
-                       smem_desc_rows(at + S::X + q * S::PANEL + k * 2048), idesc_f16<T>(S::N, true, true),
-                       i > 0 || k > 0 || !first);
-          }
-      tc_commit(&filled[i % ST]);
-    }
-    if (i + ST - 1 < stages) {
-      if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
-      issue(i + ST - 1);
-    }
-    copy_commit();
-  }
-  copy_wait<0>();
-  wait(&filled[(stages - 1) % ST], ((stages - 1) / ST) & 1);  // (the last commit covers all before)
+  copy_wait_all();
+  wait(&freed[(stages - 1) % ST], ((stages - 1) / ST) & 1);  // (the last commit covers all before)
   tc_fence_after();
 
-  // A lane has a column of x, its ranks side by side in tensor memory.
-  const int quarter = warp & 3, m = warp >> 2, c = n0 + m * 128 + quarter * 32 + lane;
-  const float back = std::is_same<T, __nv_bfloat16>::value ? 1.0f : a.back[side][blockIdx.x];
-  const float lost = gave_up ? NAN : 0.0f;
-  const int64_t n = (int64_t)a.rank * N;
-  const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
-  float* sums = a.sums[side] + (int64_t)blockIdx.x * n + c;
-  T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
-#pragma unroll
-  for (int r0 = 0; r0 < R; r0 += 8) {
-    float v[8], w[8];
-    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + m * S::D + r0;
-    tmem_ld8(at, v);
-    if (R <= 32) tmem_ld8(at + R, w);  // (the parts have columns of their own)
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (r0 + i >= a.rank || c >= N) continue;
-      const float f = (R <= 32 ? v[i] + w[i] : v[i]) * back + lost;
-      if (alone)
-        grad[(int64_t)(r0 + i) * N] = from_f32<T>(f);
-      else
-        sums[(int64_t)(r0 + i) * N] = f;
+  if (warp < ADAPTER_WARPS) {
+    // A lane has a column of x, its ranks side by side in tensor memory.
+    const int quarter = warp & 3, m = warp >> 2, c = n0 + m * 128 + quarter * 32 + lane;
+    const float back = std::is_same<T, __nv_bfloat16>::value ? 1.0f : a.back[side][blockIdx.x];
+    const float lost = gave_up ? NAN : 0.0f;
+    const int64_t n = (int64_t)a.rank * N;
+    const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
+    float* sums = a.sums[side] + (int64_t)blockIdx.x * n + c;
+    T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
+  #pragma unroll
+    for (int r0 = 0; r0 < R; r0 += 8) {
+      float v[8], w[8];
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + m * S::D + r0;
+      tmem_ld8(at, v);
+      if (R <= 32) tmem_ld8(at + R, w);  // (the parts have columns of their own)
+      tmem_ld_wait();
+  #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i >= a.rank || c >= N) continue;
+        const float f = (R <= 32 ? v[i] + w[i] : v[i]) * back + lost;
+        if (alone)
+          grad[(int64_t)(r0 + i) * N] = from_f32<T>(f);
+        else
+          sums[(int64_t)(r0 + i) * N] = f;
+      }
     }
   }
   tc_fence_before();
@@ -292,7 +297,7 @@ cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
   e = launch_k(adapter_split_kernel<T, R>, dim3(pieces, 2, (unsigned)(a.unit / SPLIT_ROWS)), dim3(256), 0, s, true,
                a);
   if (e != cudaSuccess) return e;
-  e = launch_k(kernel, dim3(pieces, (unsigned)(a.blocks[0] + a.blocks[1])), dim3(ADAPTER_THREADS),
+  e = launch_k(kernel, dim3(pieces, (unsigned)(a.blocks[0] + a.blocks[1])), dim3(TENSOR_THREADS),
                GradientShared<R>::BYTES, s, true, a);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);

@@ -9,11 +9,11 @@ namespace moe {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// An arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Sixteen bytes of a row that starts anywhere: the aligned words around them, to be
 // put in order once they have arrived.  (Words that hold an element of the row are
 // read, others not.)
@@ -42,10 +42,12 @@ __device__ __forceinline__ void put16(uint32_t dst, const uint4& v) {
                : "memory");
 }
 
-// This thread's writes to shared memory so far, before later accesses of the
-// tensor cores: its own CTA's memory, or any in the cluster.
+// Writes to shared memory that this thread made, or waited for, before later
+// accesses of the tensor cores: to its own CTA's memory, or any in the cluster.
+// (It also waits for the thread's own copies in flight: the thread that issues the
+// products issues no copies, or every stage would cost their whole latency.)
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_cluster() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // D[tmem] (+)= A B, both operands 16-bit in shared memory.
 __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -58,6 +60,10 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, u
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// Threads of the tcgen05 kernels: eight warps that copy and one whose first lane
+// issues the products.
+constexpr int TENSOR_THREADS = ADAPTER_THREADS + 32;
+
 // M 128, FP32 sums; a_rows, b_rows: the operand's contraction runs across its
 // rows.
 template <typename T>

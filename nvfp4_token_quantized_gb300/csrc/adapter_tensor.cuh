@@ -15,11 +15,10 @@
 // as aligned words one stage ahead, put in order in registers and stored to the
 // same places; their output leaves element by element.
 //
-// Stages follow one another without roles: every thread copies, waits for its own
-// copies, meets the others, and one thread issues the stage's products; the slot is
-// filled again when their commit has arrived.  Two CTAs share an SM, so that one's
-// barriers and the join between the products hide behind the other's copies.  The
-// CTAs of a cluster split a tile as in adapter_apply.cuh.
+// Eight warps copy (and later add and store); a ninth issues a stage's products when
+// all copies of the stage have arrived on its barrier, and their commit frees the
+// slot.  Two CTAs share an SM, so that the join between one's products hides behind
+// the other's copies.  The CTAs of a cluster split a tile as in adapter_apply.cuh.
 //
 // Waits are bounded: one that runs out raises a flag, further waits return at once,
 // and the tile's rows become NaN.
@@ -46,7 +45,7 @@ struct TensorShared {
 };
 
 template <typename T, int R, bool VEC>
-__global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tensor_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tensor_kernel(const AdapterArgs a) {
   using S = TensorShared<R>;
   constexpr int ST = S::STAGES, RP = S::RP, W = (R + 31) / 32;  // (a thread's chunks of a factor)
   constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
@@ -58,17 +57,26 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   __shared__ int row_of[ADAPTER_TILE];
   __shared__ float back[ADAPTER_TILE];
   __shared__ Piece found;
-  __shared__ uint64_t filled[ST], done[2];       // commits: of the first product's slots, of D2
+  // Of the first product's slots: copies in, products done; of the second's: copies
+  // in; of D2's two halves: products done, sums read.
+  __shared__ uint64_t in1[ST], free1[ST], in2[ST], done[2], drained[2];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool issuer = warp == ADAPTER_WARPS;
   const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
 
   // (set up while the plan is made)
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(&filled[i], 1);
-    mbar_init(&done[0], 1);
-    mbar_init(&done[1], 1);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&in1[i], ADAPTER_THREADS);
+      mbar_init(&in2[i], ADAPTER_THREADS);
+      mbar_init(&free1[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&done[i], 1);
+      mbar_init(&drained[i], ADAPTER_WARPS);
+    }
     gave_up = 0;
     fence_mbarrier_init();
   }
@@ -99,11 +107,14 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   __syncthreads();
   if (group == a.L) {
     if (warp == 0) tmem_dealloc(tmem, 128);
-    rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
+    if (!issuer) rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
     return;
   }
-  const auto wait = [&](uint64_t* bar, int parity) {
+  const auto wait_alone = [&](uint64_t* bar, int parity) {  // (one lane)
     if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
+  };
+  const auto wait = [&](uint64_t* bar, int parity) {  // (whole warps)
+    wait_alone(bar, parity);
     __syncwarp();
   };
 
@@ -112,7 +123,20 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
   const int c0 = min(crank * each, chunks), nk = min(each, chunks - c0);
   const int blocks = (N + 63) / 64, blocks_each = (blocks + C - 1) / C;  // (of the second product)
   const int b0 = min(crank * blocks_each, blocks), nb = min(blocks_each, blocks - b0);
-  {
+  if (issuer) {
+    if (lane == 0)
+      for (int i = 0; i < nk; ++i) {
+        wait_alone(&in1[i % ST], (i / ST) & 1);
+        fence_async_shared();
+        const uint32_t at = ring_at + (i % ST) * S::STAGE;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_f16(tmem, smem_desc_sw128(at + k * 32), smem_desc_sw128(at + S::ROWS + k * 32),
+                     idesc_f16<T>(R, false, false), i > 0 || k > 0);
+        tc_commit(&free1[i % ST]);
+      }
+    __syncwarp();
+  } else {
     const int sub = tid & 7, r0 = tid >> 3;  // 16-byte chunk of a row, first of the rows 32 apart
     const T* px[4];
     bool on[4];
@@ -156,54 +180,31 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         if (r < R) put16(at + S::ROWS + swizzled(r, sub), lw[q].chunk(Loose::odd(down + (int64_t)r * K + col), K - col));
       }
     };
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < ST - 1; ++i) {
-        if (i < nk) issue(i);
-        copy_commit();
-      }
-    } else {
-      if (nk > 0) fetch(0);
-    }
+    if (!VEC && nk > 0) fetch(0);
     for (int i = 0; i < nk; ++i) {
+      if (i >= ST) wait(&free1[i % ST], ((i - ST) / ST) & 1);
       if constexpr (VEC) {
-        copy_wait<ST - 2>();
+        issue(i);
+        copy_arrive(&in1[i % ST]);
       } else {
-        if (i >= ST) wait(&filled[i % ST], ((i - ST) / ST) & 1);
         put(i);
         if (i + 1 < nk) fetch(i + 1);
-      }
-      fence_async_shared();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t at = ring_at + (i % ST) * S::STAGE;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_f16(tmem, smem_desc_sw128(at + k * 32), smem_desc_sw128(at + S::ROWS + k * 32), idesc_f16<T>(R, false, false),
-                     i > 0 || k > 0);
-        tc_commit(&filled[i % ST]);
-      }
-      if constexpr (VEC) {
-        if (i + ST - 1 < nk) {
-          if (i > 0) wait(&filled[(i - 1) % ST], ((i - 1) / ST) & 1);
-          issue(i + ST - 1);
-        }
-        copy_commit();
+        mbar_arrive(&in1[i % ST]);
       }
     }
-    copy_wait<0>();
-    if (nk > 0) wait(&filled[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
-    __syncthreads();
-    tc_fence_after();
+    if (nk > 0) wait(&free1[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
   }
+  __syncthreads();
+  tc_fence_after();
 
-  const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+  const int quarter = warp & 3, half = (warp >> 2) & 1, mine = quarter * 32 + lane;  // (the issuer takes no part)
 
   // ---- the second product's copies ----
   const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
   // A warp copies the rows and the half of their columns that it adds to, and
   // stores: eight rows by four chunks at a time.
-  const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2), up_row = tid >> 3, up_chunk = tid & 7;
+  const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2);
+  const int up_row = (tid & (ADAPTER_THREADS - 1)) >> 3, up_chunk = tid & 7;
   int64_t at_row[4];
   bool on[4];
 #pragma unroll
@@ -254,18 +255,21 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         put16(at + S::ROWS + swizzled(up_row + 32 * q, up_chunk),
               lu[q].chunk(Loose::odd(up + (int64_t)(up_row + 32 * q) * N + cu), N - cu));
   };
-  if constexpr (VEC) {
+  if (!issuer) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < ST - FREE; ++i) {
-      if (i < nb) issue(i);
-      copy_commit();
+      for (int i = 0; i < ST - FREE; ++i)
+        if (i < nb) {
+          issue(i);
+          copy_arrive(&in2[(i + FREE) % ST]);
+        }
+    } else {
+      if (nb > 0) fetch(0);
     }
-  } else {
-    if (nb > 0) fetch(0);
   }
 
   // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
-  {
+  if (!issuer) {
     float* to = part + mine * RP + half * (R / 2);
 #pragma unroll
     for (int c = 0; c < R / 2; c += 8) {
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
     cluster.sync();
   else
     __syncthreads();
-  {
+  if (!issuer) {
     constexpr int G = R / 8;  // lanes of a row, eight ranks each
     const float scale = a.scales ? a.scales[group] : 1.0f;
     const int share = ADAPTER_TILE / C, lane8 = tid % G;
@@ -295,12 +299,21 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      for (int q = 0; q < C; ++q) {
-        const float4* f =
-            reinterpret_cast<const float4*>((C > 1 ? cluster.map_shared_rank(part, q) : part) + r * RP + lane8 * 8);
-        const float4 lo = f[0], hi = f[1];
-        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
+      for (int q0 = 0; q0 < C; q0 += 4) {  // (four CTAs' sums on their way together)
+        float4 f[4][2];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int from = q0 + q < C ? q0 + q : q0;
+          const float4* p =
+              reinterpret_cast<const float4*>((C > 1 ? cluster.map_shared_rank(part, from) : part) + r * RP + lane8 * 8);
+          f[q][0] = p[0], f[q][1] = p[1];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q0 + q < C) {
+            v[0] += f[q][0].x, v[1] += f[q][0].y, v[2] += f[q][0].z, v[3] += f[q][0].w;
+            v[4] += f[q][1].x, v[5] += f[q][1].y, v[6] += f[q][1].z, v[7] += f[q][1].w;
+          }
       }
       float m = 0.0f;
 #pragma unroll
@@ -335,47 +348,48 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         if (SCALED && lane8 == 0) *(C > 1 ? cluster.map_shared_rank(&back[r], q) : &back[r]) = b;
       }
     }
-    fence_async_proxy();
   }
   if (C > 1)
     cluster.sync();  // (the last access to another CTA's shared memory lies before)
   else
     __syncthreads();
-  fence_async_proxy();
 
   // ---- out = base + hidden up, 64 columns a stage ----
-  {
-    if constexpr (VEC) {
+  if (issuer) {
+    if (lane == 0) {
+      tc_fence_after();
+      fence_async_cluster();  // (the panels that all CTAs have written)
+      for (int i = 0; i < nb; ++i) {
+        wait_alone(&in2[(i + FREE) % ST], (i / ST) & 1);
+        if (i >= 2) wait_alone(&drained[i & 1], ((i >> 1) - 1) & 1);
+        tc_fence_after();
+        fence_async_shared();
+        const uint32_t b = ring_at + ((i + FREE) % ST) * S::STAGE + S::ROWS;
 #pragma unroll
-      for (int i = ST - FREE; i < ST; ++i) {
-        if (i < nb) issue(i);
-        copy_commit();
+        for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
+          tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
+                     smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, false, true), k > 0);
+        tc_commit(&done[i & 1]);
       }
     }
-    const float bk = back[mine];
-    for (int i = 0; i <= nb; ++i) {
-      if (i < nb) {
-        if constexpr (VEC) {
-          copy_wait<ST - 2>();
-        } else {
-          put(i);  // (the slot's last stage has been read: its products and rows, above)
-          if (i + 1 < nb) fetch(i + 1);
-        }
-        fence_async_shared();
-        __syncthreads();
-        if (tid == 0) {
-          tc_fence_after();
-          const uint32_t b = ring_at + ((i + FREE) % ST) * S::STAGE + S::ROWS;
-#pragma unroll
-          for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
-            tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
-                       smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, false, true), k > 0);
-          tc_commit(&done[i & 1]);
-        }
+    __syncwarp();
+  } else {
+    // stage i into its slot, its last stage read by this warp and the products
+    const auto fill = [&](int i) {
+      if constexpr (VEC) {
+        issue(i);
+        copy_arrive(&in2[(i + FREE) % ST]);
+      } else {
+        put(i);
+        if (i + 1 < nb) fetch(i + 1);
+        mbar_arrive(&in2[(i + FREE) % ST]);
       }
-      if (i == 0) continue;
-      // the stage before, while the tensor cores work on this one
-      const int j = i - 1, col = (b0 + j) * 64;
+    };
+    for (int i = VEC ? ST - FREE : 0; i < min(ST, nb); ++i) fill(i);
+    const float bk = back[mine];
+    for (int j = 0; j < nb; ++j) {
+      const int col = (b0 + j) * 64;
+      wait(&in2[(j + FREE) % ST], (j / ST) & 1);  // (the rows of base; products follow them)
       wait(&done[j & 1], (j >> 1) & 1);
       tc_fence_after();
       float v[32];
@@ -387,6 +401,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         y[c] = base ? *reinterpret_cast<const uint4*>(tile + swizzled(mine, half * 4 + c)) : make_uint4(0, 0, 0, 0);
       tmem_ld_wait();
       tc_fence_before();
+      if (lane == 0) mbar_arrive(&drained[j & 1]);
       const float lost = gave_up ? NAN : 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -410,8 +425,6 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
           for (int q = 0; q < 4; ++q)
             if (on[q]) *reinterpret_cast<uint4*>(out + at_row[q] * a.out_stride + col + sub * 8) = o[q];
         }
-        if (j + ST < nb) issue(j + ST);
-        copy_commit();
       } else {
         // a row's 32 columns, an element a lane
         const int c = col + half * 32 + lane;
@@ -423,8 +436,9 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, R <= 64 ? 2 : 1) adapter_tens
         }
         __syncwarp();
       }
+      if (j + ST < nb) fill(j + ST);
     }
-    copy_wait<0>();
+    copy_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -440,7 +454,7 @@ cudaError_t launch_tensor_one(const AdapterArgs& a, cudaStream_t s) {
   const auto kernel = adapter_tensor_kernel<T, R, VEC>;
   const cudaError_t e = raise_shared(kernel, TensorShared<R>::BYTES, done);
   if (e != cudaSuccess) return e;
-  return launch_clustered(kernel, a, TensorShared<R>::BYTES, true, s);
+  return launch_clustered(kernel, a, TENSOR_THREADS, TensorShared<R>::BYTES, true, s);
 }
 
 template <typename T>
