@@ -119,9 +119,15 @@ __device__ __forceinline__ void rows_without_adapter(const AdapterArgs& a, const
     if (a.hidden)
       for (int i = lane; i < a.rank; i += 32) a.hidden[row * a.rank + i] = 0.0f;
     if (out == base) continue;
-    for (int c = lane * 8; c < a.n_out; c += 256)
-      store8<T, VEC>(out + row * a.out_stride, c, a.n_out,
-                     base ? load8<T, VEC>(base + row * a.base_stride, c, a.n_out, true) : make_uint4(0, 0, 0, 0));
+    constexpr int U = 8;  // accesses in flight: one at a time the row takes a latency each
+    for (int c = lane * 8; c < a.n_out; c += 256 * U) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = load8<T, VEC>(base + row * a.base_stride, c + 256 * u, a.n_out, base != nullptr);
+#pragma unroll
+      for (int u = 0; u < U; ++u) store8<T, VEC>(out + row * a.out_stride, c + 256 * u, a.n_out, v[u]);
+    }
   }
 }
 

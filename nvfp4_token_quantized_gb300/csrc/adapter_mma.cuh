@@ -43,9 +43,9 @@ __device__ __forceinline__ void put16(uint32_t dst, const uint4& v) {
 }
 
 // Writes to shared memory that this thread made, or waited for, before later
-// accesses of the tensor cores: to its own CTA's memory, or any in the cluster.
-// (It also waits for the thread's own copies in flight: the thread that issues the
-// products issues no copies, or every stage would cost their whole latency.)
+// accesses of the tensor cores: to its own CTA's memory, or any in the cluster.  (A
+// fence also waits for the thread's own copies in flight: the thread that issues
+// the products issues no copies, or every stage would cost their whole latency.)
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_cluster() { asm volatile("fence.proxy.async;" ::: "memory"); }
 

@@ -212,13 +212,9 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     at_row[q] = row_of[first + 8 * q];
     on[q] = first + 8 * q < count;
   }
-  // Stage i lies in slot (i + FREE) % ST: the first FREE slots hold the sums until
-  // they are joined, the others can be filled at once.
-  constexpr int FREE = (ADAPTER_TILE * RP * 4 + S::STAGE - 1) / S::STAGE;
-  static_assert(FREE < ST, "a slot beside the sums");
   const auto issue = [&](int i) {
     const int col = (b0 + i) * 64;
-    const uint32_t at = ring_at + ((i + FREE) % ST) * S::STAGE;
+    const uint32_t at = ring_at + (i % ST) * S::STAGE;
     const bool in = col + sub * 8 < N;
     if (base) {
 #pragma unroll
@@ -242,7 +238,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     for (int q = 0; q < W; ++q) lu[q].load(up + (int64_t)(up_row + 32 * q) * N + cu, N - cu, up_row + 32 * q < a.rank);
   };
   const auto put = [&](int i) {
-    const uint32_t at = ring_at + ((i + FREE) % ST) * S::STAGE;
+    const uint32_t at = ring_at + (i % ST) * S::STAGE;
     const int cb = (b0 + i) * 64 + sub * 8, cu = (b0 + i) * 64 + up_chunk * 8;
     if (base) {
 #pragma unroll
@@ -255,18 +251,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
         put16(at + S::ROWS + swizzled(up_row + 32 * q, up_chunk),
               lu[q].chunk(Loose::odd(up + (int64_t)(up_row + 32 * q) * N + cu), N - cu));
   };
-  if (!issuer) {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < ST - FREE; ++i)
-        if (i < nb) {
-          issue(i);
-          copy_arrive(&in2[(i + FREE) % ST]);
-        }
-    } else {
-      if (nb > 0) fetch(0);
-    }
-  }
+  if (!VEC && !issuer && nb > 0) fetch(0);
 
   // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
   if (!issuer) {
@@ -360,11 +345,11 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       tc_fence_after();
       fence_async_cluster();  // (the panels that all CTAs have written)
       for (int i = 0; i < nb; ++i) {
-        wait_alone(&in2[(i + FREE) % ST], (i / ST) & 1);
+        wait_alone(&in2[i % ST], (i / ST) & 1);
         if (i >= 2) wait_alone(&drained[i & 1], ((i >> 1) - 1) & 1);
         tc_fence_after();
         fence_async_shared();
-        const uint32_t b = ring_at + ((i + FREE) % ST) * S::STAGE + S::ROWS;
+        const uint32_t b = ring_at + (i % ST) * S::STAGE + S::ROWS;
 #pragma unroll
         for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
           tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
@@ -378,23 +363,23 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     const auto fill = [&](int i) {
       if constexpr (VEC) {
         issue(i);
-        copy_arrive(&in2[(i + FREE) % ST]);
+        copy_arrive(&in2[i % ST]);
       } else {
         put(i);
         if (i + 1 < nb) fetch(i + 1);
-        mbar_arrive(&in2[(i + FREE) % ST]);
+        mbar_arrive(&in2[i % ST]);
       }
     };
-    for (int i = VEC ? ST - FREE : 0; i < min(ST, nb); ++i) fill(i);
+    for (int i = 0; i < min(ST, nb); ++i) fill(i);
     const float bk = back[mine];
     for (int j = 0; j < nb; ++j) {
       const int col = (b0 + j) * 64;
-      wait(&in2[(j + FREE) % ST], (j / ST) & 1);  // (the rows of base; products follow them)
+      wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
       wait(&done[j & 1], (j >> 1) & 1);
       tc_fence_after();
       float v[32];
       tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (j & 1) * 64 + half * 32, v);
-      unsigned char* tile = ring + ((j + FREE) % ST) * S::STAGE;
+      unsigned char* tile = ring + (j % ST) * S::STAGE;
       uint4 y[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
