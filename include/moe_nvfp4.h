@@ -669,7 +669,8 @@ typedef struct {
 } moe_adapter_io;
 
 /* Device bytes of a forward's (backward 0) or a gradient's workspace; 0 for a
- * refused cfg or number of rows. */
+ * forward of up to 128 rows (workspace may then be NULL) and for a refused cfg
+ * or number of rows. */
 MOE_API size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int64_t rows, int backward);
 
 /* out may be base (same stride); other overlaps of an output with another

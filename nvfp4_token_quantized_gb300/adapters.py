@@ -63,10 +63,12 @@ class LowRankAdapters:
         return int(self._lib.moe_adapter_workspace_bytes(self._config(num_adapters, torch.bfloat16), rows,
                                                          int(backward)))
 
-    def _workspace(self, cfg, T, backward, workspace, dev) -> Tuple[int, torch.Tensor]:
+    def _workspace(self, cfg, T, backward, workspace, dev):
         need = int(self._lib.moe_adapter_workspace_bytes(cfg, T, backward))
+        if need == 0:
+            return None, None
         if workspace is None:
-            workspace = _new_vector(max(need, 16), torch.uint8)
+            workspace = _new_vector(need, torch.uint8)
         elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
             raise ValueError(f"workspace must be a contiguous tensor of {need} bytes or more on cuda:{dev}")
         return workspace.data_ptr(), workspace

@@ -134,6 +134,7 @@ cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t 
 }  // namespace
 
 size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward) {
+  if (!backward && rows <= ADAPTER_TILE) return 0;
   return (size_t)layout(c, rows, backward).end * 4;
 }
 

@@ -78,10 +78,11 @@ moe_status moe_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_
                          all_of(io->up, L * r * N, 2),
                          all_of(io->ids, rows, 4),
                          all_of(io->scales, L, 4, true)};
+  const int64_t need = (int64_t)adapter_workspace(*cfg, rows, false);
   const Operand out[3] = {{io->out, rows, N, io->out_stride, 2, false},
                           all_of(io->hidden, rows * r, 4, true),
-                          all_of(io->workspace, (int64_t)adapter_workspace(*cfg, rows, false), 1)};
-  if (!aligned(io->workspace, 16)) return MOE_ERR_INVALID_ARG;
+                          all_of(need ? io->workspace : nullptr, need, 1, need == 0)};
+  if (need && !aligned(io->workspace, 16)) return MOE_ERR_INVALID_ARG;
   st = check_all(in, 6, out, 3, 0);
   if (st != MOE_OK) return st;
   const bool vec = K % 8 == 0 && N % 8 == 0 && sixteen(in[0]) && sixteen(in[1]) && sixteen(out[0]) &&

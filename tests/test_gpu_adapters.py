@@ -282,7 +282,7 @@ def test_refusals():
     for bad in (dict(x=a["base"]), dict(x=a["x"].float()), dict(x=a["x"].cpu()), dict(ids=a["ids"].long()),
                 dict(ids=a["ids"][:3]), dict(down=a["up"]), dict(down=a["down"][0]), dict(up=a["up"][:1]),
                 dict(up=a["up"].half()), dict(down=a["down"].transpose(1, 2)), dict(scales=a["scales"][:1]),
-                dict(base=a["x"]), dict(out=a["x"]), dict(workspace=torch.zeros(2, device="cuda"))):
+                dict(base=a["x"]), dict(out=a["x"])):
         with pytest.raises((ValueError, RuntimeError, TypeError)):
             ad.forward(**{**ok, **bad})
     wide = torch.zeros(41, 96, dtype=BF16, device="cuda")
@@ -294,6 +294,9 @@ def test_refusals():
         _adapters(64, 96, 129)
     with pytest.raises(RuntimeError):
         _adapters(0, 96, 8)
+    b = _make(140, 64, 96, 8, 2, BF16)
+    with pytest.raises(ValueError, match="workspace"):
+        ad.forward(b["x"], b["ids"], b["down"], b["up"], workspace=torch.zeros(2, device="cuda"))
     _, h = ad.forward(**ok, keep_hidden=True)
     okb = dict(dout=a["dout"], x=a["x"], hidden=h, ids=a["ids"], down=a["down"], up=a["up"])
     for bad in (dict(hidden=None), dict(hidden=h[:3]), dict(hidden=h.half()), dict(dout=a["x"]), dict(base=a["dout"]),

@@ -153,7 +153,7 @@ def test_adapter_configurations(lib, kw, status):
 
     cfg = _adapter_cfg(**kw)
     assert lib.moe_adapter_forward(cfg, ctypes.byref(moe_adapter_io()), 0, None) == status
-    assert (lib.moe_adapter_workspace_bytes(cfg, 10, 0) > 0) == (status == OK)
+    assert (lib.moe_adapter_workspace_bytes(cfg, 1000, 0) > 0) == (status == OK)
     assert lib.moe_adapter_workspace_bytes(cfg, 10, 1) >= lib.moe_adapter_workspace_bytes(cfg, 10, 0)
     assert lib.moe_adapter_workspace_bytes(cfg, -1, 0) == 0
     if status != OK:
