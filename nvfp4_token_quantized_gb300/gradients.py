@@ -55,7 +55,7 @@ class GradientClip:
     def clip(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None,
              stream=None) -> Tuple[torch.Tensor, List[torch.Tensor]]:
         """(norm, the clipped gradients): in place, or into the tensors of out
-        (of the same types and shapes, their elements in the same order)."""
+        (of the same types and sizes, their elements in the same order)."""
         if self.max_norm is None:
             raise ValueError("this GradientClip has no max_norm")
         if stream is not None:
@@ -81,49 +81,52 @@ class GradientClip:
 
     @staticmethod
     def _table(grads, out, dev):
-        """moe_gradient of each tensor, as one array of integers (columns by
-        torch's own calls, so that long lists cost little)."""
-        n = len(grads)
-        table = array.array("q", bytes(32 * n))
+        """moe_gradient of each tensor, as one array of integers (by torch's
+        own calls and in as few as can be: long lists cost their number)."""
         try:
-            types = [_DTYPES.get(t.dtype) for t in grads]
-            if None in types or (n and set(map(_get_device, grads)) != {dev}) or not all(map(_is_contiguous, grads)):
-                _refuse(grads, dev)
-            where = array.array("q", list(map(_data_ptr, grads)))
-            table[0::4] = table[1::4] = where
-            table[2::4] = array.array("q", list(map(_numel, grads)))
-            table[3::4] = array.array("q", types)
-            if out is not grads:
-                if (n and set(map(_get_device, out)) != {dev}) or types != [_DTYPES.get(o.dtype) for o in out] or (
-                        list(map(_size, grads)) != list(map(_size, out))) or (
-                        list(map(_stride, grads)) != list(map(_stride, out))):
-                    for i, (t, o) in enumerate(zip(grads, out)):
-                        _refuse_out(i, t, o, dev)
-                table[1::4] = array.array("q", list(map(_data_ptr, out)))
+            return _in_place(grads, dev) if out is grads else _apart(grads, out, dev)
         except (AttributeError, TypeError):
             raise TypeError("gradients must be torch tensors") from None
-        return table
 
 
 _base = torch._C.TensorBase
 _data_ptr, _numel, _get_device, _is_contiguous = _base.data_ptr, _base.numel, _base.get_device, _base.is_contiguous
-_size, _stride = _base.size, _base.stride
 
 
-def _refuse(grads, dev):
-    """Raises for the first gradient that cannot be taken (a dense one in
-    another order of its dimensions can)."""
-    for i, t in enumerate(grads):
-        if t.dtype not in _DTYPES:
-            raise ValueError(f"gradient {i} must be bfloat16, float16 or float32, not {t.dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"gradient {i} must be on cuda:{dev}, the current device")
-        if not _dense(t):
-            raise ValueError(f"gradient {i}: the elements must lie next to each other")
+def _in_place(grads, dev):
+    n = len(grads)
+    types = [_DTYPES.get(t.dtype) for t in grads]
+    if None in types or (n and set(map(_get_device, grads)) != {dev}) or not all(map(_is_contiguous, grads)):
+        for i, t in enumerate(grads):
+            _check(i, t, dev)
+    table = array.array("q", bytes(32 * n))
+    table[0::4] = table[1::4] = array.array("q", list(map(_data_ptr, grads)))
+    table[2::4] = array.array("q", list(map(_numel, grads)))
+    table[3::4] = array.array("q", types)
+    return table
 
 
-def _refuse_out(i, t, o, dev):
-    if (o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != dev
-            or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous()))):
-        raise ValueError(f"out {i} must be laid out as gradient {i}: {tuple(t.shape)} of {t.dtype}, strides "
-                         f"{t.stride()}, on cuda:{dev}")
+def _apart(grads, out, dev):
+    rows = []
+    for i, (t, o) in enumerate(zip(grads, out)):
+        dt, n = _DTYPES.get(t.dtype), _numel(t)
+        if not (dt is not None and o.dtype is t.dtype and _numel(o) == n and _get_device(t) == dev
+                and _get_device(o) == dev and _is_contiguous(t) and _is_contiguous(o)):
+            dt = _check(i, t, dev)
+            if o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != dev or o.stride() != t.stride():
+                raise ValueError(f"out {i} must be laid out as gradient {i}: {tuple(t.shape)} of {t.dtype}, strides "
+                                 f"{t.stride()}, on cuda:{dev}")
+        rows += (_data_ptr(t), _data_ptr(o), n, dt)
+    return array.array("q", rows)
+
+
+def _check(i, t, dev) -> int:
+    """The type's code of a gradient that can be taken: contiguous, or dense in
+    another order of its dimensions."""
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"gradient {i} must be bfloat16, float16 or float32, not {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"gradient {i} must be on cuda:{dev}, the current device")
+    if not _dense(t):
+        raise ValueError(f"gradient {i}: the elements must lie next to each other")
+    return _DTYPES[t.dtype]
