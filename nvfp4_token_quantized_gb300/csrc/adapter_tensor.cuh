@@ -48,6 +48,7 @@ template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tensor_kernel(const AdapterArgs a) {
   using S = TensorShared<R>;
   constexpr int ST = S::STAGES, RP = S::RP, W = (R + 31) / 32;  // (a thread's chunks of a factor)
+  constexpr int SUMS = 4;  // stages whose sums tensor memory holds
   constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -58,8 +59,8 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   __shared__ float back[ADAPTER_TILE];
   __shared__ Piece found;
   // Of the first product's slots: copies in, products done; of the second's: copies
-  // in; of D2's two halves: products done, sums read.
-  __shared__ uint64_t in1[ST], free1[ST], in2[ST], done[2], drained[2];
+  // in; of D2's SUMS places: products done, sums read.
+  __shared__ uint64_t in1[ST], free1[ST], in2[ST], done[SUMS], drained[SUMS];
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -70,18 +71,18 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&in1[i], ADAPTER_THREADS);
-      mbar_init(&in2[i], ADAPTER_THREADS);
+      mbar_init(&in2[i], ADAPTER_THREADS / 2);
       mbar_init(&free1[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SUMS; ++i) {
       mbar_init(&done[i], 1);
-      mbar_init(&drained[i], ADAPTER_WARPS);
+      mbar_init(&drained[i], ADAPTER_WARPS / 2);
     }
     gave_up = 0;
     fence_mbarrier_init();
   }
   if (warp == 0) {
-    tmem_alloc(&tmem_at, 128);
+    tmem_alloc(&tmem_at, SUMS * 64);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   pdl_trigger();
   const int count = p.count, group = p.group;
   if (group < 0) {  // (the whole cluster)
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, SUMS * 64);
     return;
   }
   if (tid < ADAPTER_TILE) {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   const int K = a.in, N = a.n_out;
   __syncthreads();
   if (group == a.L) {
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, SUMS * 64);
     if (!issuer) rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
     return;
   }
@@ -199,60 +200,6 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
 
   const int quarter = warp & 3, half = (warp >> 2) & 1, mine = quarter * 32 + lane;  // (the issuer takes no part)
 
-  // ---- the second product's copies ----
-  const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
-  // A warp copies the rows and the half of their columns that it adds to, and
-  // stores: eight rows by four chunks at a time.
-  const int sub = half * 4 + (lane & 3), first = quarter * 32 + (lane >> 2);
-  const int up_row = (tid & (ADAPTER_THREADS - 1)) >> 3, up_chunk = tid & 7;
-  int64_t at_row[4];
-  bool on[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    at_row[q] = row_of[first + 8 * q];
-    on[q] = first + 8 * q < count;
-  }
-  const auto issue = [&](int i) {
-    const int col = (b0 + i) * 64;
-    const uint32_t at = ring_at + (i % ST) * S::STAGE;
-    const bool in = col + sub * 8 < N;
-    if (base) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        copy16(at + swizzled(first + 8 * q, sub), in ? base + at_row[q] * a.base_stride + col + sub * 8 : base,
-               in && on[q]);
-    }
-    const bool up_in = col + up_chunk * 8 < N;
-#pragma unroll
-    for (int r = up_row; r < R; r += 32) {
-      const bool have = up_in && r < a.rank;
-      copy16(at + S::ROWS + swizzled(r, up_chunk), have ? up + (int64_t)r * N + col + up_chunk * 8 : up, have);
-    }
-  };
-  Loose lb[VEC ? 1 : 4], lu[VEC ? 1 : W];
-  const auto fetch = [&](int i) {
-    const int cb = (b0 + i) * 64 + sub * 8, cu = (b0 + i) * 64 + up_chunk * 8;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) lb[q].load(base + at_row[q] * a.base_stride + cb, N - cb, base && on[q]);
-#pragma unroll
-    for (int q = 0; q < W; ++q) lu[q].load(up + (int64_t)(up_row + 32 * q) * N + cu, N - cu, up_row + 32 * q < a.rank);
-  };
-  const auto put = [&](int i) {
-    const uint32_t at = ring_at + (i % ST) * S::STAGE;
-    const int cb = (b0 + i) * 64 + sub * 8, cu = (b0 + i) * 64 + up_chunk * 8;
-    if (base) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        put16(at + swizzled(first + 8 * q, sub), lb[q].chunk(Loose::odd(base + at_row[q] * a.base_stride + cb), N - cb));
-    }
-#pragma unroll
-    for (int q = 0; q < W; ++q)
-      if (up_row + 32 * q < R)
-        put16(at + S::ROWS + swizzled(up_row + 32 * q, up_chunk),
-              lu[q].chunk(Loose::odd(up + (int64_t)(up_row + 32 * q) * N + cu), N - cu));
-  };
-  if (!VEC && !issuer && nb > 0) fetch(0);
-
   // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
   if (!issuer) {
     float* to = part + mine * RP + half * (R / 2);
@@ -340,87 +287,132 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     __syncthreads();
 
   // ---- out = base + hidden up, 64 columns a stage ----
+  // Four warps have the even stages, four the odd ones: a stage's chain (products,
+  // sums, base, stores) takes about a microsecond, which one after the other would
+  // bound the kernel.  A warp copies and stores the 32 rows that it adds to.
+  const T* up = static_cast<const T*>(a.second) + (int64_t)group * a.rank * N;
   if (issuer) {
     if (lane == 0) {
       tc_fence_after();
       fence_async_cluster();  // (the panels that all CTAs have written)
       for (int i = 0; i < nb; ++i) {
         wait_alone(&in2[i % ST], (i / ST) & 1);
-        if (i >= 2) wait_alone(&drained[i & 1], ((i >> 1) - 1) & 1);
+        if (i >= SUMS) wait_alone(&drained[i % SUMS], (i / SUMS - 1) & 1);
         tc_fence_after();
         fence_async_shared();
         const uint32_t b = ring_at + (i % ST) * S::STAGE + S::ROWS;
 #pragma unroll
         for (int k = 0; k < 2 * R / 16; ++k)  // 16 columns of the panels, 16 rows of up
-          tc_mma_f16(tmem + (i & 1) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
+          tc_mma_f16(tmem + (i % SUMS) * 64, smem_desc_sw128(panels_at + (k / 4) * S::ROWS + (k % 4) * 32),
                      smem_desc_rows(b + (k % (R / 16)) * 2048), idesc_f16<T>(64, false, true), k > 0);
-        tc_commit(&done[i & 1]);
+        tc_commit(&done[i % SUMS]);
       }
     }
     __syncwarp();
   } else {
-    // stage i into its slot, its last stage read by this warp and the products
+    const int sub = lane & 7, first = quarter * 32 + (lane >> 3);        // of base and out: rows four apart
+    const int up_row = (tid & 127) >> 3, up_chunk = tid & 7;             // rows 16 apart
     const auto fill = [&](int i) {
+      const int col = (b0 + i) * 64;
+      const uint32_t at = ring_at + (i % ST) * S::STAGE;
       if constexpr (VEC) {
-        issue(i);
+        if (base) {
+          const bool in = col + sub * 8 < N;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = first + 4 * q;
+            copy16(at + swizzled(r, sub), in ? base + row_of[r] * a.base_stride + col + sub * 8 : base, in && r < count);
+          }
+        }
+        const bool in = col + up_chunk * 8 < N;
+#pragma unroll
+        for (int r = up_row; r < R; r += 16) {
+          const bool have = in && r < a.rank;
+          copy16(at + S::ROWS + swizzled(r, up_chunk), have ? up + (int64_t)r * N + col + up_chunk * 8 : up, have);
+        }
         copy_arrive(&in2[i % ST]);
       } else {
-        put(i);
-        if (i + 1 < nb) fetch(i + 1);
+        const int cb = col + sub * 8, cu = col + up_chunk * 8;
+        Loose l[8];
+        if (base) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            l[q].load(base + row_of[first + 4 * q] * a.base_stride + cb, N - cb, first + 4 * q < count);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            put16(at + swizzled(first + 4 * q, sub),
+                  l[q].chunk(Loose::odd(base + row_of[first + 4 * q] * a.base_stride + cb), N - cb));
+        }
+        constexpr int U = R / 16;
+#pragma unroll
+        for (int q = 0; q < U; ++q) l[q].load(up + (int64_t)(up_row + 16 * q) * N + cu, N - cu, up_row + 16 * q < a.rank);
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          put16(at + S::ROWS + swizzled(up_row + 16 * q, up_chunk),
+                l[q].chunk(Loose::odd(up + (int64_t)(up_row + 16 * q) * N + cu), N - cu));
         mbar_arrive(&in2[i % ST]);
       }
     };
-    for (int i = 0; i < min(ST, nb); ++i) fill(i);
+    for (int i = half; i < min(ST, nb); i += 2) fill(i);
     const float bk = back[mine];
-    for (int j = 0; j < nb; ++j) {
+    for (int j = half; j < nb; j += 2) {
       const int col = (b0 + j) * 64;
-      wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
-      wait(&done[j & 1], (j >> 1) & 1);
-      tc_fence_after();
-      float v[32];
-      tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (j & 1) * 64 + half * 32, v);
       unsigned char* tile = ring + (j % ST) * S::STAGE;
-      uint4 y[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        y[c] = base ? *reinterpret_cast<const uint4*>(tile + swizzled(mine, half * 4 + c)) : make_uint4(0, 0, 0, 0);
-      tmem_ld_wait();
-      tc_fence_before();
-      if (lane == 0) mbar_arrive(&drained[j & 1]);
+      wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
+      wait(&done[j % SUMS], (j / SUMS) & 1);
+      tc_fence_after();
       const float lost = gave_up ? NAN : 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
-        uint32_t o[4];
+      for (int h = 0; h < 2; ++h) {
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (j % SUMS) * 64 + h * 32, v);
+        uint4 y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack2(w[e], T());
-          o[e] = pack2(fmaf(v[c * 8 + 2 * e], bk, f.x) + lost, fmaf(v[c * 8 + 2 * e + 1], bk, f.y) + lost, T());
+        for (int c = 0; c < 4; ++c)
+          y[c] = base ? *reinterpret_cast<const uint4*>(tile + swizzled(mine, h * 4 + c)) : make_uint4(0, 0, 0, 0);
+        tmem_ld_wait();
+        if (h == 1) {
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&drained[j % SUMS]);
         }
-        *reinterpret_cast<uint4*>(tile + swizzled(mine, half * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2(w[e], T());
+            o[e] = pack2(fmaf(v[c * 8 + 2 * e], bk, f.x) + lost, fmaf(v[c * 8 + 2 * e + 1], bk, f.y) + lost, T());
+          }
+          *reinterpret_cast<uint4*>(tile + swizzled(mine, h * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
       __syncwarp();
       if constexpr (VEC) {
-        uint4 o[4];
+        uint4 o[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const uint4*>(tile + swizzled(first + 8 * q, sub));
-        __syncwarp();  // (the warp's part of the slot is filled again below)
+        for (int q = 0; q < 8; ++q) o[q] = *reinterpret_cast<const uint4*>(tile + swizzled(first + 4 * q, sub));
         if (col + sub * 8 < N) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (on[q]) *reinterpret_cast<uint4*>(out + at_row[q] * a.out_stride + col + sub * 8) = o[q];
+          for (int q = 0; q < 8; ++q)
+            if (first + 4 * q < count)
+              *reinterpret_cast<uint4*>(out + row_of[first + 4 * q] * a.out_stride + col + sub * 8) = o[q];
         }
       } else {
-        // a row's 32 columns, an element a lane
-        const int c = col + half * 32 + lane;
+        // a row's 64 columns, two elements a lane
         const unsigned char* from = tile + (lane & 7) * 2;
 #pragma unroll 4
-        for (int r = quarter * 32; r < min(quarter * 32 + 32, count); ++r) {
-          const uint16_t v = *reinterpret_cast<const uint16_t*>(from + swizzled(r, half * 4 + (lane >> 3)));
-          if (c < N) reinterpret_cast<uint16_t*>(out)[row_of[r] * a.out_stride + c] = v;
-        }
-        __syncwarp();
+        for (int r = quarter * 32; r < min(quarter * 32 + 32, count); ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = col + h * 32 + lane;
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(from + swizzled(r, h * 4 + (lane >> 3)));
+            if (c < N) reinterpret_cast<uint16_t*>(out)[row_of[r] * a.out_stride + c] = v;
+          }
       }
+      // The slot's next stage, whoever will add to it: its rows of this warp have
+      // been read by this warp, its products are done.
+      __syncwarp();
       if (j + ST < nb) fill(j + ST);
     }
     copy_wait_all();
@@ -429,7 +421,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, SUMS * 64);
   }
 }
 
