@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   unsigned char* ring = smem + S::HIDDEN;
   float* part = reinterpret_cast<float*>(ring);  // (between the products)
   __shared__ int row_of[ADAPTER_TILE];
+  __shared__ int64_t base_at[ADAPTER_TILE], out_at[ADAPTER_TILE];  // the rows' first elements
   __shared__ float back[ADAPTER_TILE];
   __shared__ Piece found;
   // Of the first product's slots: copies in, products done; of the second's: copies
@@ -98,7 +99,10 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     return;
   }
   if (tid < ADAPTER_TILE) {
-    row_of[tid] = tid < count ? a.row_list[p.start + tid] : 0;
+    const int row = tid < count ? a.row_list[p.start + tid] : 0;
+    row_of[tid] = row;
+    base_at[tid] = row * a.base_stride;
+    out_at[tid] = row * a.out_stride;
     back[tid] = 1.0f;
   }
   const T* x = static_cast<const T*>(a.x);
@@ -148,15 +152,15 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     }
     const T* down = static_cast<const T*>(a.first) + (int64_t)group * a.rank * K;
     const auto issue = [&](int i) {
-      const int col = (c0 + i) * 64 + sub * 8;
       const uint32_t at = ring_at + (i % ST) * S::STAGE;
-      const bool in = col < K;
+      const bool in = (c0 + i) * 64 + sub * 8 < K;
+      const int col = in ? (c0 + i) * 64 + sub * 8 : 0;  // (a copy of nothing has an address all the same)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) copy16(at + swizzled(r0 + 32 * q, sub), in ? px[q] + col : x, in && on[q]);
+      for (int q = 0; q < 4; ++q) copy16(at + swizzled(r0 + 32 * q, sub), px[q] + col, in && on[q]);
 #pragma unroll
       for (int r = r0; r < R; r += 32) {
-        const bool have = in && r < a.rank;
-        copy16(at + S::ROWS + swizzled(r, sub), have ? down + (int64_t)r * K + col : down, have);
+        const bool have = r < a.rank;
+        copy16(at + S::ROWS + swizzled(r, sub), down + (have ? r * K : 0) + col, in && have);
       }
     };
     Loose lx[VEC ? 1 : 4], lw[VEC ? 1 : W];
@@ -318,18 +322,16 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       if constexpr (VEC) {
         if (base) {
           const bool in = col + sub * 8 < N;
+          const T* from = base + (in ? col + sub * 8 : 0);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = first + 4 * q;
-            copy16(at + swizzled(r, sub), in ? base + row_of[r] * a.base_stride + col + sub * 8 : base, in && r < count);
-          }
+          for (int q = 0; q < 8; ++q)
+            copy16(at + swizzled(first + 4 * q, sub), from + base_at[first + 4 * q], in && first + 4 * q < count);
         }
         const bool in = col + up_chunk * 8 < N;
+        const T* from = up + (in ? col + up_chunk * 8 : 0);
 #pragma unroll
-        for (int r = up_row; r < R; r += 16) {
-          const bool have = in && r < a.rank;
-          copy16(at + S::ROWS + swizzled(r, up_chunk), have ? up + (int64_t)r * N + col + up_chunk * 8 : up, have);
-        }
+        for (int r = up_row; r < R; r += 16)
+          copy16(at + S::ROWS + swizzled(r, up_chunk), from + (r < a.rank ? r * N : 0), in && r < a.rank);
         copy_arrive(&in2[i % ST]);
       } else {
         const int cb = col + sub * 8, cu = col + up_chunk * 8;
@@ -337,11 +339,11 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
         if (base) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            l[q].load(base + row_of[first + 4 * q] * a.base_stride + cb, N - cb, first + 4 * q < count);
+            l[q].load(base + base_at[first + 4 * q] + cb, N - cb, first + 4 * q < count);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             put16(at + swizzled(first + 4 * q, sub),
-                  l[q].chunk(Loose::odd(base + row_of[first + 4 * q] * a.base_stride + cb), N - cb));
+                  l[q].chunk(Loose::odd(base + base_at[first + 4 * q] + cb), N - cb));
         }
         constexpr int U = R / 16;
 #pragma unroll
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
       wait(&done[j % SUMS], (j / SUMS) & 1);
       tc_fence_after();
-      const float lost = gave_up ? NAN : 0.0f;
+      const float by = gave_up ? NAN : bk;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = unpack2(w[e], T());
-            o[e] = pack2(fmaf(v[c * 8 + 2 * e], bk, f.x) + lost, fmaf(v[c * 8 + 2 * e + 1], bk, f.y) + lost, T());
+            o[e] = pack2(fmaf(v[c * 8 + 2 * e], by, f.x), fmaf(v[c * 8 + 2 * e + 1], by, f.y), T());
           }
           *reinterpret_cast<uint4*>(tile + swizzled(mine, h * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             if (first + 4 * q < count)
-              *reinterpret_cast<uint4*>(out + row_of[first + 4 * q] * a.out_stride + col + sub * 8) = o[q];
+              *reinterpret_cast<uint4*>(out + out_at[first + 4 * q] + col + sub * 8) = o[q];
         }
       } else {
         // a row's 64 columns, two elements a lane
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
           for (int h = 0; h < 2; ++h) {
             const int c = col + h * 32 + lane;
             const uint16_t v = *reinterpret_cast<const uint16_t*>(from + swizzled(r, h * 4 + (lane >> 3)));
-            if (c < N) reinterpret_cast<uint16_t*>(out)[row_of[r] * a.out_stride + c] = v;
+            if (c < N) reinterpret_cast<uint16_t*>(out)[out_at[r] + c] = v;
           }
       }
       // The slot's next stage, whoever will add to it: its rows of this warp have
