@@ -19,6 +19,8 @@
 // all copies of the stage have arrived on its barrier, and their commit frees the
 // slot.  Two CTAs share an SM, so that the join between one's products hides behind
 // the other's copies.  The CTAs of a cluster split a tile as in adapter_apply.cuh.
+// Rows behind a tile's last are not copied: what lies in their places gives rows
+// that are not stored.
 //
 // Waits are bounded: one that runs out raises a flag, further waits return at once,
 // and the tile's rows become NaN.
@@ -156,7 +158,8 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       const bool in = (c0 + i) * 64 + sub * 8 < K;
       const int col = in ? (c0 + i) * 64 + sub * 8 : 0;  // (a copy of nothing has an address all the same)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) copy16(at + swizzled(r0 + 32 * q, sub), px[q] + col, in && on[q]);
+      for (int q = 0; q < 4; ++q)
+        if (on[q]) copy16(at + swizzled(r0 + 32 * q, sub), px[q] + col, in);
 #pragma unroll
       for (int r = r0; r < R; r += 32) {
         const bool have = r < a.rank;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
           const T* from = base + (in ? col + sub * 8 : 0);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            copy16(at + swizzled(first + 4 * q, sub), from + base_at[first + 4 * q], in && first + 4 * q < count);
+            if (first + 4 * q < count) copy16(at + swizzled(first + 4 * q, sub), from + base_at[first + 4 * q], in);
         }
         const bool in = col + up_chunk * 8 < N;
         const T* from = up + (in ? col + up_chunk * 8 : 0);
@@ -362,6 +365,11 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       unsigned char* tile = ring + (j % ST) * S::STAGE;
       wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
       wait(&done[j % SUMS], (j / SUMS) & 1);
+      if (quarter * 32 >= count) {  // (no rows here: only the copies of up)
+        if (lane == 0) mbar_arrive(&drained[j % SUMS]);
+        if (j + ST < nb) fill(j + ST);
+        continue;
+      }
       tc_fence_after();
       const float by = gave_up ? NAN : bk;
 #pragma unroll
