@@ -1,0 +1,163 @@
+"""Edges of the balance loss, gradient clipping and low-rank adapters: offsets past
+32 bits, one short sequence inside a batch, gradients of one row, calls at the
+same time on several streams."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training as ot
+from tests.parity import built, gpu, needs_gpu
+
+pytestmark = [gpu, needs_gpu]
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _lib():
+    import nvfp4_token_quantized_gb300 as lib
+
+    built()
+    return lib
+
+
+def test_gradients_past_32_bit_offsets():
+    clip = _lib().GradientClip(1.0)
+    n = (1 << 31) + 1000
+    t = torch.zeros(n, dtype=BF16, device="cuda")
+    t[5], t[n - 1], t[n - 700] = 3.0, 4.0, 12.0
+    assert clip.norm([t]).item() == 13.0
+    norm, _ = clip.clip([t])
+    assert norm.item() == 13.0
+    f = 1.0 / (13.0 + 1e-6)
+    for at, v in ((5, 3.0), (n - 1, 4.0), (n - 700, 12.0)):
+        assert abs(t[at].item() - v * f) <= 2.0 ** -8 * v * f
+    assert torch.count_nonzero(t).item() == 3
+
+
+def test_rows_past_32_bit_offsets():
+    lib = _lib()
+    T, K, N, r, L = 200, 128, 136, 8, 3
+    g = torch.Generator().manual_seed(0)
+    stride = (1 << 31) // 128 + 8  # rows from 128 on start behind 2^31 elements
+    wide = torch.empty(T * stride, dtype=BF16, device="cuda")
+    ids = torch.randint(0, L, (T,), generator=g).int().cuda()
+    down = (torch.randn(L, r, K, generator=g) / 11).to(BF16).cuda()
+    up = torch.randn(L, r, N, generator=g).to(BF16).cuda()
+    x = torch.randn(T, K, generator=g).to(BF16).cuda()
+    base = torch.randn(T, N, generator=g).to(BF16).cuda()
+    ad = lib.LowRankAdapters(K, N, r)
+    want, hidden = ad.forward(x, ids, down, up, base=base, keep_hidden=True)
+    wantb = ad.backward(base, x, hidden, ids, down, up)
+    xs = wide.as_strided((T, K), (stride, 1))
+    xs.copy_(x)
+    bs = wide.as_strided((T, N), (stride, 1), 256)
+    bs.copy_(base)
+    os = wide.as_strided((T, N), (stride, 1), 512)
+    got, h = ad.forward(xs, ids, down, up, base=bs, out=os, keep_hidden=True)
+    assert torch.equal(got, want) and torch.equal(h, hidden)
+    gotb = ad.backward(bs, xs, h, ids, down, up)
+    assert all(torch.equal(a, b) for a, b in zip(gotb, wantb))
+    # logits alike
+    E, k = 64, 4
+    router = lib.ExpertRouter(E, k)
+    l = torch.randn(T, E, generator=g).to(BF16).cuda()
+    chosen = torch.rand(T, E, generator=g).argsort(dim=1)[:, :k].int().cuda()
+    want = router.balance_loss(l, chosen)
+    ls = wide.as_strided((T, E), (stride, 1), 1024)
+    ls.copy_(l)
+    got = router.balance_loss(ls, chosen)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ds = wide.as_strided((T, E), (stride, 1), 2048)
+    router.balance_backward(ls, got[2], dlogits=ds)
+    assert torch.equal(ds, router.balance_backward(l, want[2]))
+
+
+def test_one_short_sequence_inside_a_batch():
+    router = _lib().ExpertRouter(48, 3, score="sigmoid")
+    g = torch.Generator().manual_seed(1)
+    for T, lo, hi in ((100, 10, 53), (100, 0, 1), (100, 99, 100), (9, 4, 4), (9000, 4000, 4010)):
+        l = torch.randn(T, 48, generator=g).cuda()
+        ids = torch.rand(T, 48, generator=g).argsort(dim=1)[:, :3].int().cuda()
+        off = torch.tensor([lo, hi], dtype=torch.int32, device="cuda")
+        loss, counts, slope = router.balance_loss(l, ids, 0.5, off)
+        (rl, err), rc, (rs, _) = ot.balance(_np(l), ids.cpu().numpy(), 0.5, "sigmoid", [lo, hi])
+        assert np.array_equal(counts.cpu().numpy(), rc)
+        assert abs(loss.item() - rl) <= 2.0 ** -24 * err + 1e-30
+        assert np.allclose(_np(slope), rs, rtol=1e-6, atol=0)
+
+
+def test_offsets_that_break_their_order_stay_inside():
+    """The result is not defined, but nothing outside the outputs changes and
+    the call after it is right."""
+    router = _lib().ExpertRouter(32, 2)
+    g = torch.Generator().manual_seed(2)
+    l = torch.randn(6000, 32, generator=g).cuda()
+    ids = torch.rand(6000, 32, generator=g).argsort(dim=1)[:, :2].int().cuda()
+    good = torch.tensor([0, 3000, 6000], dtype=torch.int32, device="cuda")
+    want = router.balance_loss(l, ids, 1.0, good)
+    for bad in ([5000, 100, 4000], [-50, 9000, 2], [7000, 8000, 9000], [6000, 3000, 0]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        _, _, slope = router.balance_loss(l, ids, 1.0, off)
+        router.balance_backward(l, slope, offsets=off)
+    got = router.balance_loss(l, ids, 1.0, good)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_values_beyond_the_sets_adapters():
+    """ids of every size stand for no adapter."""
+    ad = _lib().LowRankAdapters(64, 64, 4)
+    g = torch.Generator().manual_seed(3)
+    down, up = (torch.randn(2, 4, 64, generator=g).to(F16).cuda() for _ in range(2))
+    for T in (8, 300):
+        x = torch.randn(T, 64, generator=g).to(F16).cuda()
+        ids = torch.tensor([-1, 2, -(1 << 31), (1 << 31) - 1] * (T // 4), dtype=torch.int32, device="cuda")
+        out, h = ad.forward(x, ids, down, up, base=x.clone(), keep_hidden=True)
+        assert torch.equal(out, x) and not h.any()
+
+
+def test_calls_at_the_same_time():
+    """Several streams at once, each with buffers of its own."""
+    lib = _lib()
+    g = torch.Generator().manual_seed(4)
+    T, K, r, L = 3000, 512, 64, 5
+    down = (torch.randn(L, r, K, generator=g) / 22).to(BF16).cuda()
+    up = (torch.randn(L, r, K, generator=g) / 8).to(BF16).cuda()
+    ids = torch.randint(-1, L, (T,), generator=g).int().cuda()
+    xs = [torch.randn(T, K, generator=g).to(BF16).cuda() for _ in range(4)]
+    ad, clip = lib.LowRankAdapters(K, K, r), lib.GradientClip(0.25)
+
+    def step(x):
+        y, h = ad.forward(x, ids, down, up, base=x, keep_hidden=True)
+        grads = ad.backward(y, x, h, ids, down, up)
+        norm, _ = clip.clip(grads[1:])
+        return y, *grads, norm
+
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = []
+        for x, s in zip(xs, streams):
+            s.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(s):
+                got.append(step(x))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_another_device_is_refused_or_used():
+    lib = _lib()
+    clip, ad, router = lib.GradientClip(1.0), lib.LowRankAdapters(8, 8, 2), lib.ExpertRouter(8, 2)
+    cpu = torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        clip.norm([cpu])
+    with pytest.raises(ValueError):
+        ad.forward(cpu.half(), torch.zeros(4, dtype=torch.int32), torch.zeros(1, 2, 8).half(), torch.zeros(1, 2, 8).half())
+    with pytest.raises(ValueError):
+        router.balance_loss(cpu, torch.zeros(4, 2, dtype=torch.int32))
