@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
         float4 f[4][2];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int from = q0 + q < C ? q0 + q : q0;
+          const int from = (crank + (q0 + q < C ? q0 + q : q0)) % C;  // (each begins at its own)
           const float4* p =
               reinterpret_cast<const float4*>((C > 1 ? cluster.map_shared_rank(part, from) : part) + r * RP + lane8 * 8);
           f[q][0] = p[0], f[q][1] = p[1];
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       // columns [0, R) of the panels hold the first parts, [R, 2R) the second
       const int ch = lane8, cl = G + lane8;
       const uint32_t at_hi = (ch >> 3) * S::ROWS + swizzled(r, ch & 7), at_lo = (cl >> 3) * S::ROWS + swizzled(r, cl & 7);
-      for (int q = 0; q < C; ++q) {
+      for (int i = 0; i < C; ++i) {
+        const int q = (crank + i) % C;
         unsigned char* to = C > 1 ? cluster.map_shared_rank(panels, q) : panels;
         *reinterpret_cast<uint4*>(to + at_hi) = hi;
         *reinterpret_cast<uint4*>(to + at_lo) = lo;
