@@ -140,14 +140,14 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
     const int r = i / R, c = i % R, at = r * RP + c;
     float s = 0.0f;
     if (C > 1) {
-      for (int p = 0; p < C; ++p) s += cluster.map_shared_rank(part, p)[at];
+      for (int p = 0; p < C; ++p) s += cluster.map_shared_rank(part, (crank + p) % C)[at];  // (each begins at its own)
     } else {
       for (int w = 0; w < ways; ++w) s += part[w * wm * 16 * RP + at];
     }
     s *= scale;
     if (a.hidden && c < a.rank) a.hidden[(int64_t)row_of[r] * a.rank + c] = s;
     if (C > 1) {
-      for (int p = 0; p < C; ++p) cluster.map_shared_rank(hid, p)[at] = s;
+      for (int p = 0; p < C; ++p) cluster.map_shared_rank(hid, (crank + p) % C)[at] = s;
     } else {
       hid[at] = s;
     }
