@@ -387,7 +387,9 @@ cudaError_t run(const moe_gradient* t, int64_t n, const ClipArgs& a, cudaStream_
     return launch_k(gradient_norm_kernel, dim3(1), dim3(THREADS), 0, s, true, (const double*)a.sums, l.parts, a.norm);
   for (int64_t i = 0; i < n; i += CAP) {
     if (n > CAP) fill(l, t + i, (int)std::min<int64_t>(n - i, CAP));
-    const uint32_t grid = std::min<uint32_t>(l.first[l.n], SCALE_WAVES * CLIP_PARTS);
+    // (in place one wave: most steps change nothing, and its CTAs only look: 48 MB
+    // in 252 tensors 24 us, with twelve waves 32)
+    const uint32_t grid = std::min<uint32_t>(l.first[l.n], (l.in_place ? 1 : SCALE_WAVES) * CLIP_PARTS);
     const cudaError_t e =
         launch_k(gradient_scale_kernel<CAP>, dim3(std::max(grid, 1u)), dim3(THREADS), 0, s, n <= CAP, l);
     if (e != cudaSuccess) return e;
