@@ -150,8 +150,8 @@ typedef struct {
                           MOE_FLAG_STATIC_ACT_SCALES) */
 } moe_config;
 
-/* Expert weights are bf16; the operators around the layer (moe_route_select,
- * moe_block_norm) take any of the three. */
+/* Expert weights are bf16; the operators around the layer take any of the three
+ * (the adapters the two 16-bit ones). */
 typedef enum { MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_F32 = 3 } moe_dtype;
 
 /* Shape of an expert weight tensor as the caller holds it: a contiguous,
@@ -400,13 +400,15 @@ MOE_API moe_status moe_debug_block_scaled_gemm(const uint8_t* a_codes, const uin
                                        float* d, int M, int N, int K, void* stream);
 
 /* ------------------------------------------------------------------------
- * Operators around the layer.  They need no handle, allocate nothing, keep
- * nothing between calls and launch on `stream` of the current device, which
+ * Operators around the layer.  They need no handle, allocate no device memory,
+ * keep nothing between calls and launch on `stream` of the current device, which
  * must be an sm_103a device (else MOE_ERR_UNSUPPORTED).  Row strides are in
  * elements and at least the row's length; rows need no alignment beyond
  * their element's (aligned rows whose length is a multiple of 8, for the
  * routing of 4, take wider loads; of other rows whole 16-byte granules may be
- * read, whose bytes outside the row are not used).  Zero tokens are a no-op.
+ * read, whose bytes outside the row are not used).  Zero tokens are a no-op,
+ * but for sums over them, which become 0.  A workspace is of one call at a time:
+ * the caller orders calls, and graphs, that share one.
  * ------------------------------------------------------------------------ */
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
@@ -647,6 +649,7 @@ MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, 
  *   out_features], contiguous, of `dtype` (bf16 or FP16) as x, base and out.
  * Adapters of lower rank than the set's have rows of zeros.  Sums are FP32;
  * hidden keeps 16 bits or more between the products; out is rounded once.
+ * Kernel-side waits are bounded: rows whose wait ran out become NaN.
  * Limits: rank <= 128, features <= 2^20, num_adapters < 65536. */
 typedef struct {
   int in_features, out_features;

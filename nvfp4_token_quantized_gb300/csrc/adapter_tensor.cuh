@@ -22,6 +22,20 @@
 // Rows behind a tile's last are not copied: what lies in their places gives rows
 // that are not stored.
 //
+// Bound by bytes: x once, base and out once, and from L2 the factors once a tile
+// (as many as x and base again at rank 128).  16384 rows, 4096 to 4096, eight
+// adapters, bf16: rank 16 79 us, 32 81, 64 89, 128 126 for 403 MB (60 us at a copy's
+// rate); of the 89 the plan takes 4, the first product 28, the join 8, the second
+// product 43.  The join is distributed shared memory's: every CTA sums a share of
+// the rows and sends it to the others (gathering all of them everywhere took up to
+// twice the kernel's time at eight CTAs, and lanes of a warp that read several CTAs
+// at once a tenth more).  65536 rows, rank 64: 305 us (241).  Rows of odd alignment
+// take twice the time (16384 rows, 4095 to 4097, rank 16: 180 us).
+//
+// Two of these CTAs at most share an SM, or one beside a CTA of the gradients'
+// kernel (registers, shared memory), and the layer's GEMMs leave no room beside
+// theirs: tensor memory is never waited for.
+//
 // Waits are bounded: one that runs out raises a flag, further waits return at once,
 // and the tile's rows become NaN.
 #pragma once
