@@ -44,6 +44,7 @@ class GradientClip:
         if not (math.isfinite(self.eps) and self.eps > 0.0):
             raise ValueError(f"eps must be finite and positive, got {eps}")
         self._lib = load_library()
+        self._bytes = int(self._lib.moe_gradient_workspace_bytes())
 
     def norm(self, grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
         """The norm of all of grads together, a float32 scalar."""
@@ -68,7 +69,7 @@ class GradientClip:
         if out is not None and len(out) != len(grads):
             raise ValueError(f"out holds {len(out)} tensors for {len(grads)} gradients")
         table, n = self._table(grads, grads if out is None else out, dev), len(grads)
-        norm, ws = _new_scalar(), _new_vector(int(self._lib.moe_gradient_workspace_bytes()), torch.uint8)
+        norm, ws = _new_scalar(), _new_vector(self._bytes, torch.uint8)
         where = table.buffer_info()[0] if n else None
         stream = _current(dev) if stream is None else stream
         if clip:
