@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
         for (int q = 0; q < 4; ++q) {
           const int from = (crank + (q0 + q < C ? q0 + q : q0)) % C;  // (each begins at its own)
           const float4* p =
-              reinterpret_cast<const float4*>((C > 1 ? cluster.map_shared_rank(part, from) : part) + r * RP + lane8 * 8);
+              reinterpret_cast<const float4*>((from != crank ? cluster.map_shared_rank(part, from) : part) + r * RP + lane8 * 8);
           f[q][0] = p[0], f[q][1] = p[1];
         }
 #pragma unroll
@@ -296,10 +296,10 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       const uint32_t at_hi = (ch >> 3) * S::ROWS + swizzled(r, ch & 7), at_lo = (cl >> 3) * S::ROWS + swizzled(r, cl & 7);
       for (int i = 0; i < C; ++i) {
         const int q = (crank + i) % C;
-        unsigned char* to = C > 1 ? cluster.map_shared_rank(panels, q) : panels;
+        unsigned char* to = q != crank ? cluster.map_shared_rank(panels, q) : panels;
         *reinterpret_cast<uint4*>(to + at_hi) = hi;
         *reinterpret_cast<uint4*>(to + at_lo) = lo;
-        if (SCALED && lane8 == 0) *(C > 1 ? cluster.map_shared_rank(&back[r], q) : &back[r]) = b;
+        if (SCALED && lane8 == 0) *(q != crank ? cluster.map_shared_rank(&back[r], q) : &back[r]) = b;
       }
     }
   }
