@@ -649,6 +649,9 @@ MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, 
  *   out_features], contiguous, of `dtype` (bf16 or FP16) as x, base and out.
  * Adapters of lower rank than the set's have rows of zeros.  Sums are FP32;
  * hidden keeps 16 bits or more between the products; out is rounded once.
+ * Values that are no finite numbers stay in their row and adapter; an infinite
+ * element of the second factor, or of x in the factors' gradients, may give NaN
+ * where the formula gives an infinity (hidden's parts meet it one by one).
  * Kernel-side waits are bounded: rows whose wait ran out become NaN.
  * Limits: rank <= 128, features <= 2^20, num_adapters < 65536. */
 typedef struct {

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
     } else {
       for (int w = 0; w < ways; ++w) s += part[w * wm * 16 * RP + at];
     }
-    s *= scale;
+    s = c < a.rank ? s * scale : 0.0f;  // (nothing for the ranks that fill up)
     if (a.hidden && c < a.rank) a.hidden[(int64_t)row_of[r] * a.rank + c] = s;
     if (C > 1) {
       for (int p = 0; p < C; ++p) cluster.map_shared_rank(hid, (crank + p) % C)[at] = s;

@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] *= scale;
+        // (nothing for the ranks that fill up: an infinite x times their zeros is none)
+        v[i] = lane8 * 8 + i < a.rank ? v[i] * scale : 0.0f;
         m = fmaxf(m, fabsf(v[i]));
       }
       if (a.hidden && r < count) {

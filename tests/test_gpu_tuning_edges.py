@@ -120,6 +120,25 @@ def test_values_beyond_the_sets_adapters():
         assert torch.equal(out, x) and not h.any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_an_infinite_row_is_the_formulas(dtype):
+    """Rank 1, filled up to whole fragments: an infinite x gives infinities of
+    the factors' signs, not NaN; other rows stay as they are."""
+    ad = _lib().LowRankAdapters(72, 80, 1)
+    g = torch.Generator().manual_seed(5)
+    down, up = torch.randn(2, 1, 72, generator=g).to(dtype).cuda(), torch.randn(2, 1, 80, generator=g).to(dtype).cuda()
+    for T in (8, 300):
+        x = torch.randn(T, 72, generator=g).to(dtype).cuda()
+        ids = (torch.arange(T, device="cuda") % 2).int()
+        want, _ = ad.forward(x, ids, down, up)
+        x[3, 5] = float("inf")
+        out, h = ad.forward(x, ids, down, up, keep_hidden=True)
+        assert torch.equal(out[3], torch.sign(down[1, 0, 5]) * torch.sign(up[1, 0]) * float("inf"))
+        assert torch.isinf(h[3, 0])
+        keep = torch.arange(T, device="cuda") != 3
+        assert torch.equal(out[keep], want[keep])
+
+
 def test_calls_at_the_same_time():
     """Several streams at once, each with buffers of its own."""
     lib = _lib()
