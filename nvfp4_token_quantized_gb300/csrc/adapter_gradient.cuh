@@ -24,7 +24,7 @@
 
 namespace moe {
 
-constexpr int GRADIENT_COLUMNS = 256, GRADIENT_ROWS = 32;  // of a CTA, of a stage
+constexpr int GRADIENT_COLUMNS = 256;                      // of a CTA
 constexpr int SPLIT_ROWS = 64;                             // of a CTA that splits
 
 template <int R>
@@ -37,6 +37,15 @@ struct GradientShared {
   static constexpr int D = R <= 64 ? 64 : 128;                // tensor memory columns of 128 columns of x
   static constexpr int BYTES = STAGES * STAGE + 1024;         // (aligned inside)
 };
+
+// Where a piece's stages of hidden's parts begin (numbered as pieces are), and
+// where the sums of a group that begins at row `start` of the list and has several
+// pieces: such a group of n rows has at most 2n / unit, so twice as many places as
+// pieces of all rows are enough, whatever the number of adapters.
+__device__ __forceinline__ int64_t first_stage(const Piece& p, int unit) {
+  return (p.start - p.number * unit) / GRADIENT_ROWS + p.group + (int64_t)p.number * (unit / GRADIENT_ROWS);
+}
+__device__ __forceinline__ int64_t first_sums(int start, int unit) { return 2 * (int64_t)start / unit; }
 
 // hidden's parts of one piece: [stage][panel][row] of 128 bytes, swizzled; ranks
 // [0, R) of the panels' columns hold the first parts, [R, 2R) the second.
@@ -80,7 +89,7 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
     if (tid == 0 && blockIdx.z == 0) a.back[side][blockIdx.x] = back;
   }
   const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
-  unsigned char* to = a.parts[side] + (int64_t)blockIdx.x * (a.unit / GRADIENT_ROWS) * S::HIDDEN;
+  unsigned char* to = a.parts[side] + first_stage(p, a.unit) * S::HIDDEN;
   const int stop = min(stages * GRADIENT_ROWS, (int)(blockIdx.z + 1) * SPLIT_ROWS);
   for (int r = blockIdx.z * SPLIT_ROWS + tid / G; r < stop; r += 256 / G) {
     float v[8];
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   };
 
   const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
-  const unsigned char* parts = a.parts[side] + (int64_t)blockIdx.x * (a.unit / GRADIENT_ROWS) * S::HIDDEN;
+  const unsigned char* parts = a.parts[side] + first_stage(p, a.unit) * S::HIDDEN;
   // a warp copies whole rows: 32 chunks of 16 bytes, four rows a warp
   const int col = n0 + lane * 8;
   const bool in = col < N;
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
     const float lost = gave_up ? NAN : 0.0f;
     const int64_t n = (int64_t)a.rank * N;
     const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
-    float* sums = a.sums[side] + (int64_t)blockIdx.x * n + c;
+    float* sums = a.sums[side] + (first_sums(p.start - p.number * a.unit, a.unit) + p.number) * n + c;
     T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
   #pragma unroll
     for (int r0 = 0; r0 < R; r0 += 8) {
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(256) adapter_join_kernel(const OuterArgs a) {
   const int lo = a.starts[group], hi = a.starts[group + 1];
   const int parts = (hi - lo + a.unit - 1) / a.unit;
   if (parts == 1) return;  // (written already)
-  const float* sums = a.sums[side] + (lo / a.unit + group) * n;
+  const float* sums = a.sums[side] + first_sums(lo, a.unit) * n;
   T* out = static_cast<T*>(a.grad[side]) + group * n;
   constexpr int U = 4;  // elements and pieces whose loads are in flight together
   for (int64_t i = (int64_t)blockIdx.x * 256 * U + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256 * U) {

@@ -101,13 +101,15 @@ Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
   const int unit = outer_unit(rows);
   const int64_t pieces = backward ? pieces_of(rows, c.num_adapters, unit) : 0;
   // (two 16-bit parts of up to 16, 32, 64 or 128 ranks in rows of 128 bytes)
-  const int64_t part = pieces * unit * (c.rank <= 32 ? 1 : c.rank <= 64 ? 2 : 4) * 32;
+  const int64_t stages = backward ? pieces_of(rows, c.num_adapters, GRADIENT_ROWS) : 0;
+  const int64_t part = stages * GRADIENT_ROWS * (c.rank <= 32 ? 1 : c.rank <= 64 ? 2 : 4) * 32;
+  const int64_t sums = backward ? 2 * rows / unit + 1 : 0;
   l.back = l.hidden + (backward ? words16(rows * c.rank) : 0);
   l.parts[0] = l.back + words16(2 * pieces);
   l.parts[1] = l.parts[0] + part;
   l.sums[0] = l.parts[1] + part;
-  l.sums[1] = l.sums[0] + words16(pieces * c.rank * c.in_features);
-  l.end = l.sums[1] + words16(pieces * c.rank * c.out_features);
+  l.sums[1] = l.sums[0] + words16(sums * c.rank * c.in_features);
+  l.end = l.sums[1] + words16(sums * c.rank * c.out_features);
   return l;
 }
 

@@ -139,6 +139,32 @@ def test_an_infinite_row_is_the_formulas(dtype):
         assert torch.equal(out[keep], want[keep])
 
 
+def test_the_workspace_follows_the_rows():
+    """A thousand adapters cost a batch of some rows no more than its sums, and
+    groups of one, two and many pieces beside empty ones keep theirs apart."""
+    ad = _lib().LowRankAdapters(256, 264, 16)
+    assert ad.workspace_bytes(100, 1000, True) < 16 << 20
+    T, L = 2600, 300
+    g = torch.Generator().manual_seed(6)
+    sizes = {3: 1, 4: 192, 5: 193, 120: 900, 121: 385, 250: 384, 299: 500}
+    which = torch.cat([torch.full((n,), a) for a, n in sizes.items()])
+    ids = torch.full((T,), -1)
+    ids[torch.randperm(T, generator=g)[:which.numel()]] = which
+    x, d = torch.randn(T, 256, generator=g).to(BF16).cuda(), torch.randn(T, 264, generator=g).to(BF16).cuda()
+    down, up = (torch.randn(L, 16, n, generator=g).mul(0.1).to(BF16).cuda() for n in (256, 264))
+    ids = ids.int().cuda()
+    _, h = ad.forward(x, ids, down, up, keep_hidden=True)
+    _, dd, du = ad.backward(d, x, h, ids, down, up)
+    _, v, _, _ = ot.adapters(_np(d), ids.cpu().numpy(), _np(up), _np(down))
+    for a in range(L):
+        rows = (ids == a).cpu().numpy()
+        for got, left, right in ((dd[a], v, _np(x)), (du[a], _np(h), _np(d))):
+            want = left[rows].T @ right[rows]
+            mag = np.abs(left[rows]).T @ np.abs(right[rows])
+            # (half a step of bf16; FP32 sums and the two parts, of their terms)
+            assert (np.abs(_np(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -13 * mag + 1e-37).all(), a
+
+
 def test_calls_at_the_same_time():
     """Several streams at once, each with buffers of its own."""
     lib = _lib()
