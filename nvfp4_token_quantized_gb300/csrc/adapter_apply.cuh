@@ -42,9 +42,13 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   __shared__ int row_of[ADAPTER_TILE];
   __shared__ int counts[4];  // of the warps that hold a row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int C = a.cluster, crank = blockIdx.x % C, group = blockIdx.x / C;
+  const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
 
   // ---- the group's rows, found in ids ----
+  // Of more adapters than rows a cluster stands for a row, and takes its adapter
+  // if no row before has the same.
+  const bool by_row = a.L + 1 > a.rows;
+  const int group = by_row ? adapter_key(a.ids[number], a.L) : number;
   const bool mine = tid < a.rows && adapter_key(a.ids[tid], a.L) == group;
   const unsigned m = __ballot_sync(0xffffffffu, mine);
   if (warp < 4 && lane == 0) counts[warp] = __popc(m);
@@ -58,6 +62,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   if (mine) row_of[before + __popc(m & ((1u << lane) - 1))] = tid;
   if (count == 0) return;  // (the whole cluster)
   __syncthreads();
+  if (by_row && row_of[0] != number) return;
 
   const T* x = static_cast<const T*>(a.x);
   const T* base = static_cast<const T*>(a.base);

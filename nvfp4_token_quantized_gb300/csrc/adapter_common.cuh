@@ -100,8 +100,10 @@ __device__ __forceinline__ float exponent_scale(float m, float& back) {
 
 // ---- rows by adapter ----
 
-// Adapter a's rows are rows[starts[a]] .. rows[starts[a + 1] - 1], in ascending
-// order; group L holds the rows without an adapter, starts[L + 1] = T.
+// Group i's rows are rows[starts[i]] .. rows[starts[i + 1] - 1], in ascending
+// order.  Of few adapters every one is a group, and L the rows without one; of many
+// only those that have rows, in ascending order (group_of says which; groups behind
+// the last begin at T).
 __device__ __forceinline__ int adapter_key(int id, int L) { return (unsigned)id < (unsigned)L ? id : L; }
 
 // Row pitch of FP32 tiles in shared memory: the eight rows and four pairs of a
@@ -153,10 +155,10 @@ cudaError_t launch_clustered(K kernel, const AdapterArgs& a, int threads, int by
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Pieces of `unit` rows of the groups: group a's pieces have the numbers
-// starts[a] / unit + a and up; numbers between two groups' may be unused.
+// Pieces of `unit` rows of the groups: group i's pieces have the numbers
+// starts[i] / unit + i and up; numbers between two groups' may be unused.
 struct Piece {
-  int group;
+  int group;         // -1: none of the number
   int start, count;  // in rows[]
   int number;        // of the group's pieces
 };

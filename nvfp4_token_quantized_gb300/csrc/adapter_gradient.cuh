@@ -38,6 +38,10 @@ struct GradientShared {
   static constexpr int BYTES = STAGES * STAGE + 1024;         // (aligned inside)
 };
 
+__device__ __forceinline__ int adapter_of(const OuterArgs& a, int group) {
+  return a.group_of ? a.group_of[group] : group;
+}
+
 // Where a piece's stages of hidden's parts begin (numbered as pieces are), and
 // where the sums of a group that begins at row `start` of the list and has several
 // pieces: such a group of n rows has at most 2n / unit, so twice as many places as
@@ -59,8 +63,8 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
   pdl_wait();
   pdl_trigger();
   // (blockIdx.z: SPLIT_ROWS of the piece's rows)
-  const Piece p = find_piece(a.starts, a.L, a.unit, blockIdx.x, &found);
-  if (p.group < 0) return;
+  const Piece p = find_piece(a.starts, a.groups, a.unit, blockIdx.x, &found);
+  if (p.group < 0 || adapter_of(a, p.group) == a.L) return;
   const float* hidden = a.hidden[side];
   const int32_t* rows = a.row_list + p.start;
   constexpr int G = R / 8;  // threads of a row, eight ranks each
@@ -137,9 +141,10 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   const uint32_t tmem = tmem_at;
   pdl_wait();
   pdl_trigger();
-  const Piece p = find_piece(a.starts, a.L, a.unit, blockIdx.x, &found);
+  const Piece p = find_piece(a.starts, a.groups, a.unit, blockIdx.x, &found);
   const int side = blockIdx.y < a.blocks[0] ? 0 : 1;  // down's gradient, then up's
-  if (p.group < 0) {
+  const int adapter = p.group < 0 ? a.L : adapter_of(a, p.group);
+  if (adapter == a.L) {  // (rows without one have no factors)
     if (warp == 0) tmem_dealloc(tmem, 2 * S::D);
     return;
   }
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
     const int64_t n = (int64_t)a.rank * N;
     const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
     float* sums = a.sums[side] + (first_sums(p.start - p.number * a.unit, a.unit) + p.number) * n + c;
-    T* grad = static_cast<T*>(a.grad[side]) + p.group * n + c;
+    T* grad = static_cast<T*>(a.grad[side]) + adapter * n + c;
   #pragma unroll
     for (int r0 = 0; r0 < R; r0 += 8) {
       float v[8], w[8];
@@ -267,19 +272,21 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   }
 }
 
-// A factor's gradient: its pieces' sums in order, rounded once.
+// A factor's gradient: its pieces' sums in order, rounded once; zeros for an
+// adapter without rows (of many adapters they are written beforehand).
 template <typename T>
 __global__ void __launch_bounds__(256) adapter_join_kernel(const OuterArgs a) {
   pdl_wait();
-  const int side = blockIdx.z, group = blockIdx.y;
+  const int side = blockIdx.z, group = blockIdx.x, adapter = adapter_of(a, group);
+  if (adapter < 0 || adapter == a.L) return;
   const int64_t n = (int64_t)a.rank * a.width[side];
   const int lo = a.starts[group], hi = a.starts[group + 1];
   const int parts = (hi - lo + a.unit - 1) / a.unit;
   if (parts == 1) return;  // (written already)
   const float* sums = a.sums[side] + first_sums(lo, a.unit) * n;
-  T* out = static_cast<T*>(a.grad[side]) + group * n;
+  T* out = static_cast<T*>(a.grad[side]) + adapter * n;
   constexpr int U = 4;  // elements and pieces whose loads are in flight together
-  for (int64_t i = (int64_t)blockIdx.x * 256 * U + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256 * U) {
+  for (int64_t i = (int64_t)blockIdx.y * 256 * U + threadIdx.x; i < n; i += (int64_t)gridDim.y * 256 * U) {
     float s[U] = {};
     for (int p = 0; p < parts; p += U) {
       float v[U][U];
@@ -304,7 +311,7 @@ cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
   const auto kernel = adapter_gradient_kernel<T, R, VEC>;
   cudaError_t e = raise_shared(kernel, GradientShared<R>::BYTES, done);
   if (e != cudaSuccess) return e;
-  const unsigned pieces = (unsigned)pieces_of(a.rows, a.L, a.unit);
+  const unsigned pieces = (unsigned)pieces_of(a.rows, a.groups, a.unit);
   e = launch_k(adapter_split_kernel<T, R>, dim3(pieces, 2, (unsigned)(a.unit / SPLIT_ROWS)), dim3(256), 0, s, true,
                a);
   if (e != cudaSuccess) return e;
@@ -312,7 +319,7 @@ cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
                GradientShared<R>::BYTES, s, true, a);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);
-  const dim3 grid((unsigned)std::min<int64_t>((n + 1023) / 1024, 1024), (unsigned)a.L, 2);
+  const dim3 grid((unsigned)a.groups, (unsigned)std::min<int64_t>((n + 1023) / 1024, 1024), 2);
   return launch_k(adapter_join_kernel<T>, grid, dim3(256), 0, s, true, a);
 }
 

@@ -107,13 +107,13 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   tc_fence_after();
   const uint32_t tmem = tmem_at, ring_at = smem_u32(ring), panels_at = smem_u32(panels);
   pdl_wait();
-  const Piece p = find_piece(a.starts, a.L + 1, ADAPTER_TILE, number, &found);
+  const Piece p = find_piece(a.starts, a.groups, ADAPTER_TILE, number, &found);
   pdl_trigger();
-  const int count = p.count, group = p.group;
-  if (group < 0) {  // (the whole cluster)
+  if (p.group < 0) {  // (the whole cluster)
     if (warp == 0) tmem_dealloc(tmem, SUMS * 64);
     return;
   }
+  const int count = p.count, group = a.group_of ? a.group_of[p.group] : p.group;  // (the adapter)
   if (tid < ADAPTER_TILE) {
     const int row = tid < count ? a.row_list[p.start + tid] : 0;
     row_of[tid] = row;

@@ -26,17 +26,68 @@ __device__ __forceinline__ void load_groups(const int32_t* ids, int64_t first, i
   }
 }
 
-// Group blockIdx.x (an adapter, or L for rows without one): its first place,
-// the number of rows of the groups before it, and its rows in ascending order.
-// Every CTA goes through all ids, 16 a thread and round (up to 16384 rows, once):
-// no CTA waits for another.  (16384 rows: 4 us; the kernel behind is set up
-// meanwhile.)
+constexpr int MAX_WORDS = (65536 + 32) / 32 + 1;  // a bit for each adapter and for none
+
+// The adapter with rows (L: rows without one) that comes in place `index`, or -1:
+// all threads mark the adapters they meet, then count.
+__device__ __forceinline__ int present_group(const int32_t* ids, int rows, int L, int index) {
+  constexpr int PER = 16, ROUND = PLAN_THREADS * PER, EACH = (MAX_WORDS + PLAN_THREADS - 1) / PLAN_THREADS;
+  __shared__ unsigned marks[EACH * PLAN_THREADS];
+  __shared__ int sums[32], result;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < EACH * PLAN_THREADS; i += PLAN_THREADS) marks[i] = 0;
+  if (tid == 0) result = -1;
+  __syncthreads();
+  for (int64_t base = 0; base < rows; base += ROUND) {
+    int g[PER];
+    load_groups(ids, base + tid * PER, rows, L, g);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (g[i] >= 0 && !(*(volatile unsigned*)&marks[g[i] >> 5] >> (g[i] & 31) & 1)) atomicOr(&marks[g[i] >> 5], 1u << (g[i] & 31));
+  }
+  __syncthreads();
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) mine += __popc(marks[tid * EACH + i]);
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(ALL, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  const int w = sums[lane];
+  int before = __reduce_add_sync(ALL, lane < warp ? w : 0) + upto - mine;
+  if (index >= before && index < before + mine) {
+    for (int i = 0; i < EACH; ++i) {
+      unsigned m = marks[tid * EACH + i];
+      for (; m; m &= m - 1)
+        if (before++ == index) result = (tid * EACH + i) * 32 + __ffs(m) - 1;
+    }
+  }
+  __syncthreads();
+  return result;
+}
+
+// Group blockIdx.x: its first place, the number of rows of the groups before it,
+// and its rows in ascending order.  Every CTA goes through all ids, 16 a thread and
+// round (up to 16384 rows, once): no CTA waits for another.  (16384 rows: 4 us; the
+// kernel behind is set up meanwhile.)  group_of: only groups with rows.
 __global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_t* ids, int rows, int L,
-                                                                    int32_t* starts, int32_t* row_list) {
+                                                                    int32_t* starts, int32_t* row_list,
+                                                                    int32_t* group_of) {
   constexpr int PER = 16, ROUND = PLAN_THREADS * PER;
   __shared__ int less_sum[32], warp_sum[32];
   pdl_trigger();
-  const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = group_of ? present_group(ids, rows, L, blockIdx.x) : blockIdx.x;
+  if (tid == 0 && blockIdx.x == gridDim.x - 1) starts[gridDim.x] = rows;
+  if (tid == 0 && group_of) group_of[blockIdx.x] = group;
+  if (group < 0 || rows == 0) {
+    if (tid == 0) starts[blockIdx.x] = rows;
+    return;
+  }
   int g[PER], less = 0;
   for (int64_t base = 0; base < rows; base += ROUND) {
     load_groups(ids, base + tid * PER, rows, L, g);
@@ -61,7 +112,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_
     if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
     if (base == 0) at = __reduce_add_sync(ALL, less_sum[lane]);
-    if (base == 0 && tid == 0) starts[group] = at;
+    if (base == 0 && tid == 0) starts[blockIdx.x] = at;
     const int w = warp_sum[lane];
     const int before = __reduce_add_sync(ALL, lane < warp ? w : 0), all = __reduce_add_sync(ALL, w);
     int put = at + before + upto - n;
@@ -73,18 +124,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_
     at += all;
     __syncthreads();  // (the next round overwrites the warps' sums)
   }
-  if (tid == 0) {
-    if (rows == 0) starts[group] = 0;
-    if (group == L) starts[L + 1] = rows;
-  }
 }
 
 int64_t words16(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Where the parts of a workspace lie, in 4-byte words, 16-byte aligned.
 struct Layout {
-  int64_t starts, row_list, hidden, back, parts[2], sums[2], end;
+  int64_t starts, row_list, group_of, hidden, back, parts[2], sums[2], end;
 };
+
+// Groups of a call.  Of few adapters each is one, with rows or without; of more only
+// as many as rows can have: a CTA of the plan and a tile's number each, for a search
+// of 4 us (300 rows: 64 adapters 32 and 36 us, 256 52 and 55, 1000 91 and 51).
+constexpr int FEW_GROUPS = 256;
+bool few_groups(int L) { return L < FEW_GROUPS; }
+int groups_of(int64_t rows, int L) { return (int)(few_groups(L) ? L + 1 : std::min<int64_t>(L + 1, std::max<int64_t>(rows, 1))); }
 
 int outer_unit(int64_t rows) {
   // about sixteen pieces of a large batch: with a side's column blocks that fills
@@ -96,12 +150,14 @@ int outer_unit(int64_t rows) {
 Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
   Layout l{};
   l.starts = 0;
-  l.row_list = words16(c.num_adapters + 2);
-  l.hidden = l.row_list + words16(rows);
+  const int groups = groups_of(rows, c.num_adapters);
+  l.row_list = words16(groups + 1);
+  l.group_of = l.row_list + words16(rows);
+  l.hidden = l.group_of + words16(groups);
   const int unit = outer_unit(rows);
-  const int64_t pieces = backward ? pieces_of(rows, c.num_adapters, unit) : 0;
+  const int64_t pieces = backward ? pieces_of(rows, groups, unit) : 0;
   // (two 16-bit parts of up to 16, 32, 64 or 128 ranks in rows of 128 bytes)
-  const int64_t stages = backward ? pieces_of(rows, c.num_adapters, GRADIENT_ROWS) : 0;
+  const int64_t stages = backward ? pieces_of(rows, groups, GRADIENT_ROWS) : 0;
   const int64_t part = stages * GRADIENT_ROWS * (c.rank <= 32 ? 1 : c.rank <= 64 ? 2 : 4) * 32;
   const int64_t sums = backward ? 2 * rows / unit + 1 : 0;
   l.back = l.hidden + (backward ? words16(rows * c.rank) : 0);
@@ -114,8 +170,9 @@ Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
 }
 
 cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
-  return launch_k(adapter_plan_kernel, dim3((unsigned)a.L + 1), dim3(PLAN_THREADS), 0, s, false, a.ids, (int)a.rows,
-                  a.L, const_cast<int32_t*>(a.starts), const_cast<int32_t*>(a.row_list));
+  return launch_k(adapter_plan_kernel, dim3((unsigned)a.groups), dim3(PLAN_THREADS), 0, s, false, a.ids, (int)a.rows,
+                  a.L, const_cast<int32_t*>(a.starts), const_cast<int32_t*>(a.row_list),
+                  const_cast<int32_t*>(a.group_of));
 }
 
 // CTAs of a cluster: as many as keep the likely tiles within one wave of two
@@ -129,7 +186,7 @@ int cluster_of(int64_t tiles, int64_t rows, int L) {
 }
 
 cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
-  a.tiles = planned ? pieces_of(a.rows, a.L + 1, ADAPTER_TILE) : a.L + 1;
+  a.tiles = planned ? pieces_of(a.rows, a.groups, ADAPTER_TILE) : std::min<int64_t>(a.L + 1, a.rows);
   a.cluster = cluster_of(a.tiles, a.rows, a.L);
   if (planned) return f16 ? launch_tensor_f16(a, vec, s) : launch_tensor_bf16(a, vec, s);
   return f16 ? launch_apply_f16(a, vec, s) : launch_apply_bf16(a, vec, s);
@@ -147,6 +204,8 @@ cudaError_t launch_adapter(AdapterArgs a, const moe_adapter_config& c, bool vec,
   int32_t* w = static_cast<int32_t*>(workspace);
   a.starts = w + l.starts;
   a.row_list = w + l.row_list;
+  a.groups = groups_of(a.rows, a.L);
+  a.group_of = few_groups(a.L) ? nullptr : w + l.group_of;
   const bool planned = a.rows > ADAPTER_TILE;
   if (planned) {
     const cudaError_t e = launch_plan(a, s);
@@ -161,9 +220,15 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
   int32_t* w = static_cast<int32_t*>(workspace);
   a.starts = o.starts = w + l.starts;
   a.row_list = o.row_list = w + l.row_list;
+  a.groups = o.groups = groups_of(a.rows, a.L);
+  a.group_of = o.group_of = few_groups(a.L) ? nullptr : w + l.group_of;
   a.hidden = reinterpret_cast<float*>(w + l.hidden);
   const bool f16 = c.dtype == MOE_DTYPE_F16;
-  cudaError_t e = launch_plan(a, s);
+  cudaError_t e = cudaSuccess;
+  if (a.group_of)  // (most adapters have no rows, and no group that would write zeros)
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+      e = cudaMemsetAsync(o.grad[i], 0, (size_t)a.L * a.rank * o.width[i] * 2, s);
+  if (e == cudaSuccess) e = launch_plan(a, s);
   if (e == cudaSuccess) e = apply(a, f16, vec, true, s);
   if (e != cudaSuccess) return e;
   o.hidden[0] = a.hidden;  // down's gradient goes by dout up^T, up's by the forward's hidden
@@ -176,7 +241,7 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
   for (int i = 0; i < 2; ++i) {
     o.blocks[i] = (o.width[i] + 255) / 256;
     o.parts[i] = reinterpret_cast<unsigned char*>(w + l.parts[i]);
-    o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, a.L, o.unit);
+    o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, o.groups, o.unit);
   }
   return f16 ? launch_gradient_f16(o, vec, s) : launch_gradient_bf16(o, vec, s);
 }

@@ -143,6 +143,8 @@ struct AdapterArgs {
   int in, n_out, rank, L;
   // set by the launch
   const int32_t *starts, *row_list;
+  const int32_t* group_of;  // groups' adapters; NULL: group a is adapter a
+  int groups;
   int64_t tiles;
   int cluster;
 };
@@ -155,7 +157,8 @@ struct OuterArgs {
   void* grad[2];
   int width[2];
   // set by the launch
-  const int32_t *starts, *row_list;
+  const int32_t *starts, *row_list, *group_of;
+  int groups;
   float* sums[2];
   unsigned char* parts[2];  // hidden split in two
   float* back[2];           // and its scale, a piece each (FP16)

@@ -165,6 +165,42 @@ def test_the_workspace_follows_the_rows():
             assert (np.abs(_np(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -13 * mag + 1e-37).all(), a
 
 
+@pytest.mark.parametrize("L", [64, 255, 256, 257, 500, 65535])
+def test_many_adapters(L):
+    """Around the number of adapters from which only those with rows are listed,
+    and the largest; the first and the last among those that have rows."""
+    ad = _lib().LowRankAdapters(24, 40, 3)
+    g = torch.Generator().manual_seed(7)
+    down, up = (torch.randn(L, 3, n, generator=g).to(BF16).cuda() for n in (24, 40))
+    for T in (1, 7, 100, 129, 700, 17000):
+        ids = torch.randint(-2, L + 2, (T,), generator=g).int()
+        ids[::3] = L - 1
+        ids[::5] = 0
+        ids[::7] = -1
+        x, d = torch.randn(T, 24, generator=g).to(BF16).cuda(), torch.randn(T, 40, generator=g).to(BF16).cuda()
+        which = ids.cuda()
+        out, h = ad.forward(x, which, down, up, base=d, keep_hidden=True)
+        has = (ids >= 0) & (ids < L)
+        a = ids.clamp(0, L - 1).long()
+        dn, un = down.cpu().double()[a], up.cpu().double()[a]
+        hr = torch.einsum("tk,trk->tr", x.cpu().double(), dn) * has[:, None]
+        want = d.cpu().double() + torch.einsum("tr,trn->tn", hr, un)
+        mag = d.cpu().double().abs() + torch.einsum("tr,trn->tn", torch.einsum(
+            "tk,trk->tr", x.cpu().double().abs(), dn.abs()), un.abs())
+        # (FP32 sums of 24 and 3 products, two 16-bit parts; half a step of bf16)
+        assert ((h.cpu().double() - hr).abs() <= 2.0 ** -16 * mag.amax(1, keepdim=True)).all()
+        assert ((out.cpu().double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * mag).all()
+        _, dd, du = ad.backward(d, x, h, which, down, up)
+        present = torch.zeros(L, dtype=torch.bool)
+        present[a[has]] = True
+        assert not dd.cpu()[~present].any() and not du.cpu()[~present].any()
+        for i in (0, L - 1, L // 2):
+            rows = ids == i
+            r = h.cpu().double()[rows].t() @ d.cpu().double()[rows]
+            m = h.cpu().double()[rows].abs().t() @ d.cpu().double()[rows].abs()
+            assert ((du[i].cpu().double() - r).abs() <= 2.0 ** -8 * r.abs() + 2.0 ** -13 * m + 1e-37).all()
+
+
 def test_calls_at_the_same_time():
     """Several streams at once, each with buffers of its own."""
     lib = _lib()
