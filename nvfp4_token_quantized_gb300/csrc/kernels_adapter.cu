@@ -176,13 +176,17 @@ cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
 }
 
 // CTAs of a cluster: as many as keep the likely tiles within one wave of two
-// CTAs an SM (half of the adapters' last tiles count: which are used is known
-// on the device only).  16384 rows, rank 64: two 89 us, one 108, four 122; 4096
-// rows, rank 16: eight 31, four 39.
+// CTAs an SM.  Which adapters have rows is known on the device only: half of
+// their last tiles count, and a quarter for the step from one CTA to two (a CTA
+// alone takes all of both long axes).  16384 rows, rank 64: two 89 us, one 108,
+// four 122; 4096 rows, rank 16: eight 31, four 39; 512 rows, rank 16, of 1, 8,
+// 64 and all of 300 adapters: two 41, 37, 35 and 60 us, one 63, 55, 48 and 52.
 int cluster_of(int64_t tiles, int64_t rows, int L) {
-  const int64_t full = std::min<int64_t>(rows, (rows + ADAPTER_TILE - 1) / ADAPTER_TILE + std::min<int64_t>(L, rows) / 2);
-  const int64_t t = std::max<int64_t>(std::min(tiles, full), 1);
-  return t * 8 <= 304 ? 8 : t * 4 <= 304 ? 4 : t * 2 <= 304 ? 2 : 1;
+  const auto likely = [&](int share) {
+    const int64_t full = (rows + ADAPTER_TILE - 1) / ADAPTER_TILE + std::min<int64_t>(L, rows) / share;
+    return std::max<int64_t>(std::min(tiles, std::min(rows, full)), 1);
+  };
+  return likely(2) * 8 <= 304 ? 8 : likely(2) * 4 <= 304 ? 4 : likely(4) * 2 <= 304 ? 2 : 1;
 }
 
 cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
