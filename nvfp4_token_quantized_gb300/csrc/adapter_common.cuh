@@ -168,11 +168,13 @@ __host__ __device__ __forceinline__ int64_t pieces_of(int64_t rows, int64_t grou
 }
 
 // The piece of a number, by all threads of the CTA; group -1 for an unused
-// number.  `found` is shared.
-__device__ __forceinline__ Piece find_piece(const int32_t* starts, int groups, int unit, int number, Piece* found) {
+// number.  `found` is shared.  (Group a's numbers lie in [a, a + rows / unit].)
+__device__ __forceinline__ Piece find_piece(const int32_t* starts, int64_t rows, int groups, int unit, int number,
+                                            Piece* found) {
   if (threadIdx.x == 0) found->group = -1;
   __syncthreads();
-  for (int a = threadIdx.x; a < groups; a += blockDim.x) {
+  const int last = min(number, groups - 1);
+  for (int a = max(number - (int)(rows / unit), 0) + threadIdx.x; a <= last; a += blockDim.x) {
     const int lo = starts[a], hi = starts[a + 1];
     const int i = number - (lo / unit + a);
     if (i >= 0 && lo + (int64_t)i * unit < hi) {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
   pdl_wait();
   pdl_trigger();
   // (blockIdx.z: SPLIT_ROWS of the piece's rows)
-  const Piece p = find_piece(a.starts, a.groups, a.unit, blockIdx.x, &found);
+  const Piece p = find_piece(a.starts, a.rows, a.groups, a.unit, blockIdx.x, &found);
   if (p.group < 0 || adapter_of(a, p.group) == a.L) return;
   const float* hidden = a.hidden[side];
   const int32_t* rows = a.row_list + p.start;
@@ -122,6 +122,13 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   __shared__ volatile int gave_up;
   __shared__ int row_of[1024];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Piece p;
+  if (a.group_of) {  // (as in adapter_tensor.cuh)
+    pdl_wait();
+    pdl_trigger();
+    p = find_piece(a.starts, a.rows, a.groups, a.unit, blockIdx.x, &found);
+    if (p.group < 0) return;
+  }
   // (set up while the kernels before run)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -139,9 +146,11 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  pdl_wait();
-  pdl_trigger();
-  const Piece p = find_piece(a.starts, a.groups, a.unit, blockIdx.x, &found);
+  if (!a.group_of) {
+    pdl_wait();
+    pdl_trigger();
+    p = find_piece(a.starts, a.rows, a.groups, a.unit, blockIdx.x, &found);
+  }
   const int side = blockIdx.y < a.blocks[0] ? 0 : 1;  // down's gradient, then up's
   const int adapter = p.group < 0 ? a.L : adapter_of(a, p.group);
   if (adapter == a.L) {  // (rows without one have no factors)
@@ -319,7 +328,9 @@ cudaError_t launch_gradient_one(const OuterArgs& a, cudaStream_t s) {
                GradientShared<R>::BYTES, s, true, a);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.rank * std::max(a.width[0], a.width[1]);
-  const dim3 grid((unsigned)a.groups, (unsigned)std::min<int64_t>((n + 1023) / 1024, 1024), 2);
+  // (of many groups few have several pieces: fewer CTAs each)
+  const int64_t most = std::max<int64_t>(16384 / a.groups, 4);
+  const dim3 grid((unsigned)a.groups, (unsigned)std::min<int64_t>((n + 1023) / 1024, a.group_of ? most : 1024), 2);
   return launch_k(adapter_join_kernel<T>, grid, dim3(256), 0, s, true, a);
 }
 

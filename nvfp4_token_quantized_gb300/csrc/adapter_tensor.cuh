@@ -84,6 +84,13 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   const bool issuer = warp == ADAPTER_WARPS;
   const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
 
+  // Of many adapters most numbers are unused, and leave before they take anything.
+  Piece p;
+  if (a.group_of) {
+    pdl_wait();
+    p = find_piece(a.starts, a.rows, a.groups, ADAPTER_TILE, number, &found);
+    if (p.group < 0) return;  // (the whole cluster)
+  }
   // (set up while the plan is made)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -106,8 +113,10 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at, ring_at = smem_u32(ring), panels_at = smem_u32(panels);
-  pdl_wait();
-  const Piece p = find_piece(a.starts, a.groups, ADAPTER_TILE, number, &found);
+  if (!a.group_of) {
+    pdl_wait();
+    p = find_piece(a.starts, a.rows, a.groups, ADAPTER_TILE, number, &found);
+  }
   pdl_trigger();
   if (p.group < 0) {  // (the whole cluster)
     if (warp == 0) tmem_dealloc(tmem, SUMS * 64);

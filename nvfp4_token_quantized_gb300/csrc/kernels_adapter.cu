@@ -1,13 +1,14 @@
 // kernels_adapter.cu - low-rank adapters of many requests: rows grouped by their
 // adapter, and the launches of a forward and of the gradients.
 #include <algorithm>
+#include <type_traits>
 
 #include "adapter_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 1024, PLAN_CTAS = 304;  // (two an SM)
 constexpr unsigned ALL = 0xffffffffu;
 
 // Sixteen neighbouring ids, as groups (-1 from `rows` on).
@@ -28,101 +29,115 @@ __device__ __forceinline__ void load_groups(const int32_t* ids, int64_t first, i
 
 constexpr int MAX_WORDS = (65536 + 32) / 32 + 1;  // a bit for each adapter and for none
 
-// The adapter with rows (L: rows without one) that comes in place `index`, or -1:
-// all threads mark the adapters they meet, then count.
-__device__ __forceinline__ int present_group(const int32_t* ids, int rows, int L, int index) {
-  constexpr int PER = 16, ROUND = PLAN_THREADS * PER, EACH = (MAX_WORDS + PLAN_THREADS - 1) / PLAN_THREADS;
-  __shared__ unsigned marks[EACH * PLAN_THREADS];
-  __shared__ int sums[32], result;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < EACH * PLAN_THREADS; i += PLAN_THREADS) marks[i] = 0;
-  if (tid == 0) result = -1;
-  __syncthreads();
-  for (int64_t base = 0; base < rows; base += ROUND) {
-    int g[PER];
-    load_groups(ids, base + tid * PER, rows, L, g);
+// The adapters with rows (L: rows without one), numbered in ascending order: all
+// threads mark the adapters they meet, then count.
+struct Present {
+  static constexpr int EACH = (MAX_WORDS + PLAN_THREADS - 1) / PLAN_THREADS;
+  unsigned marks[EACH * PLAN_THREADS];
+  int sums[32], result;
+  // Returns the number of those before this thread's words, and of all.
+  __device__ __forceinline__ int2 mark(const int32_t* ids, int rows, int L) {
+    constexpr int PER = 16, ROUND = PLAN_THREADS * PER;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < EACH * PLAN_THREADS; i += PLAN_THREADS) marks[i] = 0;
+    __syncthreads();
+    for (int64_t base = 0; base < rows; base += ROUND) {
+      int g[PER];
+      load_groups(ids, base + tid * PER, rows, L, g);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (g[i] >= 0 && !(*(volatile unsigned*)&marks[g[i] >> 5] >> (g[i] & 31) & 1)) atomicOr(&marks[g[i] >> 5], 1u << (g[i] & 31));
-  }
-  __syncthreads();
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) mine += __popc(marks[tid * EACH + i]);
-  int upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(ALL, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  const int w = sums[lane];
-  int before = __reduce_add_sync(ALL, lane < warp ? w : 0) + upto - mine;
-  if (index >= before && index < before + mine) {
-    for (int i = 0; i < EACH; ++i) {
-      unsigned m = marks[tid * EACH + i];
-      for (; m; m &= m - 1)
-        if (before++ == index) result = (tid * EACH + i) * 32 + __ffs(m) - 1;
+      for (int i = 0; i < PER; ++i)
+        if (g[i] >= 0 && !(*(volatile unsigned*)&marks[g[i] >> 5] >> (g[i] & 31) & 1)) atomicOr(&marks[g[i] >> 5], 1u << (g[i] & 31));
     }
+    __syncthreads();
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) mine += __popc(marks[tid * EACH + i]);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(ALL, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    const int w = sums[lane];
+    return make_int2(__reduce_add_sync(ALL, lane < warp ? w : 0) + upto - mine, __reduce_add_sync(ALL, w));
   }
-  __syncthreads();
-  return result;
-}
+  // The one of a number that there is.
+  __device__ __forceinline__ int pick(int before, int number) {
+    const int tid = threadIdx.x;
+    for (int i = 0; i < EACH; ++i)
+      for (unsigned m = marks[tid * EACH + i]; m; m &= m - 1)
+        if (before++ == number) result = (tid * EACH + i) * 32 + __ffs(m) - 1;
+    __syncthreads();
+    return result;  // (another is written behind the next barrier only)
+  }
+};
 
-// Group blockIdx.x: its first place, the number of rows of the groups before it,
-// and its rows in ascending order.  Every CTA goes through all ids, 16 a thread and
-// round (up to 16384 rows, once): no CTA waits for another.  (16384 rows: 4 us; the
-// kernel behind is set up meanwhile.)  group_of: only groups with rows.
-__global__ void __launch_bounds__(PLAN_THREADS) adapter_plan_kernel(const int32_t* ids, int rows, int L,
+// A group's first place, the number of rows of the groups before it, and its rows in
+// ascending order.  Every CTA goes through all ids, 16 a thread and round (up to
+// 16384 rows, once): no CTA waits for another.  (16384 rows: 4 us; the kernel behind
+// is set up meanwhile.)  COMPACT: only groups with rows, a CTA every so many (4096
+// rows of 64 adapters in a set of 4000: the forward in 54 us, with a CTA a group 91).
+template <bool COMPACT>
+__global__ void __launch_bounds__(PLAN_THREADS, 2) adapter_plan_kernel(const int32_t* ids, int rows, int L, int groups,
                                                                     int32_t* starts, int32_t* row_list,
                                                                     int32_t* group_of) {
   constexpr int PER = 16, ROUND = PLAN_THREADS * PER;
   __shared__ int less_sum[32], warp_sum[32];
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = group_of ? present_group(ids, rows, L, blockIdx.x) : blockIdx.x;
-  if (tid == 0 && blockIdx.x == gridDim.x - 1) starts[gridDim.x] = rows;
-  if (tid == 0 && group_of) group_of[blockIdx.x] = group;
-  if (group < 0 || rows == 0) {
-    if (tid == 0) starts[blockIdx.x] = rows;
-    return;
-  }
-  int g[PER], less = 0;
-  for (int64_t base = 0; base < rows; base += ROUND) {
-    load_groups(ids, base + tid * PER, rows, L, g);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) less += (unsigned)g[i] < (unsigned)group;
-  }
-  less = __reduce_add_sync(ALL, less);
-  if (lane == 0) less_sum[warp] = less;
-  int at = 0;
-  for (int64_t base = 0; base < rows; base += ROUND) {
-    if (rows > ROUND) load_groups(ids, base + tid * PER, rows, L, g);  // (else they are still here)
-    unsigned mine = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) mine |= (unsigned)(g[i] == group) << i;
-    const int n = __popc(mine);
-    int upto = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(ALL, upto, o);
-      if (lane >= o) upto += v;
+  if (tid == 0 && blockIdx.x == 0) starts[groups] = rows;
+  int2 present = make_int2(0, groups);
+  __shared__ std::conditional_t<COMPACT, Present, int> of;
+  if constexpr (COMPACT) present = of.mark(ids, rows, L);
+  for (int number = blockIdx.x; number < groups; number += gridDim.x) {
+    const bool none = rows == 0 || number >= present.y;
+    int group = none ? -1 : number;
+    if constexpr (COMPACT) {
+      if (!none) group = of.pick(present.x, number);
+      if (tid == 0) group_of[number] = group;
     }
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    if (base == 0) at = __reduce_add_sync(ALL, less_sum[lane]);
-    if (base == 0 && tid == 0) starts[blockIdx.x] = at;
-    const int w = warp_sum[lane];
-    const int before = __reduce_add_sync(ALL, lane < warp ? w : 0), all = __reduce_add_sync(ALL, w);
-    int put = at + before + upto - n;
-    const int32_t first = (int32_t)(base + tid * PER);
-    while (mine) {
-      row_list[put++] = first + __ffs(mine) - 1;
-      mine &= mine - 1;
+    if (none) {
+      if (tid == 0) starts[number] = rows;
+      continue;
     }
-    at += all;
-    __syncthreads();  // (the next round overwrites the warps' sums)
+    int g[PER], less = 0;
+    for (int64_t base = 0; base < rows; base += ROUND) {
+      load_groups(ids, base + tid * PER, rows, L, g);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) less += (unsigned)g[i] < (unsigned)group;
+    }
+    less = __reduce_add_sync(ALL, less);
+    if (lane == 0) less_sum[warp] = less;
+    int at = 0;
+    for (int64_t base = 0; base < rows; base += ROUND) {
+      if (rows > ROUND) load_groups(ids, base + tid * PER, rows, L, g);  // (else they are still here)
+      unsigned mine = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) mine |= (unsigned)(g[i] == group) << i;
+      const int n = __popc(mine);
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(ALL, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      if (base == 0) at = __reduce_add_sync(ALL, less_sum[lane]);
+      if (base == 0 && tid == 0) starts[number] = at;
+      const int w = warp_sum[lane];
+      const int before = __reduce_add_sync(ALL, lane < warp ? w : 0), all = __reduce_add_sync(ALL, w);
+      int put = at + before + upto - n;
+      const int32_t first = (int32_t)(base + tid * PER);
+      while (mine) {
+        row_list[put++] = first + __ffs(mine) - 1;
+        mine &= mine - 1;
+      }
+      at += all;
+      __syncthreads();  // (the next round overwrites the warps' sums)
+    }
   }
 }
 
@@ -134,8 +149,8 @@ struct Layout {
 };
 
 // Groups of a call.  Of few adapters each is one, with rows or without; of more only
-// as many as rows can have: a CTA of the plan and a tile's number each, for a search
-// of 4 us (300 rows: 64 adapters 32 and 36 us, 256 52 and 55, 1000 91 and 51).
+// as many as rows can have: a tile's number each, for a search of 4 us (300 rows: 64
+// adapters 32 and 36 us, 256 52 and 55, 1000 91 and 51, before clusters of two).
 constexpr int FEW_GROUPS = 256;
 bool few_groups(int L) { return L < FEW_GROUPS; }
 int groups_of(int64_t rows, int L) { return (int)(few_groups(L) ? L + 1 : std::min<int64_t>(L + 1, std::max<int64_t>(rows, 1))); }
@@ -170,9 +185,11 @@ Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
 }
 
 cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
-  return launch_k(adapter_plan_kernel, dim3((unsigned)a.groups), dim3(PLAN_THREADS), 0, s, false, a.ids, (int)a.rows,
-                  a.L, const_cast<int32_t*>(a.starts), const_cast<int32_t*>(a.row_list),
-                  const_cast<int32_t*>(a.group_of));
+  const bool compact = a.group_of != nullptr;
+  const unsigned grid = (unsigned)(compact ? std::min(a.groups, PLAN_CTAS) : a.groups);
+  return launch_k(compact ? adapter_plan_kernel<true> : adapter_plan_kernel<false>, dim3(grid), dim3(PLAN_THREADS), 0, s,
+                  false, a.ids, (int)a.rows, a.L, a.groups, const_cast<int32_t*>(a.starts),
+                  const_cast<int32_t*>(a.row_list), const_cast<int32_t*>(a.group_of));
 }
 
 // CTAs of a cluster: as many as keep the likely tiles within one wave of two
