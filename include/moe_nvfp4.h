@@ -675,8 +675,8 @@ typedef struct {
 } moe_adapter_io;
 
 /* Device bytes of a forward's (backward 0) or a gradient's workspace; 0 for a
- * forward of up to 128 rows (workspace may then be NULL) and for a refused cfg
- * or number of rows. */
+ * forward of few rows (up to 256, of some configurations up to 512: workspace may
+ * then be NULL) and for a refused cfg or number of rows. */
 MOE_API size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int64_t rows, int backward);
 
 /* out may be base (same stride); other overlaps of an output with another

@@ -14,7 +14,7 @@ from .binding import (MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_OK, MoEError, load_libr
 from .operators import _OnStream, _current, _device, _empty_strided, _new_rows, _new_vector, _rows, _vector
 
 # (forwards of so few rows need no workspace: not asked for, a call less)
-_FEW_ROWS = 128
+_FEW_ROWS = 256
 _HALVES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 
@@ -69,6 +69,8 @@ class LowRankAdapters:
         if T <= _FEW_ROWS and not backward:
             return None, None
         need = int(self._lib.moe_adapter_workspace_bytes(cfg, T, backward))
+        if need == 0:
+            return None, None
         if workspace is None:
             workspace = _new_vector(need, torch.uint8)
         elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:

@@ -1,8 +1,11 @@
-// adapter_apply.cuh - rows through their adapters, up to 128 of them (a decode step):
+// adapter_apply.cuh - rows through their adapters, a few hundred at most (a decode
+// step's):
 // hidden = scale x down^T, out = base + hidden up, in one launch.
 //
-// Bound by the adapters' bytes and by latency.  A cluster takes the rows of one
-// adapter, which its CTAs find in ids themselves; the CTAs split the first
+// Bound by the adapters' bytes and by latency.  A cluster takes up to 32 rows of one
+// adapter, which its CTAs find in ids themselves (more rows a tile would read the
+// factors less often, but leave CTAs idle: 128 rows of one adapter, rank 64, 4096
+// wide, 20 us, in one tile of 128 rows 46); the CTAs split the first
 // product's long axis, add their parts through distributed shared memory, and
 // split the second product's columns, so that few rows still spread over the GPU.
 // Within a CTA a warp has 16 rows; fewer rows leave more warps for the split.  The
@@ -25,10 +28,10 @@ namespace cg = cooperative_groups;
 template <int NT>
 struct ApplyShared {
   static constexpr int R = 8 * NT, RP = hidden_pitch(R), KS = (NT + 1) / 2;
-  static constexpr int PART = ADAPTER_TILE * RP * 4;                        // sums, then fragments
-  static constexpr int FRAGS = (ADAPTER_TILE / 16) * KS * 2 * 512;
+  static constexpr int PART = ADAPTER_WARPS * 16 * RP * 4;                  // sums, then fragments
+  static constexpr int FRAGS = (APPLY_TILE / 16) * KS * 2 * 512;
   static constexpr int FIRST = PART > FRAGS ? PART : FRAGS;
-  static constexpr int BYTES = FIRST + PART;
+  static constexpr int BYTES = FIRST + APPLY_TILE * RP * 4;
 };
 
 template <typename T, int NT, bool VEC>
@@ -39,30 +42,42 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   float* part = reinterpret_cast<float*>(smem);
   uint4* frags = reinterpret_cast<uint4*>(smem);
   float* hid = reinterpret_cast<float*>(smem + S::FIRST);
-  __shared__ int row_of[ADAPTER_TILE];
-  __shared__ int counts[4];  // of the warps that hold a row
+  __shared__ int row_of[APPLY_TILE];
+  __shared__ int counts[FEW_ROWS / 32], place;  // the group's rows among 32 each; of row `number`
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int C = a.cluster, crank = blockIdx.x % C, number = blockIdx.x / C;
 
   // ---- the group's rows, found in ids ----
-  // Of more adapters than rows a cluster stands for a row, and takes its adapter
-  // if no row before has the same.
-  const bool by_row = a.L + 1 > a.rows;
-  const int group = by_row ? adapter_key(a.ids[number], a.L) : number;
-  const bool mine = tid < a.rows && adapter_key(a.ids[tid], a.L) == group;
-  const unsigned m = __ballot_sync(0xffffffffu, mine);
-  if (warp < 4 && lane == 0) counts[warp] = __popc(m);
-  __syncthreads();
-  int before = 0, count = 0;
+  // A cluster stands for a tile that an adapter's rows may fill, or, where there are
+  // more of those than rows, for a row, and takes a tile if that row is its first.
+  const bool by_row = a.tiles == a.rows;
+  const int group = by_row ? adapter_key(a.ids[number], a.L) : number / a.subs;
+  constexpr int PASSES = FEW_ROWS / ADAPTER_THREADS;
+  int at[PASSES];  // places of this thread's rows among the group's, -1: another's
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    before += w < warp ? counts[w] : 0;
-    count += counts[w];
+  for (int i = 0; i < PASSES; ++i) {
+    const int row = tid + i * ADAPTER_THREADS;
+    const bool mine = row < a.rows && adapter_key(a.ids[row], a.L) == group;
+    const unsigned m = __ballot_sync(0xffffffffu, mine);
+    at[i] = mine ? __popc(m & ((1u << lane) - 1)) : -1;
+    if (lane == 0) counts[warp + i * ADAPTER_WARPS] = __popc(m);
   }
-  if (mine) row_of[before + __popc(m & ((1u << lane) - 1))] = tid;
-  if (count == 0) return;  // (the whole cluster)
   __syncthreads();
-  if (by_row && row_of[0] != number) return;
+  const int n = lane < FEW_ROWS / 32 ? counts[lane] : 0, total = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp + i * ADAPTER_WARPS ? n : 0);
+    if (at[i] >= 0) at[i] += before;
+    if (by_row && tid + i * ADAPTER_THREADS == number) place = at[i];
+  }
+  if (total == 0) return;  // (the whole cluster)
+  __syncthreads();
+  const int begin = by_row ? place : number % a.subs * APPLY_TILE, count = min(APPLY_TILE, total - begin);
+  if (count <= 0 || begin % APPLY_TILE != 0) return;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i)
+    if (at[i] >= begin && at[i] < begin + count) row_of[at[i] - begin] = tid + i * ADAPTER_THREADS;
+  __syncthreads();
 
   const T* x = static_cast<const T*>(a.x);
   const T* base = static_cast<const T*>(a.base);
@@ -75,7 +90,7 @@ __global__ void __launch_bounds__(ADAPTER_THREADS, NT <= 8 ? 2 : 1) adapter_appl
   }
 
   // warps: wm groups of 16 rows, the rest splits the long axes
-  const int wm = count <= 16 ? 1 : count <= 32 ? 2 : count <= 64 ? 4 : 8;
+  const int wm = count <= 16 ? 1 : 2;
   const int ways = ADAPTER_WARPS / wm, rg = warp & (wm - 1), way = warp / wm;
   const int r0 = rg * 16 + g, r1 = r0 + 8;
   const bool on0 = r0 < count, on1 = r1 < count;

@@ -25,6 +25,8 @@ namespace moe {
 constexpr int ADAPTER_THREADS = 256;
 constexpr int ADAPTER_WARPS = ADAPTER_THREADS / 32;
 constexpr int ADAPTER_TILE = 128;  // rows of a tile: 16 a warp
+constexpr int FEW_ROWS = 512;      // most rows of a forward in one launch
+constexpr int APPLY_TILE = 32;     // rows of its clusters
 constexpr int GRADIENT_ROWS = 32;  // rows of a stage of the factors' gradients
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1, __nv_bfloat16) {

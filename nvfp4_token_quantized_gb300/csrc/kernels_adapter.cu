@@ -149,8 +149,8 @@ struct Layout {
 };
 
 // Groups of a call.  Of few adapters each is one, with rows or without; of more only
-// as many as rows can have: a tile's number each, for a search of 4 us (300 rows: 64
-// adapters 32 and 36 us, 256 52 and 55, 1000 91 and 51, before clusters of two).
+// as many as rows can have: a tile's number each, for a search of 4 us (300 rows,
+// planned: 64 adapters 32 and 36 us, 256 52 and 55, 1000 91 and 51).
 constexpr int FEW_GROUPS = 256;
 bool few_groups(int L) { return L < FEW_GROUPS; }
 int groups_of(int64_t rows, int L) { return (int)(few_groups(L) ? L + 1 : std::min<int64_t>(L + 1, std::max<int64_t>(rows, 1))); }
@@ -196,8 +196,8 @@ cudaError_t launch_plan(const AdapterArgs& a, cudaStream_t s) {
 // CTAs an SM.  Which adapters have rows is known on the device only: half of
 // their last tiles count, and a quarter for the step from one CTA to two (a CTA
 // alone takes all of both long axes).  16384 rows, rank 64: two 89 us, one 108,
-// four 122; 4096 rows, rank 16: eight 31, four 39; 512 rows, rank 16, of 1, 8,
-// 64 and all of 300 adapters: two 41, 37, 35 and 60 us, one 63, 55, 48 and 52.
+// four 122; 4096 rows, rank 16: eight 31, four 39; 2048 rows, rank 16, of 1, 8,
+// 64 and all of 300 adapters: two 42, 42, 38 and 61 us, one 63, 63, 50 and 54.
 int cluster_of(int64_t tiles, int64_t rows, int L) {
   const auto likely = [&](int share) {
     const int64_t full = (rows + ADAPTER_TILE - 1) / ADAPTER_TILE + std::min<int64_t>(L, rows) / share;
@@ -206,17 +206,34 @@ int cluster_of(int64_t tiles, int64_t rows, int L) {
   return likely(2) * 8 <= 304 ? 8 : likely(2) * 4 <= 304 ? 4 : likely(4) * 2 <= 304 ? 2 : 1;
 }
 
+// Whether a forward is one launch without a plan.  Above 256 rows the tensor cores'
+// path is the faster one where few adapters of higher ranks share the rows.  (160
+// rows of 1, 8, 64 and 160 adapters in a set of 300, rank 16, 2048 wide: 16, 16, 14
+// and 20 us, planned 35, 33, 35 and 39; 512 rows of 1, 8, 64 and 512: 20, 20, 20 and
+// 34, planned 36, 36, 34 and 63.  512 rows, rank 64, 4096 wide, of 8 adapters in a
+// set of 8 37 and 28, in one of 64 36 and 34, of all 64 36 and 52.)
+bool few_rows(const moe_adapter_config& c, int64_t rows) {
+  return rows <= FEW_ROWS / 2 || (rows <= FEW_ROWS && (c.rank <= 32 || c.num_adapters > 32));
+}
+
 cudaError_t apply(AdapterArgs a, bool f16, bool vec, bool planned, cudaStream_t s) {
-  a.tiles = planned ? pieces_of(a.rows, a.groups, ADAPTER_TILE) : std::min<int64_t>(a.L + 1, a.rows);
-  a.cluster = cluster_of(a.tiles, a.rows, a.L);
-  if (planned) return f16 ? launch_tensor_f16(a, vec, s) : launch_tensor_bf16(a, vec, s);
+  if (planned) {
+    a.tiles = pieces_of(a.rows, a.groups, ADAPTER_TILE);
+    a.cluster = cluster_of(a.tiles, a.rows, a.L);
+    return f16 ? launch_tensor_f16(a, vec, s) : launch_tensor_bf16(a, vec, s);
+  }
+  a.subs = (int)((a.rows + APPLY_TILE - 1) / APPLY_TILE);
+  a.tiles = std::min<int64_t>((a.L + 1) * (int64_t)a.subs, a.rows);
+  // (of more rows four, whoever has them: 300 rows, rank 64, of one adapter, 4096
+  // wide, four 29 us, two 44, eight 27; of 300 adapters, 2048 wide, 43, 45 and 56)
+  a.cluster = a.rows <= ADAPTER_TILE ? cluster_of(a.tiles, a.rows, a.L) : 4;
   return f16 ? launch_apply_f16(a, vec, s) : launch_apply_bf16(a, vec, s);
 }
 
 }  // namespace
 
 size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward) {
-  if (!backward && rows <= ADAPTER_TILE) return 0;
+  if (!backward && few_rows(c, rows)) return 0;
   return (size_t)layout(c, rows, backward).end * 4;
 }
 
@@ -227,7 +244,7 @@ cudaError_t launch_adapter(AdapterArgs a, const moe_adapter_config& c, bool vec,
   a.row_list = w + l.row_list;
   a.groups = groups_of(a.rows, a.L);
   a.group_of = few_groups(a.L) ? nullptr : w + l.group_of;
-  const bool planned = a.rows > ADAPTER_TILE;
+  const bool planned = !few_rows(c, a.rows);
   if (planned) {
     const cudaError_t e = launch_plan(a, s);
     if (e != cudaSuccess) return e;

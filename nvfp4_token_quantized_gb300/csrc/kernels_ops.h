@@ -146,6 +146,7 @@ struct AdapterArgs {
   const int32_t* group_of;  // groups' adapters; NULL: group a is adapter a
   int groups;
   int64_t tiles;
+  int subs;                 // tiles that a group may have (few rows)
   int cluster;
 };
 

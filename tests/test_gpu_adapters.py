@@ -123,9 +123,10 @@ def _check(T, K, N, r, L, dtype=BF16, base=True, scales=True, backward=True, arr
 def test_ranks(r, dtype):
     _check(40, 256, 320, r, 3, dtype)
     _check(333, 264, 136, r, 4, dtype)
+    _check(600, 264, 136, r, 4, dtype, backward=False)
 
 
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 33, 64, 65, 127, 128, 129, 300, 1000])
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 33, 64, 65, 127, 128, 129, 256, 257, 300, 512, 513, 1000])
 def test_lengths(T):
     for L in (1, 5, 40):
         _check(T, 512, 256, 16, L)
@@ -137,6 +138,7 @@ def test_lengths(T):
 def test_widths(K, N, dtype):
     _check(50, K, N, 8, 3, dtype)
     _check(200, K, N, 20, 3, dtype)
+    _check(520, K, N, 20, 3, dtype, backward=False)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -144,6 +146,8 @@ def test_strides(dtype):
     for pad in (1, 3, 8, 64):
         _check(77, 128, 192, 16, 4, dtype, pad=pad)
         _check(200, 129, 192, 16, 4, dtype, pad=pad)
+        _check(520, 129, 192, 16, 4, dtype, pad=pad, backward=False)
+        _check(530, 128, 192, 16, 4, dtype, pad=pad, backward=False)
 
 
 def test_operands_that_may_be_absent():
@@ -151,6 +155,7 @@ def test_operands_that_may_be_absent():
         for scales in (False, True):
             _check(60, 256, 256, 16, 4, base=base, scales=scales)
             _check(260, 256, 256, 16, 4, F16, base=base, scales=scales)
+            _check(530, 256, 256, 16, 4, F16, base=base, scales=scales, backward=False)
 
 
 def test_who_has_which_adapter():
@@ -161,6 +166,9 @@ def test_who_has_which_adapter():
                 torch.arange(T) - 300):
         _check(T, 256, 128, 16, 6, ids=ids)
         _check(90, 256, 128, 16, 6, F16, ids=ids[:90])
+        for n in (48, 129, 300, 500):  # (tiles of one adapter, beside those that it does not fill)
+            for L in (6, 300):
+                _check(n, 256, 128, 16, L, ids=ids[:n], backward=False)
     _check(300, 64, 64, 4, 1000)  # more adapters than rows
 
 
@@ -187,11 +195,11 @@ def test_no_rows():
 def test_hidden_past_the_types_range(dtype):
     """Large rows and factors: hidden near the end of FP16's range and far
     beyond it; and tiny ones."""
-    for size in (30.0, 200.0):
-        a = _make(50, 256, 128, 16, 2, dtype, size=size)
+    for T, size in ((50, 30.0), (600, 200.0), (50, 200.0)):
+        a = _make(T, 256, 128, 16, 2, dtype, size=size)
         a["down"] = (a["down"].float() * 300).to(dtype)
         a["up"] = (a["up"].float() * 1e-3).to(dtype)
-        _, _, _, hidden = _check(50, 256, 128, 16, 2, dtype, arrays=a)
+        _, _, _, hidden = _check(T, 256, 128, 16, 2, dtype, arrays=a)
     assert hidden.abs().max() > 1e5
     a = _make(300, 256, 128, 16, 2, dtype, size=1e-3)
     a["down"] = (a["down"].float() * 1e-2).to(dtype)
@@ -202,7 +210,7 @@ def test_hidden_past_the_types_range(dtype):
 def test_rows_do_not_mix():
     """Values that are no numbers stay in their row and, for the factors'
     gradients, their adapter."""
-    for T in (60, 400):
+    for T in (60, 400, 700):
         ad, a, out, hidden = _check(T, 256, 128, 16, 4, ids=torch.arange(T) % 5 - 1)
         bad = a["x"].clone()
         row = 7
@@ -224,7 +232,7 @@ def test_rows_do_not_mix():
 
 
 def test_in_place_and_repeated():
-    for T, dtype in ((50, BF16), (900, F16)):
+    for T, dtype in ((50, BF16), (300, BF16), (900, F16)):
         ad, a, out, hidden = _check(T, 256, 256, 16, 4, dtype)
         for _ in range(2):
             again, h2 = ad.forward(a["x"], a["ids"], a["down"], a["up"], scales=a["scales"], base=a["base"],
@@ -248,7 +256,7 @@ def test_rows_behind_the_batch_are_left():
 
 
 def test_captured_and_on_another_stream():
-    for T in (64, 1000):
+    for T in (64, 300, 1000):
         ad, a, out, hidden = _check(T, 256, 192, 16, 4)
         want = ad.backward(a["dout"], a["x"], hidden, a["ids"], a["down"], a["up"], scales=a["scales"])
         side = torch.cuda.Stream()
@@ -294,7 +302,7 @@ def test_refusals():
         _adapters(64, 96, 129)
     with pytest.raises(RuntimeError):
         _adapters(0, 96, 8)
-    b = _make(140, 64, 96, 8, 2, BF16)
+    b = _make(600, 64, 96, 8, 2, BF16)
     with pytest.raises(ValueError, match="workspace"):
         ad.forward(b["x"], b["ids"], b["down"], b["up"], workspace=torch.zeros(2, device="cuda"))
     _, h = ad.forward(**ok, keep_hidden=True)

@@ -113,7 +113,7 @@ def test_values_beyond_the_sets_adapters():
     ad = _lib().LowRankAdapters(64, 64, 4)
     g = torch.Generator().manual_seed(3)
     down, up = (torch.randn(2, 4, 64, generator=g).to(F16).cuda() for _ in range(2))
-    for T in (8, 300):
+    for T in (8, 300, 600):
         x = torch.randn(T, 64, generator=g).to(F16).cuda()
         ids = torch.tensor([-1, 2, -(1 << 31), (1 << 31) - 1] * (T // 4), dtype=torch.int32, device="cuda")
         out, h = ad.forward(x, ids, down, up, base=x.clone(), keep_hidden=True)
@@ -127,7 +127,7 @@ def test_an_infinite_row_is_the_formulas(dtype):
     ad = _lib().LowRankAdapters(72, 80, 1)
     g = torch.Generator().manual_seed(5)
     down, up = torch.randn(2, 1, 72, generator=g).to(dtype).cuda(), torch.randn(2, 1, 80, generator=g).to(dtype).cuda()
-    for T in (8, 300):
+    for T in (8, 300, 600):
         x = torch.randn(T, 72, generator=g).to(dtype).cuda()
         ids = (torch.arange(T, device="cuda") % 2).int()
         want, _ = ad.forward(x, ids, down, up)

@@ -163,7 +163,7 @@ def test_adapter_configurations(lib, kw, status):
 def test_adapter_operands(lib):
     from nvfp4_token_quantized_gb300.binding import moe_adapter_io
 
-    def call(rows=200, **kw):
+    def call(rows=600, **kw):
         d = dict(x=MB, base=2 * MB, down=3 * MB, up=4 * MB, ids=5 * MB, scales=6 * MB, out=7 * MB, hidden=8 * MB,
                  workspace=9 * MB, x_stride=64, base_stride=96, out_stride=96)
         d.update(kw)
