@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) adapter_plan_kernel(const int
   __shared__ std::conditional_t<COMPACT, Present, int> of;
   if constexpr (COMPACT) present = of.mark(ids, rows, L);
   for (int number = blockIdx.x; number < groups; number += gridDim.x) {
-    const bool none = rows == 0 || number >= present.y;
+    const bool none = rows == 0 || (COMPACT && number >= present.y);
     int group = none ? -1 : number;
     if constexpr (COMPACT) {
       if (!none) group = of.pick(present.x, number);
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) adapter_plan_kernel(const int
       at += all;
       __syncthreads();  // (the next round overwrites the warps' sums)
     }
+    if constexpr (!COMPACT) return;  // (a CTA a group)
   }
 }
 
