@@ -648,7 +648,10 @@ MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, 
  *   down: [num_adapters, rank, in_features], up: [num_adapters, rank,
  *   out_features], contiguous, of `dtype` (bf16 or FP16) as x, base and out.
  * Adapters of lower rank than the set's have rows of zeros.  Sums are FP32;
- * hidden keeps 16 bits or more between the products; out is rounded once.
+ * hidden keeps 16 bits or more between the products; out is rounded once.  With
+ * FP16 those are bits of a value down to 2^-22 of the largest that it shares a
+ * power of two with, and 2^-39 of that largest below: a row's ranks in out and
+ * dx, in the factors' gradients one rank's hidden in up to 1024 rows.
  * Values that are no finite numbers stay in their row and adapter; an infinite
  * element of the second factor, or of x in the factors' gradients, may give NaN
  * where the formula gives an infinity (hidden's parts meet it one by one).

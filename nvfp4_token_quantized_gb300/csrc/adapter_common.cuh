@@ -88,16 +88,16 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = pack2(isinf(h.x) ? 0.0f : a - h.x, isinf(h.y) ? 0.0f : b - h.y, T());
 }
 
-// 2^-e and 2^e for values up to m in size, e the exponent of m: FP16 fragments
-// of scaled values neither overflow nor lose small ones.  1 for 0, infinity and
-// NaN.
+// The power of two that brings values up to m in size to 2^14 .. 2^15, and (back) its
+// inverse: FP16 parts of scaled values do not overflow, and split2's, whose last bit
+// is 2^-24 at least, keep 16 bits down to 2^-22 of m and to 2^-39 of m what is
+// smaller.  (Products and sums are FP32: 2^15 leaves room for any 16-bit factor.)
+// Both are normal numbers; an infinite m counts as the largest finite one.
 __device__ __forceinline__ float exponent_scale(float m, float& back) {
-  const int e = (int)(__float_as_uint(m) >> 23);  // m >= 0
-  const bool plain = e == 0 || e == 255;
-  // (2^-e of a biased exponent e is 254 - e: kept a normal number)
-  const int b = plain ? 127 : min(max(e, 1), 253);
-  back = __uint_as_float((uint32_t)b << 23);
-  return __uint_as_float((uint32_t)(254 - b) << 23);
+  const int e = min((int)(__float_as_uint(m) >> 23), 254);  // m >= 0
+  const int b = min(127 + 14 - (e - 127), 253);             // (at least 14)
+  back = __uint_as_float((uint32_t)(254 - b) << 23);
+  return __uint_as_float((uint32_t)b << 23);
 }
 
 // ---- rows by adapter ----

@@ -6,8 +6,10 @@
 // layout of operands whose contraction runs across rows.  x's rows come by
 // asynchronous copies of 512 bytes a row.  hidden is first split into its two
 // 16-bit parts, by a kernel that writes them in the order and swizzle in which the
-// tensor cores read them, once for all columns.  With FP16 the parts of a piece
-// share a power of two.
+// tensor cores read them, once for all columns.  With FP16 the parts of one rank in a
+// piece share a power of two: a rank's sums are a column of D of their own, so ranks
+// of any size beside each other keep their bits.  (The search for the largest value
+// of each rank: 16 us of 144 at 16384 rows of 32 ranks, under 1 of 20 at 777 of 8.)
 //
 // Rows that do not start on 16 bytes come as in adapter_tensor.cuh.  The CTAs' FP32
 // sums are joined by a last kernel in the order of the rows.
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
   using S = GradientShared<R>;
   constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
   __shared__ Piece found;
-  __shared__ float warp_max[8];
+  __shared__ float some_max[SCALED ? 256 : 1], scale_of[SCALED ? R : 1];
   const int tid = threadIdx.x, side = blockIdx.y;
   pdl_wait();
   pdl_trigger();
@@ -74,24 +76,34 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r < p.count && lane8 * 8 + i < a.rank ? h[lane8 * 8 + i] : 0.0f;
   };
-  float s = 1.0f;
-  if constexpr (SCALED) {
-    float m = 0.0f, back;
-    for (int r = tid / G; r < p.count; r += 256 / G) {
-      float v[8];
-      load(r, v);
+  if constexpr (SCALED) {  // the largest value of each rank
+    const int rank = tid % R;
+    float m = 0.0f;
+    if (rank < a.rank) {
+      constexpr int U = 8, STEP = 256 / R;  // rows whose loads are in flight together
+      for (int r = tid / R; r < p.count; r += U * STEP) {
+        float v[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+        for (int u = 0; u < U; ++u)
+          v[u] = r + u * STEP < p.count ? hidden[(int64_t)rows[r + u * STEP] * a.rank + rank] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) m = fmaxf(m, fabsf(v[u]));
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) warp_max[tid >> 5] = m;
+    some_max[tid] = m;
     __syncthreads();
+    if (tid < R) {
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
-    s = exponent_scale(m, back);
-    if (tid == 0 && blockIdx.z == 0) a.back[side][blockIdx.x] = back;
+      for (int w = R; w < 256; w += R) m = fmaxf(m, some_max[w + tid]);
+      float back;
+      scale_of[tid] = exponent_scale(m, back);
+      if (blockIdx.z == 0 && tid < a.rank) a.back[side][(int64_t)blockIdx.x * a.rank + tid] = back;
+    }
+    __syncthreads();
   }
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = SCALED ? scale_of[lane8 * 8 + i] : 1.0f;
   const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
   unsigned char* to = a.parts[side] + first_stage(p, a.unit) * S::HIDDEN;
   const int stop = min(stages * GRADIENT_ROWS, (int)(blockIdx.z + 1) * SPLIT_ROWS);
@@ -99,10 +111,10 @@ __global__ void __launch_bounds__(256) adapter_split_kernel(const OuterArgs a) {
     float v[8];
     load(r, v);
     uint4 hi, lo;
-    split2<T>(v[0] * s, v[1] * s, hi.x, lo.x);
-    split2<T>(v[2] * s, v[3] * s, hi.y, lo.y);
-    split2<T>(v[4] * s, v[5] * s, hi.z, lo.z);
-    split2<T>(v[6] * s, v[7] * s, hi.w, lo.w);
+    split2<T>(v[0] * s[0], v[1] * s[1], hi.x, lo.x);
+    split2<T>(v[2] * s[2], v[3] * s[3], hi.y, lo.y);
+    split2<T>(v[4] * s[4], v[5] * s[5], hi.z, lo.z);
+    split2<T>(v[6] * s[6], v[7] * s[7], hi.w, lo.w);
     unsigned char* stage = to + (int64_t)(r / GRADIENT_ROWS) * S::HIDDEN;
     const int row = r % GRADIENT_ROWS, ch = lane8, cl = G + lane8;
     *reinterpret_cast<uint4*>(stage + (ch >> 3) * S::PANEL + swizzled(row, ch & 7)) = hi;
@@ -114,6 +126,7 @@ template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(const OuterArgs a) {
   using S = GradientShared<R>;
   constexpr int ST = S::STAGES;
+  constexpr bool SCALED = !std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char raw[];
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   __shared__ Piece found;
@@ -121,6 +134,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   __shared__ int row_of[1024];
+  __shared__ float back_of[SCALED ? R : 1];  // the ranks' powers of two
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Piece p;
   if (a.group_of) {  // (as in adapter_tensor.cuh)
@@ -161,6 +175,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   const T* x = static_cast<const T*>(a.x[side]);
   const int64_t stride = a.stride[side];
   for (int r = tid; r < p.count; r += TENSOR_THREADS) row_of[r] = a.row_list[p.start + r];
+  if (SCALED && tid < a.rank) back_of[tid] = a.back[side][(int64_t)blockIdx.x * a.rank + tid];
   __syncthreads();
   const auto wait_alone = [&](uint64_t* bar, int parity) {  // (one lane)
     if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
@@ -249,7 +264,6 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   if (warp < ADAPTER_WARPS) {
     // A lane has a column of x, its ranks side by side in tensor memory.
     const int quarter = warp & 3, m = warp >> 2, c = n0 + m * 128 + quarter * 32 + lane;
-    const float back = std::is_same<T, __nv_bfloat16>::value ? 1.0f : a.back[side][blockIdx.x];
     const float lost = gave_up ? NAN : 0.0f;
     const int64_t n = (int64_t)a.rank * N;
     const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (r0 + i >= a.rank || c >= N) continue;
-        const float f = (R <= 32 ? v[i] + w[i] : v[i]) * back + lost;
+        const float f = (R <= 32 ? v[i] + w[i] : v[i]) * (SCALED ? back_of[r0 + i] : 1.0f) + lost;
         if (alone)
           grad[(int64_t)(r0 + i) * N] = from_f32<T>(f);
         else

@@ -177,7 +177,7 @@ Layout layout(const moe_adapter_config& c, int64_t rows, bool backward) {
   const int64_t part = stages * GRADIENT_ROWS * (c.rank <= 32 ? 1 : c.rank <= 64 ? 2 : 4) * 32;
   const int64_t sums = backward ? 2 * rows / unit + 1 : 0;
   l.back = l.hidden + (backward ? words16(rows * c.rank) : 0);
-  l.parts[0] = l.back + words16(2 * pieces);
+  l.parts[0] = l.back + words16(2 * pieces * c.rank);
   l.parts[1] = l.parts[0] + part;
   l.sums[0] = l.parts[1] + part;
   l.sums[1] = l.sums[0] + words16(sums * c.rank * c.in_features);
@@ -280,7 +280,7 @@ cudaError_t launch_adapter_backward(AdapterArgs a, OuterArgs o, const moe_adapte
   for (int i = 0; i < 2; ++i) {
     o.blocks[i] = (o.width[i] + 255) / 256;
     o.parts[i] = reinterpret_cast<unsigned char*>(w + l.parts[i]);
-    o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, o.groups, o.unit);
+    o.back[i] = reinterpret_cast<float*>(w + l.back) + i * pieces_of(a.rows, o.groups, o.unit) * a.rank;
   }
   return f16 ? launch_gradient_f16(o, vec, s) : launch_gradient_bf16(o, vec, s);
 }

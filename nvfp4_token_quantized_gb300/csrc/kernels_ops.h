@@ -162,7 +162,7 @@ struct OuterArgs {
   int groups;
   float* sums[2];
   unsigned char* parts[2];  // hidden split in two
-  float* back[2];           // and its scale, a piece each (FP16)
+  float* back[2];           // and its scales, one for each rank of a piece (FP16)
   int64_t rows;
   int L, rank, unit, blocks[2];
 };
