@@ -621,9 +621,11 @@ typedef struct {
 MOE_API size_t moe_gradient_workspace_bytes(void);
 
 /* norm (FP32 scalar on the device) = square root of the sum of the squares of
- * every element of every tensor.  Squares are summed in FP32 by runs and the
- * runs in FP64; where a run leaves FP32's range its squares are FP64 too, so
- * the norm is finite and exact to a few 2^-24 whenever it fits FP32.  It is
+ * every element of every tensor.  Squares are summed in FP32 by 64, these sums
+ * with what each addition rounds away, in FP32 over a CTA and in FP64 over the
+ * CTAs; where 64 squares leave FP32's range they are FP64 too, so the norm of any
+ * set is finite and exact to some 2^-24 whenever it fits FP32 (25 of them at most:
+ * half of what 64 squares' 33, a CTA's 13 and the root's 3 come to).  It is
  * infinite or NaN if an element is.  `out` is not used.  tensors is read
  * before the call returns. */
 MOE_API moe_status moe_gradient_norm(const moe_gradient* tensors, int64_t num, float* norm, void* workspace,

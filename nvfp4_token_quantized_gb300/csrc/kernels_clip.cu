@@ -171,16 +171,21 @@ struct Granules {
 
 // A thread's sum of squares: FP32 for chunks whose squares keep their bits
 // there, FP64 for the rest (some hundred times slower, so only where a sum of
-// 64 squares leaves [2^-90, 2^100]).
+// 64 squares leaves [2^-90, 2^100]).  What an FP32 addition of a chunk rounds away is
+// kept (Knuth's two-sum) and added at the end: a large set gives a thread hundreds of
+// chunks, whose roundings, of gradients alike, would all go one way (862 chunks: 66
+// units of 2^-24 in the norm).
 struct Squares {
-  float sum = 0.0f;
+  float sum = 0.0f, rest = 0.0f;
   double wide = 0.0;
   template <typename T>
   __device__ __forceinline__ void add(const Granules<T>& g) {
     const float s = g.squares();
-    if (s > 0x1p-90f && s < 0x1p100f)
-      sum += s;
-    else if (!g.zero()) {
+    if (s > 0x1p-90f && s < 0x1p100f) {
+      const float t = sum + s, from = t - sum;
+      rest += (sum - (t - from)) + (s - from);
+      sum = t;
+    } else if (!g.zero()) {
       uint4 q[GRANULES];
 #pragma unroll
       for (int j = 0; j < GRANULES; ++j) q[j] = g.q[j];
@@ -241,9 +246,11 @@ __device__ __forceinline__ V block_sum(V v, double* red) {
 }
 
 // The threads' sums: in FP32, which is four times as quick as FP64's shuffles
-// and slow adds, and FP64 only where a thread has some.
+// and slow adds (its 13 steps round the sum by 2^-24 each), what they rounded away
+// where a thread has several chunks, and FP64 only where a thread has some.
 __device__ __forceinline__ double block_squares(const Squares& s, double* red) {
   double t = block_sum(s.sum, red);
+  if (__syncthreads_or(s.rest != 0.0f)) t += (double)block_sum(s.rest, red);
   if (__syncthreads_or(s.wide != 0.0)) t += block_sum(s.wide, red);
   return t;
 }
