@@ -574,8 +574,9 @@ MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const moe
  *            num_sequences 1): all rows are one sequence;
  *   mask:    one byte a token, 0 for a token that is not counted; NULL: all
  *            are.  What such a token's logits hold, NaN too, reaches nothing.
- * Sums are FP32 over runs of a few hundred rows, joined in a fixed order: a
- * call repeats bit for bit. */
+ * Sums are FP32 over 512 rows at most and then over 32 of those; these are joined,
+ * in a fixed order, with what each addition rounds away, so the error does not
+ * grow with the batch.  A call repeats bit for bit. */
 typedef struct {
   const void* logits;
   const int32_t* topk_ids;

@@ -27,6 +27,13 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
+// sum += v; what that addition rounds away is added to rest (Knuth's two-sum).
+__device__ __forceinline__ void add_kept(float& sum, float& rest, float v) {
+  const float t = sum + v, from = t - sum;
+  rest += (sum - (t - from)) + (v - from);
+  sum = t;
+}
+
 // Two packed 16-bit values.
 __device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));

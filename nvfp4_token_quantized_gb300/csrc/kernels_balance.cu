@@ -5,7 +5,13 @@
 // The loss of a sequence of N tokens is coefficient * E / (K N^2) times the sum
 // over the experts of (times chosen) * (sum of p), so one pass over the logits
 // leaves E sums and E counts a run of rows, which a second, small kernel joins
-// in the order of the runs: no atomics on floats, the same bits every time.
+// in the order of the runs: no atomics on floats, the same bits every time.  The
+// roundings of tokens alike all go one way, so no FP32 chain grows with the batch: a
+// lane adds 32 rows at a time, a run is one such sum (128 experts and fewer) or up to
+// 32, a thread of the join keeps what each addition rounds away (add_kept), and the
+// threads' sums meet in a tree.  (1048576 rows FP32, runs of one sum or of more: 64
+// experts 87 and 103 us, 256 experts 188 and 167: few CTAs an SM gain by fewer starts,
+// many lose by the longer code.)
 //
 // Sixteen lanes share a row: four experts a lane and chunk, so that a row of
 // 256 takes four 16-byte loads a lane and two trees of four steps for a
@@ -33,6 +39,8 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int ROWS_AT_ONCE = 2 * WARPS;  // sixteen lanes a row
+constexpr int SUM_ROWS = 32 * ROWS_AT_ONCE;  // that a CTA adds before its lanes' sums are kept
+constexpr int LONG_RUNS = 2;             // of more than so many 64 experts: several such sums
 constexpr int JOIN = 8;                  // CTAs of a cluster that joins the runs' sums
 constexpr int JOIN_THREADS = 1024;       // of a CTA that joins all runs of a batch
 constexpr int OFFSETS = 1024;            // that a CTA keeps in shared memory
@@ -290,37 +298,44 @@ __device__ __forceinline__ void sum_run(const BalanceArgs& a, int64_t lo, int64_
   Part cur;
   int id[2];
   bool on = fetch(lo + warp * 2 + half, cur, id);
-  for (int64_t base = lo + warp * 2; base < hi; base += ROWS_AT_ONCE) {
-    Part nxt;
-    int nxt_id[2];
-    const bool nxt_on = fetch(base + ROWS_AT_ONCE + half, nxt, nxt_id);
-    if (on && (unsigned)id[0] < (unsigned)a.E) atomicAdd(&sh.counts[id[0]], 1);
-    if (on && (unsigned)id[1] < (unsigned)a.E) atomicAdd(&sh.counts[id[1]], 1);
-    float x[N];
-    cur.values(x);
-    if (a.mask && !on) {
+  constexpr bool LONG = C > LONG_RUNS;
+  int64_t base = lo + warp * 2;
+  bool kept = false;
+  do {
+    for (const int64_t stop = LONG ? min(base + SUM_ROWS, hi) : hi; base < stop; base += ROWS_AT_ONCE) {
+      Part nxt;
+      int nxt_id[2];
+      const bool nxt_on = fetch(base + ROWS_AT_ONCE + half, nxt, nxt_id);
+      if (on && (unsigned)id[0] < (unsigned)a.E) atomicAdd(&sh.counts[id[0]], 1);
+      if (on && (unsigned)id[1] < (unsigned)a.E) atomicAdd(&sh.counts[id[1]], 1);
+      float x[N];
+      cur.values(x);
+      if (a.mask && !on) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+        for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+      }
+      float none[1], inv;
+      if (a.sigmoid)
+        inv = sigmoid_scores<N, false>(x, none);
+      else
+        inv = softmax_scores(x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+      mine += on;
+      cur = nxt;
+      on = nxt_on;
+      id[0] = nxt_id[0];
+      id[1] = nxt_id[1];
     }
-    float none[1], inv;
-    if (a.sigmoid)
-      inv = sigmoid_scores<N, false>(x, none);
-    else
-      inv = softmax_scores(x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
-    mine += on;
-    cur = nxt;
-    on = nxt_on;
-    id[0] = nxt_id[0];
-    id[1] = nxt_id[1];
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    acc[i] += __shfl_xor_sync(ALL, acc[i], 16);
-    const int e = Part::expert(i, sub);
-    if (half == 0 && e < a.E) sh.sums[warp][e] = acc[i];
-  }
+    for (int i = 0; i < N; ++i) {
+      acc[i] += __shfl_xor_sync(ALL, acc[i], 16);
+      const int e = Part::expert(i, sub);
+      if (half == 0 && e < a.E) sh.sums[warp][e] = kept ? sh.sums[warp][e] + acc[i] : acc[i];
+      acc[i] = 0.0f;
+    }
+    kept = true;
+  } while (LONG && base < hi);
   if (sub == 0 && mine) atomicAdd(&sh.tokens, mine);
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += THREADS) {
@@ -345,7 +360,7 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
   const int local = threadIdx.x % width, group = threadIdx.x / width, e = rank * width + local;
   if (threadIdx.x == 0) sh.tokens = 0;
   __syncthreads();
-  float sum = 0.0f;
+  float sum = 0.0f, rest = 0.0f;
   int count = 0, tokens = 0;
   if (group < groups && e < a.E) {
     constexpr int U = 8;  // runs whose loads are in flight together
@@ -360,7 +375,7 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        sum += __uint_as_float(s[u]);
+        add_kept(sum, rest, __uint_as_float(s[u]));
         count += (int)c[u];
       }
     }
@@ -368,17 +383,22 @@ __device__ __forceinline__ void join_parts(const BalanceArgs& a, int64_t s, int 
   for (int p = threadIdx.x; p < parts; p += THREADS) tokens += (int)part_at(p)[2 * a.E];
   tokens = __reduce_add_sync(ALL, tokens);
   if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(&sh.tokens, tokens);
-  sh.sums[threadIdx.x] = sum;
+  sh.sums[threadIdx.x] = sum + rest;
   sh.counts[threadIdx.x] = count;
   __syncthreads();
+  for (int h = 1 << (31 - __clz(max(groups - 1, 1))); h > 0; h >>= 1) {  // (from the largest power of two below)
+    if (group < h && group + h < groups) {
+      sh.sums[threadIdx.x] += sh.sums[threadIdx.x + h * width];
+      sh.counts[threadIdx.x] += sh.counts[threadIdx.x + h * width];
+    }
+    __syncthreads();
+  }
   const float n = (float)max(sh.tokens, 1);
   const float unit = a.coefficient * ((float)a.E / (float)a.K) / n;
   float term = 0.0f;
   if (group == 0 && e < a.E) {
-    for (int g = 1; g < groups; ++g) {
-      sum += sh.sums[g * width + local];
-      count += sh.counts[g * width + local];
-    }
+    sum = sh.sums[threadIdx.x];
+    count = sh.counts[threadIdx.x];
     a.counts[s * a.E + e] = count;
     const float slope = unit * (float)count / n;
     a.slope[s * a.E + e] = slope;
@@ -467,14 +487,14 @@ __global__ void __launch_bounds__(THREADS) balance_mean_kernel(BalanceArgs a) {
   __syncthreads();
   pdl_wait();
   int n = 0;
-  float loss = 0.0f;
+  float loss = 0.0f, rest = 0.0f;
   for (int64_t s = threadIdx.x; s < a.sequences; s += THREADS) {
     n += a.seq_tokens[s] > 0;
-    if (blockIdx.x == 0) loss += a.seq_loss[s];
+    if (blockIdx.x == 0) add_kept(loss, rest, a.seq_loss[s]);
   }
   n = __reduce_add_sync(ALL, n);
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&used, n);
-  losses[threadIdx.x] = loss;
+  losses[threadIdx.x] = isfinite(loss) ? loss + rest : loss;
   __syncthreads();
   const float share = 1.0f / (float)max(used, 1);
   const int64_t all = a.sequences * a.E;
@@ -617,20 +637,27 @@ Kernel kernel_for(const BalanceArgs& a, bool vec, Which w) {
 int64_t sum_ctas(int E) { return 152 * (E <= 128 ? 5 : E <= 256 ? 3 : 2); }
 int64_t grad_ctas(int E) { return 152 * (E <= 128 ? 3 : E <= 256 ? 2 : 1); }
 // Logits that one cluster takes, in one launch (512 KB of FP32: eight SMs read
-// that in the time that a second launch takes).
-constexpr int64_t SMALL_ELEMENTS = 1 << 17;
+// that in the time that a second launch takes), of rows that its lanes add at once.
+constexpr int64_t SMALL_ELEMENTS = 1 << 17, SMALL_ROWS = JOIN * SUM_ROWS;
 
 int64_t rows_of_a_block(int64_t rows, int64_t ctas) {
   const int64_t r = (rows + ctas - 1) / ctas;
   return std::max<int64_t>((r + ROWS_AT_ONCE - 1) / ROWS_AT_ONCE * ROWS_AT_ONCE, ROWS_AT_ONCE);
 }
 
+// Rows of a CTA that sums: one wave of CTAs, or more where its runs would be too long.
+int64_t rows_of_a_run(int E, int64_t rows) {
+  return std::min<int64_t>(rows_of_a_block(rows, sum_ctas(E)), (E > 64 * LONG_RUNS ? 32 : 1) * SUM_ROWS);
+}
+
 int64_t sum_blocks(int E, int64_t rows) {
-  const int64_t r = rows_of_a_block(rows, sum_ctas(E));
+  const int64_t r = rows_of_a_run(E, rows);
   return (rows + r - 1) / r;
 }
 
-bool small_call(int E, int64_t rows, int64_t sequences) { return sequences == 1 && rows * E <= SMALL_ELEMENTS; }
+bool small_call(int E, int64_t rows, int64_t sequences) {
+  return sequences == 1 && rows * E <= SMALL_ELEMENTS && rows <= SMALL_ROWS;
+}
 
 }  // namespace
 
@@ -642,7 +669,7 @@ size_t balance_workspace(int E, int64_t rows, int64_t sequences) {
 
 cudaError_t launch_balance(BalanceArgs a, bool vec, void* workspace, cudaStream_t s) {
   if (small_call(a.E, a.rows, a.sequences)) return launch(kernel_for(a, vec, SMALL), JOIN, THREADS, JOIN, false, s, a);
-  a.block_rows = rows_of_a_block(a.rows, sum_ctas(a.E));
+  a.block_rows = rows_of_a_run(a.E, a.rows);
   const int64_t blocks = sum_blocks(a.E, a.rows);
   a.parts = static_cast<uint32_t*>(workspace);
   a.seq_loss = reinterpret_cast<float*>(a.parts + (blocks + a.sequences) * part_words(a.E));

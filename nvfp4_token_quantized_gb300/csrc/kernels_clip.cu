@@ -172,7 +172,7 @@ struct Granules {
 // A thread's sum of squares: FP32 for chunks whose squares keep their bits
 // there, FP64 for the rest (some hundred times slower, so only where a sum of
 // 64 squares leaves [2^-90, 2^100]).  What an FP32 addition of a chunk rounds away is
-// kept (Knuth's two-sum) and added at the end: a large set gives a thread hundreds of
+// kept (add_kept) and added at the end: a large set gives a thread hundreds of
 // chunks, whose roundings, of gradients alike, would all go one way (862 chunks: 66
 // units of 2^-24 in the norm).
 struct Squares {
@@ -181,11 +181,9 @@ struct Squares {
   template <typename T>
   __device__ __forceinline__ void add(const Granules<T>& g) {
     const float s = g.squares();
-    if (s > 0x1p-90f && s < 0x1p100f) {
-      const float t = sum + s, from = t - sum;
-      rest += (sum - (t - from)) + (s - from);
-      sum = t;
-    } else if (!g.zero()) {
+    if (s > 0x1p-90f && s < 0x1p100f)
+      add_kept(sum, rest, s);
+    else if (!g.zero()) {
       uint4 q[GRANULES];
 #pragma unroll
       for (int j = 0; j < GRANULES; ++j) q[j] = g.q[j];
