@@ -715,6 +715,16 @@ typedef struct {
 MOE_API moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows,
                                         void* stream);
 
+/* The two calls above as tests of their bounded waits take them: in every cluster
+ * of the kernels that a forward of many rows and a gradient run, the first wait of
+ * CTA `silent` (counted from 1; of the factors' gradients of every CTA) is for a
+ * barrier at which nothing arrives, and waits run out after a millisecond.  0: as
+ * above. */
+MOE_API moe_status moe_debug_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows,
+                                             int silent, void* stream);
+MOE_API moe_status moe_debug_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io,
+                                              int64_t rows, int silent, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

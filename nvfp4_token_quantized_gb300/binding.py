@@ -48,7 +48,7 @@ EXPORTED = (
     "moe_set_routing", "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
     "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward", "moe_gradient_workspace_bytes",
     "moe_gradient_norm", "moe_clip_gradients", "moe_adapter_workspace_bytes", "moe_adapter_forward",
-    "moe_adapter_backward",
+    "moe_adapter_backward", "moe_debug_adapter_forward", "moe_debug_adapter_backward",
 )
 MOE_ROUTE_NOALLOC_MAX_LOGITS = 1 << 20
 MOE_NUM_STAGES = 7
@@ -190,6 +190,9 @@ def load_library() -> ctypes.CDLL:
         "moe_adapter_workspace_bytes": (S, [ctypes.POINTER(moe_adapter_config), L, I]),
         "moe_adapter_forward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_io), L, P]),
         "moe_adapter_backward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_grad_io), L, P]),
+        "moe_debug_adapter_forward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_io), L, I, P]),
+        "moe_debug_adapter_backward": (I, [ctypes.POINTER(moe_adapter_config), ctypes.POINTER(moe_adapter_grad_io), L,
+                                           I, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   __shared__ Piece found;
   __shared__ uint64_t arrived[ST], freed[ST];  // copies in, products done
+  __shared__ uint64_t last;                    // (as in adapter_tensor.cuh)
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   __shared__ int row_of[1024];
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
       mbar_init(&arrived[i], VEC ? ADAPTER_THREADS : 2 * ADAPTER_THREADS);
       mbar_init(&freed[i], 1);
     }
+    mbar_init(&last, 1);
     gave_up = 0;
     fence_mbarrier_init();
   }
@@ -177,13 +179,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   for (int r = tid; r < p.count; r += TENSOR_THREADS) row_of[r] = a.row_list[p.start + r];
   if (SCALED && tid < a.rank) back_of[tid] = a.back[side][(int64_t)blockIdx.x * a.rank + tid];
   __syncthreads();
-  const auto wait_alone = [&](uint64_t* bar, int parity) {  // (one lane)
-    if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
-  };
-  const auto wait = [&](uint64_t* bar, int parity) {  // (whole warps)
-    wait_alone(bar, parity);
-    __syncwarp();
-  };
+  const Waits wait(&gave_up, a.silent);
 
   const int stages = (p.count + GRADIENT_ROWS - 1) / GRADIENT_ROWS;
   const unsigned char* parts = a.parts[side] + first_stage(p, a.unit) * S::HIDDEN;
@@ -226,7 +222,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   if (warp == ADAPTER_WARPS) {
     if (lane == 0)
       for (int i = 0; i < stages; ++i) {
-        wait_alone(&arrived[i % ST], (i / ST) & 1);
+        if (!wait.alone(i == 0 && a.silent ? &last : &arrived[i % ST], (i / ST) & 1)) break;
         fence_async_shared();
         const uint32_t at = ring + (i % ST) * S::STAGE;
 #pragma unroll
@@ -247,7 +243,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   } else {
     if constexpr (!VEC) fetch(0);
     for (int i = 0; i < stages; ++i) {
-      if (i >= ST) wait(&freed[i % ST], ((i - ST) / ST) & 1);
+      if (i >= ST && !wait.warp(&freed[i % ST], ((i - ST) / ST) & 1)) break;
       issue(i);
       if constexpr (!VEC) {
         put(i);
@@ -258,24 +254,27 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
     }
   }
   copy_wait_all();
-  wait(&freed[(stages - 1) % ST], ((stages - 1) / ST) & 1);  // (the last commit covers all before)
+  // (the last commit covers all before)
+  const bool ok = wait.warp(&freed[(stages - 1) % ST], ((stages - 1) / ST) & 1);
   tc_fence_after();
 
   if (warp < ADAPTER_WARPS) {
     // A lane has a column of x, its ranks side by side in tensor memory.
     const int quarter = warp & 3, m = warp >> 2, c = n0 + m * 128 + quarter * 32 + lane;
-    const float lost = gave_up ? NAN : 0.0f;
+    const float lost = ok ? 0.0f : NAN;
     const int64_t n = (int64_t)a.rank * N;
     const bool alone = a.starts[p.group + 1] - a.starts[p.group] <= a.unit;  // (the adapter's only piece)
     float* sums = a.sums[side] + (first_sums(p.start - p.number * a.unit, a.unit) + p.number) * n + c;
     T* grad = static_cast<T*>(a.grad[side]) + adapter * n + c;
   #pragma unroll
     for (int r0 = 0; r0 < R; r0 += 8) {
-      float v[8], w[8];
+      float v[8] = {}, w[8] = {};
       const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + m * S::D + r0;
-      tmem_ld8(at, v);
-      if (R <= 32) tmem_ld8(at + R, w);  // (the parts have columns of their own)
-      tmem_ld_wait();
+      if (ok) {
+        tmem_ld8(at, v);
+        if (R <= 32) tmem_ld8(at + R, w);  // (the parts have columns of their own)
+        tmem_ld_wait();
+      }
   #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (r0 + i >= a.rank || c >= N) continue;
@@ -289,6 +288,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
   }
   tc_fence_before();
   __syncthreads();
+  if (gave_up) wait.settle(&last, 0, warp == ADAPTER_WARPS && lane == 0);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * S::D);

@@ -60,6 +60,34 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, u
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// A CTA's waits, bounded: after one that runs out, further ones end at once, and whoever
+// waited in vain does no more of what it waited for.
+struct Waits {
+  volatile int* gave_up;
+  uint64_t most;  // nanoseconds
+  __device__ __forceinline__ Waits(volatile int* flag, int silent) : gave_up(flag), most(silent ? 1000000 : 2000000000) {}
+  __device__ __forceinline__ bool alone(uint64_t* bar, int parity) const {  // (one lane)
+    if (mbar_try_wait(bar, (uint32_t)parity)) return true;
+    if (!*gave_up && mbar_wait_bounded(bar, (uint32_t)parity, gave_up, most)) return true;
+    *gave_up = 1;
+    return false;
+  }
+  __device__ __forceinline__ bool warp(uint64_t* bar, int parity) const {  // (the same for all lanes)
+    return __all_sync(0xffffffffu, alone(bar, parity));
+  }
+  // After a wait that ran out, by all threads: copies and products on their way end
+  // before what they use is given back or serves something else.  `issuer`: the
+  // thread that issues the products; `last`: a barrier of one arrival.
+  __device__ __forceinline__ void settle(uint64_t* last, int parity, bool issuer) const {
+    copy_wait_all();
+    if (issuer) {
+      tc_commit(last);
+      mbar_wait_bounded(last, (uint32_t)parity, nullptr, 1000000000ull);
+    }
+    __syncthreads();
+  }
+};
+
 // Threads of the tcgen05 kernels: eight warps that copy and one whose first lane
 // issues the products.
 constexpr int TENSOR_THREADS = ADAPTER_THREADS + 32;

@@ -36,8 +36,9 @@
 // kernel (registers, shared memory), and the layer's GEMMs leave no room beside
 // theirs: tensor memory is never waited for.
 //
-// Waits are bounded: one that runs out raises a flag, further waits return at once,
-// and the tile's rows become NaN.
+// Waits are bounded: after one that runs out the CTA issues and copies no more, what is
+// on its way ends before shared memory changes its use and before tensor memory is
+// given back, and the tile's rows become NaN.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   // Of the first product's slots: copies in, products done; of the second's: copies
   // in; of D2's SUMS places: products done, sums read.
   __shared__ uint64_t in1[ST], free1[ST], in2[ST], done[SUMS], drained[SUMS];
+  __shared__ uint64_t last;  // (nothing arrives but after a wait that ran out)
   __shared__ uint32_t tmem_at;
   __shared__ volatile int gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       mbar_init(&done[i], 1);
       mbar_init(&drained[i], ADAPTER_WARPS / 2);
     }
+    mbar_init(&last, 1);
     gave_up = 0;
     fence_mbarrier_init();
   }
@@ -140,13 +143,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     if (!issuer) rows_without_adapter<T, VEC>(a, row_of, count, crank, C);
     return;
   }
-  const auto wait_alone = [&](uint64_t* bar, int parity) {  // (one lane)
-    if (!mbar_wait_bounded(bar, (uint32_t)parity, &gave_up)) gave_up = 1;
-  };
-  const auto wait = [&](uint64_t* bar, int parity) {  // (whole warps)
-    wait_alone(bar, parity);
-    __syncwarp();
-  };
+  const Waits wait(&gave_up, a.silent);
 
   // ---- D1 = x down^T over this CTA's columns ----
   const int chunks = (K + 63) / 64, each = (chunks + C - 1) / C;
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   if (issuer) {
     if (lane == 0)
       for (int i = 0; i < nk; ++i) {
-        wait_alone(&in1[i % ST], (i / ST) & 1);
+        if (!wait.alone(i == 0 && crank + 1 == a.silent ? &last : &in1[i % ST], (i / ST) & 1)) break;
         fence_async_shared();
         const uint32_t at = ring_at + (i % ST) * S::STAGE;
 #pragma unroll
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     };
     if (!VEC && nk > 0) fetch(0);
     for (int i = 0; i < nk; ++i) {
-      if (i >= ST) wait(&free1[i % ST], ((i - ST) / ST) & 1);
+      if (i >= ST && !wait.warp(&free1[i % ST], ((i - ST) / ST) & 1)) break;
       if constexpr (VEC) {
         issue(i);
         copy_arrive(&in1[i % ST]);
@@ -223,9 +220,11 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
         mbar_arrive(&in1[i % ST]);
       }
     }
-    if (nk > 0) wait(&free1[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
+    if (nk > 0) wait.warp(&free1[(nk - 1) % ST], ((nk - 1) / ST) & 1);  // (the last commit covers all before)
   }
   __syncthreads();
+  const bool lost = gave_up;  // (the same in all threads: none waits before the next barrier)
+  if (lost) wait.settle(&last, 0, issuer && lane == 0);
   tc_fence_after();
 
   const int quarter = warp & 3, half = (warp >> 2) & 1, mine = quarter * 32 + lane;  // (the issuer takes no part)
@@ -328,8 +327,8 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
       tc_fence_after();
       fence_async_cluster();  // (the panels that all CTAs have written)
       for (int i = 0; i < nb; ++i) {
-        wait_alone(&in2[i % ST], (i / ST) & 1);
-        if (i >= SUMS) wait_alone(&drained[i % SUMS], (i / SUMS - 1) & 1);
+        if (!wait.alone(&in2[i % ST], (i / ST) & 1)) break;
+        if (i >= SUMS && !wait.alone(&drained[i % SUMS], (i / SUMS - 1) & 1)) break;
         tc_fence_after();
         fence_async_shared();
         const uint32_t b = ring_at + (i % ST) * S::STAGE + S::ROWS;
@@ -388,15 +387,19 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
     for (int j = half; j < nb; j += 2) {
       const int col = (b0 + j) * 64;
       unsigned char* tile = ring + (j % ST) * S::STAGE;
-      wait(&in2[j % ST], (j / ST) & 1);  // (the rows of base; products follow them)
-      wait(&done[j % SUMS], (j / SUMS) & 1);
+      // (the rows of base; products follow them)
+      if (lost || !wait.warp(&in2[j % ST], (j / ST) & 1) || !wait.warp(&done[j % SUMS], (j / SUMS) & 1)) {
+        for (; j < nb; j += 2)
+          for (int r = quarter * 32; r < min(quarter * 32 + 32, count); ++r)
+            for (int c = (b0 + j) * 64 + lane; c < min((b0 + j) * 64 + 64, N); c += 32) out[out_at[r] + c] = from_f32<T>(NAN);
+        break;
+      }
       if (quarter * 32 >= count) {  // (no rows here: only the copies of up)
         if (lane == 0) mbar_arrive(&drained[j % SUMS]);
         if (j + ST < nb) fill(j + ST);
         continue;
       }
       tc_fence_after();
-      const float by = gave_up ? NAN : bk;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[32];
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = unpack2(w[e], T());
-            o[e] = pack2(fmaf(v[c * 8 + 2 * e], by, f.x), fmaf(v[c * 8 + 2 * e + 1], by, f.y), T());
+            o[e] = pack2(fmaf(v[c * 8 + 2 * e], bk, f.x), fmaf(v[c * 8 + 2 * e + 1], bk, f.y), T());
           }
           *reinterpret_cast<uint4*>(tile + swizzled(mine, h * 4 + c)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -454,6 +457,7 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   }
   tc_fence_before();
   __syncthreads();
+  if (gave_up) wait.settle(&last, lost ? 1 : 0, issuer && lane == 0);
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, SUMS * 64);

@@ -141,6 +141,7 @@ struct AdapterArgs {
   float* hidden;  // [rows, rank] or NULL
   int64_t rows;
   int in, n_out, rank, L;
+  int silent;  // 0, or (tests) a CTA of each cluster, from 1: its first wait runs out
   // set by the launch
   const int32_t *starts, *row_list;
   const int32_t* group_of;  // groups' adapters; NULL: group a is adapter a
@@ -165,6 +166,7 @@ struct OuterArgs {
   float* back[2];           // and its scales, one for each rank of a piece (FP16)
   int64_t rows;
   int L, rank, unit, blocks[2];
+  int silent;  // (as above, of every CTA)
 };
 
 size_t adapter_workspace(const moe_adapter_config& c, int64_t rows, bool backward);

@@ -58,15 +58,8 @@ moe_status check_all(const Operand* in, int ni, const Operand* out, int no, int 
   return MOE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int64_t rows, int backward) {
-  return check_config(cfg, rows) == MOE_OK ? adapter_workspace(*cfg, rows, backward != 0) : 0;
-}
-
-moe_status moe_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows, void* stream) {
+// silent: AdapterArgs::silent
+moe_status forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows, int silent, void* stream) {
   moe_status st = check_config(cfg, rows);
   if (st != MOE_OK) return st;
   if (!io) return MOE_ERR_INVALID_ARG;
@@ -106,11 +99,12 @@ moe_status moe_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_
   a.n_out = cfg->out_features;
   a.rank = cfg->rank;
   a.L = cfg->num_adapters;
+  a.silent = silent;
   return launched(launch_adapter(a, *cfg, vec, io->workspace, static_cast<cudaStream_t>(stream)));
 }
 
-moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows,
-                                void* stream) {
+moe_status backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows, int silent,
+                    void* stream) {
   moe_status st = check_config(cfg, rows);
   if (st != MOE_OK) return st;
   if (!io) return MOE_ERR_INVALID_ARG;
@@ -152,6 +146,7 @@ moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter
   a.n_out = cfg->in_features;
   a.rank = cfg->rank;
   a.L = cfg->num_adapters;
+  a.silent = silent;
   OuterArgs o{};
   o.x[0] = io->x;
   o.x[1] = io->dout;
@@ -162,7 +157,35 @@ moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter
   o.grad[1] = io->dup;
   o.width[0] = cfg->in_features;
   o.width[1] = cfg->out_features;
+  o.silent = silent;
   return launched(launch_adapter_backward(a, o, *cfg, vec, io->workspace, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int64_t rows, int backward) {
+  return check_config(cfg, rows) == MOE_OK ? adapter_workspace(*cfg, rows, backward != 0) : 0;
+}
+
+moe_status moe_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows, void* stream) {
+  return forward(cfg, io, rows, 0, stream);
+}
+
+moe_status moe_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows,
+                                void* stream) {
+  return backward(cfg, io, rows, 0, stream);
+}
+
+moe_status moe_debug_adapter_forward(const moe_adapter_config* cfg, const moe_adapter_io* io, int64_t rows, int silent,
+                                     void* stream) {
+  return silent < 0 ? MOE_ERR_INVALID_ARG : forward(cfg, io, rows, silent, stream);
+}
+
+moe_status moe_debug_adapter_backward(const moe_adapter_config* cfg, const moe_adapter_grad_io* io, int64_t rows,
+                                      int silent, void* stream) {
+  return silent < 0 ? MOE_ERR_INVALID_ARG : backward(cfg, io, rows, silent, stream);
 }
 
 }  // extern "C"
