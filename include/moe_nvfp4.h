@@ -658,7 +658,9 @@ MOE_API moe_status moe_clip_gradients(const moe_gradient* tensors, int64_t num, 
  * Values that are no finite numbers stay in their row and adapter; an infinite
  * element of the second factor, or of x in the factors' gradients, may give NaN
  * where the formula gives an infinity (hidden's parts meet it one by one).
- * Kernel-side waits are bounded: rows whose wait ran out become NaN.
+ * Kernel-side waits are bounded: rows whose wait ran out before their hidden was
+ * formed become NaN, and so do that hidden and the gradients formed with it; later
+ * in a call, the columns that were waited for.
  * Limits: rank <= 128, features <= 2^20, num_adapters < 65536. */
 typedef struct {
   int in_features, out_features;

@@ -254,8 +254,10 @@ __global__ void __launch_bounds__(TENSOR_THREADS, 2) adapter_gradient_kernel(con
     }
   }
   copy_wait_all();
-  // (the last commit covers all before)
-  const bool ok = wait.warp(&freed[(stages - 1) % ST], ((stages - 1) / ST) & 1);
+  __syncthreads();
+  // (The last commit covers all before.  Whether it was made is known here only: its
+  // barrier's phase before would pass for it.)
+  const bool ok = __all_sync(0xffffffffu, !gave_up) && wait.warp(&freed[(stages - 1) % ST], ((stages - 1) / ST) & 1);
   tc_fence_after();
 
   if (warp < ADAPTER_WARPS) {

@@ -38,7 +38,8 @@
 //
 // Waits are bounded: after one that runs out the CTA issues and copies no more, what is
 // on its way ends before shared memory changes its use and before tensor memory is
-// given back, and the tile's rows become NaN.
+// given back, and the tile's rows become NaN: all of them in every CTA of the cluster
+// where the first product is incomplete, else the CTA's columns from there on.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -230,17 +231,19 @@ __global__ void __launch_bounds__(TENSOR_THREADS, R <= 64 ? 2 : 1) adapter_tenso
   const int quarter = warp & 3, half = (warp >> 2) & 1, mine = quarter * 32 + lane;  // (the issuer takes no part)
 
   // ---- the cluster's sums joined, hidden's parts into every CTA's panels ----
+  // (sums that this CTA could not form are no numbers: the join carries them into
+  // hidden, every CTA's columns and the factors' gradients)
   if (!issuer) {
     float* to = part + mine * RP + half * (R / 2);
 #pragma unroll
     for (int c = 0; c < R / 2; c += 8) {
       float v[8];
-      if (nk > 0) {
+      if (nk > 0 && !lost) {
         tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + half * (R / 2) + c, v);
         tmem_ld_wait();
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = lost ? NAN : 0.0f;
       }
       reinterpret_cast<float4*>(to + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(to + c)[1] = make_float4(v[4], v[5], v[6], v[7]);

@@ -98,3 +98,32 @@ def test_nothing_waits_where_none_is_asked_to():
     same._lib = _Silent(ad._lib, -1)
     with pytest.raises(RuntimeError):
         same.forward(**a)
+
+
+@pytest.mark.parametrize("T,K,N,r,L,dtype,pad", CASES)
+def test_rows_whose_wait_ran_out_are_no_numbers(T, K, N, r, L, dtype, pad):
+    """Whole rows, whichever CTA of the cluster gave up, with their hidden, and from
+    there the gradients; rows without an adapter are their base."""
+    ad, lost, a, dout, dbase = _make(T, K, N, r, L, dtype, pad)
+    _, hidden = ad.forward(**a, keep_hidden=True)
+    has = a["ids"] >= 0
+    back = dict(dout=dout, x=a["x"], hidden=hidden, ids=a["ids"], down=a["down"], up=a["up"], base=dbase)
+    lost._lib = _Silent(ad._lib, 1)
+    out, h = lost.forward(**a, keep_hidden=True)
+    assert torch.isnan(out[has]).all() and torch.isnan(h[has]).all()
+    assert torch.equal(out[~has], a["base"][~has]) and not h[~has].any()
+    dx, dd, du = lost.backward(**back)
+    assert torch.isnan(dx[has]).all() and torch.isnan(dd).all() and torch.isnan(du).all()
+    assert torch.equal(dx[~has], dbase[~has])
+    # what comes of such a hidden elsewhere
+    _, dd, du = ad.backward(**{**back, "hidden": h})
+    assert torch.isfinite(dd).all() and torch.isnan(du).all()
+
+
+def test_another_cta_of_the_cluster():
+    T, K, N, r, L = 600, 512, 512, 16, 3
+    ad, lost, a, _, _ = _make(T, K, N, r, L, BF16)
+    for silent in range(2, 9):
+        lost._lib = _Silent(ad._lib, silent)
+        out, h = lost.forward(**a, keep_hidden=True)
+        assert torch.isnan(out[a["ids"] >= 0]).all() and torch.isnan(h[a["ids"] >= 0]).all()
