@@ -79,6 +79,9 @@ struct Present {
 // 16384 rows, once): no CTA waits for another.  (16384 rows: 4 us; the kernel behind
 // is set up meanwhile.)  COMPACT: only groups with rows, a CTA every so many (4096
 // rows of 64 adapters in a set of 4000: the forward in 54 us, with a CTA a group 91).
+// The work is rows times groups with rows, which shows from some hundred of those on:
+// 16384 rows of 64 present adapters 13 us, of 4000 121; 65536 of 4000 382; 100000 of
+// 60000 6.5 ms.  (A sort by counting would be linear in the rows.)
 template <bool COMPACT>
 __global__ void __launch_bounds__(PLAN_THREADS, 2) adapter_plan_kernel(const int32_t* ids, int rows, int L, int groups,
                                                                     int32_t* starts, int32_t* row_list,

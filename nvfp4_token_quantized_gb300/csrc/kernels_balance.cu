@@ -17,9 +17,9 @@
 // 256 takes four 16-byte loads a lane and two trees of four steps for a
 // maximum and a sum, and the lanes' own sums over the rows stay in registers.
 //
-// Bound by the bytes of the logits.  131072 x 256 FP32: the sums 27 us (138 MB, 5.1
-// TB/s with a launch's ramp and drain), their join 7.5, the gradient 38.5 (268 MB,
-// 7 TB/s: part of what it writes stays in L2), 55 with rows to add to (403 MB, 7.3
+// Bound by the bytes of the logits.  131072 x 256 FP32: the sums 25 us (138 MB, 5.4
+// TB/s with a launch's ramp and drain), their join 8, the gradient 38.5 (268 MB,
+// 7 TB/s: part of what it writes stays in L2), 56 with rows to add to (403 MB, 7.3
 // TB/s).  A few thousand rows in many sequences are a chain of latencies: 32768 x
 // 160 bf16 in 41 sequences 33 us, loss and gradient.
 #include <cooperative_groups.h>

@@ -3,13 +3,14 @@
 // Two passes over the tensors, in chunks of 32 KB that a grid takes in turn: the
 // first, one wave, leaves a sum of squares for each CTA (763 MB: 110 us, the rate
 // of a copy), the second adds those up (in every CTA, in the same order) and
-// scales (763 MB read, 763 written: 238 us, 96 % of a copy's rate).  Both are
-// bound by bytes; the second goes through the chunks from the last to the first,
+// scales (763 MB read, 763 written: 218 us, a copy's rate and what L2 spares).  Both
+// are bound by bytes; the second goes through the chunks from the last to the first,
 // so that what the first left in L2 need not come from memory again.  Sets of a
 // few chunks are one launch of one cluster.
 //
-// (216 quiet tensors, 48 MB: 12 us for the norm and 8 for the pass that finds
-// nothing to do; 14 tensors, 135 KB, one cluster: 10.)
+// (One launch each, caches flushed: 216 quiet tensors, 48 MB, 12 us for the norm and 8
+// for the pass that finds nothing to do, the two 12.6 together where the set stays in
+// L2; 14 tensors, 135 KB, one cluster: 10.)
 //
 // The list of tensors travels as a kernel parameter: no copy to the device, no
 // buffer of addresses that a captured graph would have to keep.
@@ -396,7 +397,8 @@ cudaError_t run(const moe_gradient* t, int64_t n, const ClipArgs& a, cudaStream_
   for (int64_t i = 0; i < n; i += CAP) {
     if (n > CAP) fill(l, t + i, (int)std::min<int64_t>(n - i, CAP));
     // (in place one wave: most steps change nothing, and its CTAs only look: 48 MB
-    // in 216 tensors 24 us, with twelve waves 32)
+    // in 216 tensors, caches flushed, both passes and two events 24 us, with twelve
+    // waves 32)
     const uint32_t grid = std::min<uint32_t>(l.first[l.n], (l.in_place ? 1 : SCALE_WAVES) * CLIP_PARTS);
     const cudaError_t e =
         launch_k(gradient_scale_kernel<CAP>, dim3(std::max(grid, 1u)), dim3(THREADS), 0, s, n <= CAP, l);

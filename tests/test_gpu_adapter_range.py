@@ -97,6 +97,29 @@ def test_factor_gradients_beside_a_large_row(T):
     _near(du[0, :, 1:], want[:, 1:], tol[:, 1:], "dup")
 
 
+@pytest.mark.parametrize("r", [5, 20, 40, 100])
+def test_factor_gradients_in_large_sets(r):
+    """Only adapters with rows are listed; one of several pieces, one of a row."""
+    T, K, N, L = 1500, 40, 72, 300
+    g = torch.Generator().manual_seed(r)
+    sizes = {0: 1, 7: 700, 150: 97, 299: 300}
+    ids = torch.full((T,), -1, dtype=torch.int32)
+    ids[torch.randperm(T, generator=g)[:sum(sizes.values())]] = torch.cat(
+        [torch.full((n,), a, dtype=torch.int32) for a, n in sizes.items()])
+    power = 2.0 ** -(torch.arange(r) * 20 / r).floor()
+    x, dout = torch.randn(T, K, generator=g).to(F16), torch.randn(T, N, generator=g).to(F16)
+    hidden = torch.randn(T, r, generator=g) * power * 64
+    down, up = torch.randn(L, r, K, generator=g).to(F16), torch.randn(L, r, N, generator=g).to(F16)
+    _, _, du = _adapters(K, N, r).backward(*(t.cuda() for t in (dout, x, hidden, ids, down, up)))
+    for a in range(L):
+        rows = (ids == a).numpy()
+        if not rows.any():
+            assert not du[a].any()
+            continue
+        want, tol, _ = _outer(_np(hidden)[rows], _np(dout)[rows])
+        _near(du[a], want, tol, f"dup of adapter {a}")
+
+
 def test_an_infinite_hidden_leaves_the_other_ranks():
     """Of a rank that holds an infinity nothing finite is left; the others, above
     FP16's range, stay what they are."""
